@@ -366,6 +366,129 @@ const char* moe_version(void);
  * "cudaErrorInvalidValue"), or "cudaSuccess" when there was none. */
 const char* moe_last_cuda_error(void);
 
+/* ------------------------------------------------------------------------------------------
+ * The 16-bit block around the experts: router top-k, grouping of the slots by expert, matrix
+ * products grouped by expert with ragged sizes, norms before and after the block.
+ * Conventions as above (device pointers, caller-owned buffers, stream last, no allocation, no
+ * host synchronisation, graph-capturable), except that matrices have a row stride in elements
+ * (ld*, at least the row length; the elements of a row are contiguous).  M == 0 is a no-op.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype;
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
+typedef enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+
+/* Router: the top-k experts of every token and their weights.
+ *   s_e = sigmoid(l_e) or softmax(l)_e, in fp32;  key_e = s_e + bias_e (sigmoid; the bias takes
+ *   part in the choice only) or l_e (softmax, which keeps the logits' order).
+ *   n_group > 1: the E experts are n_group runs of E / n_group; a run's key is the sum of its two
+ *   largest keys (sigmoid) or its largest (softmax), and only the topk_group best runs stay.
+ *   The topk largest keys are chosen in descending order, equal keys in ascending index (runs
+ *   likewise); w_j = s_j * scale, with renormalize s_j / sum_j s_j * scale (0 when that sum is
+ *   0).
+ *   An expert whose logit (or whose key) is NaN or -inf is masked: it is never chosen and takes
+ *   no part in the softmax.  A token with fewer than topk experts left gets id -1 and weight 0
+ *   in its last places; moe_run and moe_group drop such slots.
+ *   logits [M, E] of `dtype`, row stride ld_logits; bias [E] fp32 or NULL (sigmoid only);
+ *   topk_ids [M, topk] int32, topk_weights [M, topk] fp32, both contiguous.
+ * Limits: E <= 1024, topk <= 32 and <= topk_group * (E / n_group), n_group <= 32 dividing E.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE (limits), MOE_ERR_UNSUPPORTED (bias with softmax),
+ * MOE_ERR_CUDA. */
+moe_status moe_router(const void* logits, int dtype, long long ld_logits, const float* bias, int M,
+                      int E, int topk, int score, int n_group, int topk_group, int renormalize,
+                      float scale, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* Ragged groups of the slots by expert (the routing that moe_run does inside, for callers of
+ * moe_grouped_run): slots f = t * topk + j of topk_ids [M, topk] in stable order by expert.
+ *   offsets [E + 1]  positions [offsets[e], offsets[e + 1]) are expert first_expert + e's slots;
+ *   perm [M * topk]  flat slot of each position, -1 at and beyond offsets[E];
+ *   slot_of [M * topk]  position of each flat slot, -1 for ids outside
+ *                       [first_expert, first_expert + E), which are dropped.
+ * Limits: E <= 1024, M * topk <= 2^30.  Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_CUDA. */
+moe_status moe_group(const int32_t* topk_ids, int M, int topk, int E, int first_expert,
+                     int32_t* offsets, int32_t* perm, int32_t* slot_of, void* stream);
+
+/* Matrix products grouped by expert with ragged sizes, 16-bit operands, fp32 sums:
+ *   out[p] = act(W[e] . x[row(p)])   for offsets[e] <= p < offsets[e + 1],
+ *   row(p) = perm[p] / topk (perm given: x has one row per token) or p (perm NULL),
+ *   and rows of out at and beyond offsets[E], up to S, are set to zero.
+ * act = MOE_ACT_SWIGLU: W[e] holds the halves of `layout` (moe_w13_layout), N / 2 rows each, and
+ * out[p] the N / 2 values g' * sigmoid(alpha g') * (u' + beta), g' = min(g, limit),
+ * u' = clamp(u, -limit, limit), from the fp32 products, rounded once.
+ * The plan fixes what a layer fixes: E experts of N x K, the operand type (MOE_DTYPE_BF16 or
+ * MOE_DTYPE_F16, of x, W and out), the activation, and max_rows, the most positions of a call.
+ * Limits: E <= 1024; 1 <= N <= 2^22 (even for SwiGLU), 1 <= K <= 2^24, N * K < 2^40, E * N <
+ * 2^31, max_rows <= 2^30.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (type, activation). */
+typedef struct moe_grouped_s moe_grouped_t;
+moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout, float limit,
+                            float alpha, float beta, int max_rows, moe_grouped_t** out);
+/* Bytes of the scratch buffer of moe_grouped_run (256-byte aligned, caller-owned). */
+moe_status moe_grouped_scratch_bytes(const moe_grouped_t* plan, size_t* bytes);
+/* One product.
+ *   scratch  zero-filled by the caller once, before its first use; every call leaves it ready for
+ *            the next.  Calls that share a scratch buffer must be stream-ordered.  After a device
+ *            error (below) it has to be zero-filled again.
+ *   x        [x_rows, K], row stride ldx;  w [E, N, K] with row stride ldw and expert stride
+ *            ldw * N;  out [S, N or N / 2], row stride ldo;  offsets [E + 1] and perm [S] as
+ *            moe_group writes them (perm entries outside [0, x_rows * topk) and offsets outside
+ *            [0, S] or descending set the device error word; such rows are undefined).
+ * Rows whose x, w and strides are 16-byte aligned run on the tensor cores; other operands (for
+ * instance K % 8 != 0) on the CUDA cores, slower.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (S > max_rows), MOE_ERR_CUDA. */
+moe_status moe_grouped_run(const moe_grouped_t* plan, void* scratch, size_t scratch_bytes,
+                           const void* x, long long ldx, int x_rows, const void* w, long long ldw,
+                           const int32_t* offsets, const int32_t* perm, int topk, void* out,
+                           long long ldo, int S, void* stream);
+/* Reads and clears the device error word in `scratch` (synchronises `stream`): *code as
+ * moe_get_device_error. */
+moe_status moe_grouped_get_device_error(const moe_grouped_t* plan, void* scratch, void* stream,
+                                        int* code);
+void moe_destroy_grouped(moe_grouped_t* plan);
+
+/* Norms before and after a block, with the block's gate and residual scale, in one pass:
+ *   y  = rows[t]                                   (slot_of NULL: the block's own output), or
+ *        sum_j topk_weights[t, j] * rows[slot_of[t, j]]  over slots in [0, n_rows), j ascending
+ *        (the experts' outputs, combined here)     [+ shared[t]]
+ *   n  = norm(y) * post_weight [+ post_bias]       (post_weight NULL: n = y)
+ *   r  = residual + scale * gate * n               (gate NULL: 1; rows NULL: r = residual)
+ *   out = norm(r) * pre_weight [+ pre_bias]        (pre_weight NULL: no out)
+ *   norm(v) = v / sqrt(mean(v^2) + eps), or, MOE_NORM_LAYER, (v - mean) / sqrt(var + eps).
+ * All in fp32: r is rounded when it is stored in residual_out, and the second norm takes the
+ * unrounded r.  weight_offset is added to both weights (1 for weights stored around zero).
+ *   dtype  (bf16 / f16) of rows, shared and out; residual_dtype (dtype or fp32) of residual and
+ *   residual_out; weight_dtype (dtype or fp32) of the weights, biases and gate.
+ *   gate element (t, h) at gate[t * gate_row + h * gate_col]: strides 0 broadcast (a scalar per
+ *   token, a vector per channel), gate_col 0 or 1.
+ *   residual_out may be residual, and NULL when rows is NULL or it is not wanted; out must not
+ *   overlap an input.
+ * Limits: 1 <= H <= 32768.  Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (types),
+ * MOE_ERR_CUDA. */
+typedef struct {
+  int M, H, dtype, residual_dtype, weight_dtype, kind;
+  float eps, scale, weight_offset;
+  const void* residual;
+  long long ld_residual;
+  const void* rows;
+  long long ld_rows;
+  const int32_t* slot_of;       /* [M, topk] or NULL */
+  const float* topk_weights;    /* [M, topk], with slot_of */
+  int topk, n_rows;             /* with slot_of: top-k, and the rows of `rows` */
+  const void* shared;           /* [M, H] or NULL, with slot_of */
+  long long ld_shared;
+  const void* post_weight;
+  const void* post_bias;
+  const void* gate;
+  long long gate_row, gate_col;
+  const void* pre_weight;
+  const void* pre_bias;
+  void* residual_out;
+  long long ld_residual_out;
+  void* out;
+  long long ld_out;
+} moe_norm_args;
+moe_status moe_block_norm(const moe_norm_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

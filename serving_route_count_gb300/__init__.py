@@ -1,7 +1,8 @@
 """GB300 (sm_103a) routed mixture-of-experts expert computation.
 
 The compute path lives in ``libmoe_gb300.so`` (hand-written CUDA, C ABI in
-``include/moe_gb300.h``); ``moe`` is its Python binding (argument marshalling only).
+``include/moe_gb300.h``); ``moe`` is its Python binding (argument marshalling only), ``block``
+that of the 16-bit block around the experts (router, grouping, grouped products, norms).
 """
 from .moe import (  # noqa: F401
     MoEError, MoELayer, moe_plan_weights, moe_prepared_bytes, moe_prepare_weights, moe_unprepare_weights, moe_plan,
@@ -12,4 +13,10 @@ from .moe import (  # noqa: F401
     moe_version,
     MOE_W4A8_MXFP4, MOE_W4A16_NVFP4, MOE_W4A16_HYBRID, MOE_W4A16_HYBRID_MX, MOE_W4A8_NVFP4, MOE_W4A4_NVFP4, MOE_W13_UP_GATE, MOE_W13_GATE_UP,
     MOE_TIER_NVFP4, MOE_TIER_NF3,
+)
+from .block import (  # noqa: F401
+    MoEGrouped, moe_router, moe_group, moe_grouped_plan, moe_grouped_scratch_bytes,
+    moe_grouped_get_device_error, moe_destroy_grouped, moe_block_norm,
+    MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID,
+    MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_NORM_RMS, MOE_NORM_LAYER,
 )

@@ -16,6 +16,7 @@ c_int32_p = ctypes.POINTER(ctypes.c_int32)
 c_uint8_p = ctypes.POINTER(ctypes.c_uint8)
 c_size_t_p = ctypes.POINTER(ctypes.c_size_t)
 c_int_p = ctypes.POINTER(ctypes.c_int)
+c_longlong = ctypes.c_longlong
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "moe_gb300.h")
@@ -26,6 +27,19 @@ class MoeCheckpoint(ctypes.Structure):
                 ("w2", c_void_p), ("s2", c_void_p), ("g2", c_void_p),
                 ("nf_w13", c_void_p), ("nf_s13", c_void_p), ("nf_w2", c_void_p),
                 ("nf_s2", c_void_p), ("a1_gscale", c_void_p), ("a2_gscale", c_void_p)]
+
+
+class MoeNormArgs(ctypes.Structure):
+    _fields_ = [("M", c_int), ("H", c_int), ("dtype", c_int), ("residual_dtype", c_int),
+                ("weight_dtype", c_int), ("kind", c_int), ("eps", c_float), ("scale", c_float),
+                ("weight_offset", c_float), ("residual", c_void_p), ("ld_residual", c_longlong),
+                ("rows", c_void_p), ("ld_rows", c_longlong), ("slot_of", c_void_p),
+                ("topk_weights", c_void_p), ("topk", c_int), ("n_rows", c_int),
+                ("shared", c_void_p), ("ld_shared", c_longlong), ("post_weight", c_void_p),
+                ("post_bias", c_void_p), ("gate", c_void_p), ("gate_row", c_longlong),
+                ("gate_col", c_longlong), ("pre_weight", c_void_p), ("pre_bias", c_void_p),
+                ("residual_out", c_void_p), ("ld_residual_out", c_longlong), ("out", c_void_p),
+                ("ld_out", c_longlong)]
 
 
 # name -> (restype, argtypes)
@@ -70,6 +84,19 @@ SIGNATURES = {
     "moe_status_str": (ctypes.c_char_p, [c_int]),
     "moe_version": (ctypes.c_char_p, []),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
+    "moe_router": (c_int, [c_void_p, c_int, c_longlong, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                           c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
+    "moe_group": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                          c_void_p]),
+    "moe_grouped_plan": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_float, c_float,
+                                 c_int, ctypes.POINTER(c_void_p)]),
+    "moe_grouped_scratch_bytes": (c_int, [c_void_p, c_size_t_p]),
+    "moe_grouped_run": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_int, c_void_p,
+                                c_longlong, c_void_p, c_void_p, c_int, c_void_p, c_longlong, c_int,
+                                c_void_p]),
+    "moe_grouped_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
+    "moe_destroy_grouped": (None, [c_void_p]),
+    "moe_block_norm": (c_int, [ctypes.POINTER(MoeNormArgs), c_void_p]),
 }
 
 _LIB = None

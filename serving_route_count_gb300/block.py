@@ -1,0 +1,258 @@
+"""Python binding of the 16-bit block's entry points (include/moe_gb300.h): router, grouping of
+the slots by expert, products grouped by expert, norms around the block.
+
+Argument checks and marshalling only, like ``moe``; the computation runs in the library's CUDA
+kernels.  Matrices may have a row stride (their rows must be contiguous); everything else is
+contiguous.  Work goes to ``stream``, or to torch's current stream; tensors that are not created on
+that stream are the caller's to order and keep alive, as for any stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from .moe import MOE_W13_UP_GATE, _check, _stream
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_ACT_NONE = 0
+MOE_ACT_SWIGLU = 1
+MOE_NORM_RMS = 0
+MOE_NORM_LAYER = 1
+
+_CODE = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
+
+
+def _dev(t, name, dtype=None):
+    """Address of a CUDA tensor (of `dtype`)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _whole(t, name, dtype, numel):
+    """Address of a contiguous CUDA tensor of `numel` elements."""
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {numel} elements")
+    return _dev(t, name, dtype)
+
+
+def _rows(t, name, rows, cols, dtype=None):
+    """(address, row stride) of a CUDA matrix [rows, cols] whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {cols}], not {list(t.shape)}")
+    step, unit = t.stride()
+    if (unit != 1 and cols > 1) or (step < cols and t.shape[0] > 1):
+        raise ValueError(f"the rows of {name} must be contiguous and apart")
+    return _dev(t, name, dtype), (step if t.shape[0] > 1 else max(step, cols))
+
+
+def _code(t, name):
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: {t.dtype} is not supported")
+    return code
+
+
+# ---------------------------------------------------------------------------------- router
+
+def moe_router(logits, topk, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1,
+               renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
+    """Top-k experts and weights of every row of logits [M, E] (bf16, f16 or fp32): (ids int32
+    [M, topk], weights fp32 [M, topk]); see moe_router in include/moe_gb300.h."""
+    M, E = logits.shape
+    p, ld = _rows(logits, "logits", M, E)
+    topk = int(topk)
+    if topk < 0:
+        raise ValueError("topk must not be negative")
+    if ids is None:
+        ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
+    _check(_lib.load().moe_router(
+        p, _code(logits, "logits"), ld, None if bias is None else _whole(bias, "bias", torch.float32, E),
+        M, E, topk, score, n_group, topk_group, bool(renormalize), scale,
+        _whole(ids, "ids", torch.int32, M * topk), _whole(weights, "weights", torch.float32, M * topk),
+        _stream(stream)), "moe_router")
+    return ids, weights
+
+
+# ---------------------------------------------------------------------------------- grouping
+
+def moe_group(topk_ids, E, first_expert=0, offsets=None, perm=None, slot_of=None, stream=None):
+    """Slots of topk_ids [M, topk] (int32) grouped by expert: (offsets [E + 1], perm [M * topk],
+    slot_of [M, topk]), all int32; see moe_group in include/moe_gb300.h."""
+    M, topk = topk_ids.shape
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=topk_ids.device)
+    if perm is None:
+        perm = torch.empty(M * topk, dtype=torch.int32, device=topk_ids.device)
+    if slot_of is None:
+        slot_of = torch.empty((M, topk), dtype=torch.int32, device=topk_ids.device)
+    n = M * topk
+    _check(_lib.load().moe_group(
+        _whole(topk_ids, "topk_ids", torch.int32, n), M, topk, E, first_expert,
+        _whole(offsets, "offsets", torch.int32, E + 1), _whole(perm, "perm", torch.int32, n),
+        _whole(slot_of, "slot_of", torch.int32, n), _stream(stream)), "moe_group")
+    return offsets, perm, slot_of
+
+
+# ---------------------------------------------------------------------------------- grouped products
+
+def moe_grouped_plan(E, N, K, dtype, act, layout, limit, alpha, beta, max_rows) -> int:
+    out = ctypes.c_void_p()
+    _check(_lib.load().moe_grouped_plan(E, N, K, dtype, act, layout, limit, alpha, beta, max_rows,
+                                        ctypes.byref(out)), "moe_grouped_plan")
+    return out.value
+
+
+def moe_grouped_scratch_bytes(plan) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.load().moe_grouped_scratch_bytes(plan, ctypes.byref(n)), "moe_grouped_scratch_bytes")
+    return n.value
+
+
+def moe_grouped_get_device_error(plan, scratch, stream=None):
+    """(status, code) of the device error word in `scratch`, which is cleared."""
+    code = ctypes.c_int()
+    st = _lib.load().moe_grouped_get_device_error(plan, _dev(scratch, "scratch"), _stream(stream),
+                                                  ctypes.byref(code))
+    return st, code.value
+
+
+def moe_destroy_grouped(plan):
+    _lib.load().moe_destroy_grouped(plan)
+
+
+class MoEGrouped:
+    """Products grouped by expert with ragged sizes, 16-bit operands: the plan of one layer's
+    matrices [E, N, K] and its scratch buffer (moe_grouped_plan, moe_grouped_run).  Calls that
+    share a MoEGrouped must be stream-ordered."""
+
+    def __init__(self, E, N, K, max_rows, dtype=torch.bfloat16, act=MOE_ACT_NONE,
+                 layout=MOE_W13_UP_GATE, swiglu_limit=float("inf"), alpha=1.0, beta=0.0,
+                 device="cuda"):
+        self.E, self.N, self.K, self.dtype = E, N, K, dtype
+        if dtype not in _CODE:
+            raise ValueError(f"{dtype} is not supported")
+        self.cols = N // 2 if act == MOE_ACT_SWIGLU else N
+        self.plan = moe_grouped_plan(E, N, K, _CODE[dtype], act, layout, swiglu_limit, alpha, beta,
+                                     max_rows)
+        self.scratch = torch.zeros(moe_grouped_scratch_bytes(self.plan), dtype=torch.uint8,
+                                   device=device)
+        self._fixed = (self.plan, self.scratch.data_ptr(), self.scratch.numel())
+
+    def __call__(self, x, w, offsets, perm=None, topk=1, out=None, stream=None):
+        """out[p] = act(w[e] . x[row(p)]) for the positions p of every expert e.  offsets [E + 1]
+        and perm [S] as moe_group gives them; with perm, x holds one row per token (row(p) =
+        perm[p] // topk), without it one row per position."""
+        xp, ldx = _rows(x, "x", None, self.K, self.dtype)
+        S = x.shape[0] if perm is None else perm.numel()
+        if w.dim() != 3 or w.shape[0] != self.E or w.shape[1] != self.N or w.shape[2] != self.K:
+            raise ValueError(f"w must be [{self.E}, {self.N}, {self.K}], not {list(w.shape)}")
+        per, ldw, unit = w.stride()
+        if (unit != 1 and self.K > 1) or ldw < self.K or (per != self.N * ldw and self.E > 1):
+            raise ValueError("the rows of w must be contiguous and evenly apart over all experts")
+        if out is None:
+            out = torch.empty((S, self.cols), dtype=self.dtype, device=x.device)
+        op, ldo = _rows(out, "out", S, self.cols, self.dtype)
+        _check(_lib.load().moe_grouped_run(
+            *self._fixed, xp, ldx, x.shape[0], _dev(w, "w", self.dtype), ldw,
+            _whole(offsets, "offsets", torch.int32, self.E + 1),
+            None if perm is None else _whole(perm, "perm", torch.int32, S), topk, op, ldo, S,
+            _stream(stream)), "moe_grouped_run")
+        return out
+
+    def device_error(self, stream=None):
+        return moe_grouped_get_device_error(self.plan, self.scratch, stream)
+
+    def close(self):
+        if getattr(self, "plan", None):
+            moe_destroy_grouped(self.plan)
+            self.plan = None
+            self._fixed = (None, 0, 0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------------------------- norms
+
+def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=None,
+                   post_weight=None, post_bias=None, gate=None, scale=1.0, pre_weight=None,
+                   pre_bias=None, eps=1e-6, kind=MOE_NORM_RMS, weight_offset=0.0, residual_out=None,
+                   out=None, stream=None):
+    """Norm after a block (post_weight), gate, residual scale and the norm before the next block
+    (pre_weight) in one pass; with slot_of and topk_weights the rows are the experts' and their
+    top-k combination is taken here too.  Returns (residual_out, out): residual_out None without
+    rows, out None without pre_weight.  gate broadcasts over [M, H]; weights, biases and gate are
+    of the rows' type or all fp32.  See moe_block_norm in include/moe_gb300.h."""
+    M, H = residual.shape
+    a = _lib.MoeNormArgs()
+    a.M, a.H, a.kind, a.eps, a.scale, a.weight_offset = M, H, kind, eps, scale, weight_offset
+    if rows is not None:
+        dtype = rows.dtype
+    elif out is not None:
+        dtype = out.dtype
+    elif residual.dtype != torch.float32:
+        dtype = residual.dtype
+    else:
+        dtype = pre_weight.dtype if pre_weight is not None else torch.bfloat16
+    if dtype not in _CODE:
+        raise ValueError(f"rows: {dtype} is not supported")
+    a.dtype, a.residual_dtype = _CODE[dtype], _code(residual, "residual")
+    a.residual, a.ld_residual = _rows(residual, "residual", M, H)
+    small = [t for t in (post_weight, post_bias, gate, pre_weight, pre_bias) if t is not None]
+    wt = small[0].dtype if small else dtype
+    a.weight_dtype = _CODE.get(wt, -1)
+    if slot_of is not None:
+        if rows is None or topk_weights is None or slot_of.dim() != 2 or slot_of.shape[0] != M:
+            raise ValueError("slot_of must be [M, topk], with rows and topk_weights")
+        a.topk, a.n_rows = slot_of.shape[1], rows.shape[0]
+        a.slot_of = _whole(slot_of, "slot_of", torch.int32, M * a.topk)
+        a.topk_weights = _whole(topk_weights, "topk_weights", torch.float32, M * a.topk)
+        a.rows, a.ld_rows = _rows(rows, "rows", None, H, dtype)
+        if shared is not None:
+            a.shared, a.ld_shared = _rows(shared, "shared", M, H, dtype)
+    elif topk_weights is not None or shared is not None:
+        raise ValueError("topk_weights and shared go with slot_of")
+    elif rows is not None:
+        a.rows, a.ld_rows = _rows(rows, "rows", M, H, dtype)
+    if post_weight is not None:
+        a.post_weight = _whole(post_weight, "post_weight", wt, H)
+    if post_bias is not None:
+        a.post_bias = _whole(post_bias, "post_bias", wt, H)
+    if gate is not None:
+        if gate.dim() > 2:
+            raise ValueError("gate must broadcast over [M, H]")
+        g = gate.expand(M, H)
+        a.gate = _dev(gate, "gate", wt)
+        a.gate_row = g.stride(0) if M > 1 else 0
+        a.gate_col = g.stride(1) if H > 1 else 0
+    if pre_weight is not None:
+        a.pre_weight = _whole(pre_weight, "pre_weight", wt, H)
+        if pre_bias is not None:
+            a.pre_bias = _whole(pre_bias, "pre_bias", wt, H)
+        if out is None:
+            out = torch.empty((M, H), dtype=dtype, device=residual.device)
+        a.out, a.ld_out = _rows(out, "out", M, H, dtype)
+    elif pre_bias is not None or out is not None:
+        raise ValueError("pre_bias and out go with pre_weight")
+    if rows is not None:
+        if residual_out is None:
+            residual_out = torch.empty((M, H), dtype=residual.dtype, device=residual.device)
+        a.residual_out, a.ld_residual_out = _rows(residual_out, "residual_out", M, H, residual.dtype)
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with rows")
+    _check(_lib.load().moe_block_norm(ctypes.byref(a), _stream(stream)), "moe_block_norm")
+    return residual_out, out

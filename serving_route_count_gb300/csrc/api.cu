@@ -127,6 +127,15 @@ moe_status cuda_status(cudaError_t e) {
   return MOE_ERR_CUDA;
 }
 
+}  // namespace
+
+namespace moe {
+// the same for the entry points of the other translation units
+int report_cuda(cudaError_t e) { return cuda_status(e); }
+}  // namespace moe
+
+namespace {
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int kFc1CtasPerSm = 2;

@@ -1,0 +1,30 @@
+// block_ops.cuh - what the kernels of the 16-bit block share: element types, vector accesses,
+// block reductions.
+#pragma once
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Clamped SwiGLU in fp32: g' * sigmoid(alpha g') * (u' + beta), g' = min(g, limit),
+// u' = clamp(u, -limit, limit).
+__device__ __forceinline__ float swiglu_f32(float u, float g, float limit, float alpha,
+                                            float beta) {
+  g = g > limit ? limit : g;              // comparisons, not fminf: NaN stays NaN
+  u = u > limit ? limit : (u < -limit ? -limit : u);
+  return g / (1.0f + expf(-alpha * g)) * (u + beta);
+}
+
+}  // namespace moe

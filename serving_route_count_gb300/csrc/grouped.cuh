@@ -1,0 +1,32 @@
+// grouped.cuh - parameters of the products grouped by expert (moe_grouped_run) that the kernels
+// and the C ABI share.
+#pragma once
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+struct GroupedDims {
+  int E, N, K, dtype, act, layout, max_rows;
+  float limit, alpha, beta;
+};
+
+struct GroupedCall {
+  const void* x;
+  long long ldx;
+  int x_rows;
+  const void* w;
+  long long ldw;
+  const int32_t* offsets;
+  const int32_t* perm;      // or NULL
+  int topk;
+  void* out;
+  long long ldo;
+  int S;
+  int32_t* err;             // device error word of the scratch buffer
+};
+
+// Values of one output row: N, or the N / 2 of a SwiGLU.
+inline int grouped_cols(const GroupedDims& d) { return d.act ? d.N / 2 : d.N; }
+
+}  // namespace moe
