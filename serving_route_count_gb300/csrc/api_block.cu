@@ -19,13 +19,19 @@ cudaError_t launch_group(const int32_t* ids, int S, int E, int first, int32_t* o
 cudaError_t launch_block_norm(const moe_norm_args& a, bool vec, cudaStream_t st);
 // gemm_grouped_simt.cu
 cudaError_t launch_grouped_simt(const GroupedDims& d, const GroupedCall& c, cudaStream_t st);
+// gemm_grouped_tc.cu
+size_t grouped_tc_part_bytes(int S, int E);
+size_t grouped_tc_ticket_bytes();
+bool grouped_tc_addressable(const GroupedDims& d, const GroupedCall& c);
+cudaError_t launch_grouped_tc(const GroupedDims& d, const GroupedCall& c, float* part,
+                              int32_t* tickets, cudaStream_t st);
 }  // namespace moe
 
 using namespace moe;
 
 struct moe_grouped_s {
   GroupedDims d;
-  size_t bytes;
+  size_t tickets, part, bytes;            // sections of the scratch buffer after the error word
 };
 
 namespace {
@@ -85,7 +91,9 @@ moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout,
   moe_grouped_s* g = new (std::nothrow) moe_grouped_s();
   if (g == nullptr) return MOE_ERR_ARG;
   g->d = GroupedDims{E, N, K, dtype, act, layout, max_rows, limit, alpha, beta};
-  g->bytes = kErrBytes;
+  g->tickets = kErrBytes;
+  g->part = align_up(g->tickets + grouped_tc_ticket_bytes(), 256);
+  g->bytes = g->part + grouped_tc_part_bytes(max_rows, E);
   *out = g;
   return MOE_OK;
 }
@@ -114,7 +122,11 @@ moe_status moe_grouped_run(const moe_grouped_t* plan, void* scratch, size_t scra
   if (perm != nullptr ? (topk < 1 || x_rows < 1) : x_rows < S) return MOE_ERR_ARG;
   GroupedCall c{x, ldx, x_rows, w, ldw, offsets, perm, topk, out, ldo, S,
                 static_cast<int32_t*>(scratch)};
-  return status(launch_grouped_simt(d, c, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!grouped_tc_addressable(d, c)) return status(launch_grouped_simt(d, c, st));
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  return status(launch_grouped_tc(d, c, reinterpret_cast<float*>(base + plan->part),
+                                  reinterpret_cast<int32_t*>(base + plan->tickets), st));
 }
 
 moe_status moe_grouped_get_device_error(const moe_grouped_t* plan, void* scratch, void* stream,
