@@ -488,6 +488,10 @@ typedef struct {
   long long ld_out;
 } moe_norm_args;
 moe_status moe_block_norm(const moe_norm_args* args, void* stream);
+/* Reads and clears the device error word of moe_block_norm's calls on the current device
+ * (synchronises `stream`): *code = 0 unless a bounded wait of one of them gave up, in which case
+ * the status is MOE_ERR_TIMEOUT and that call's outputs are undefined. */
+moe_status moe_block_norm_get_device_error(void* stream, int* code);
 
 #ifdef __cplusplus
 }

@@ -96,6 +96,7 @@ SIGNATURES = {
                                 c_void_p]),
     "moe_grouped_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
     "moe_destroy_grouped": (None, [c_void_p]),
+    "moe_block_norm_get_device_error": (c_int, [c_void_p, c_int_p]),
     "moe_block_norm": (c_int, [ctypes.POINTER(MoeNormArgs), c_void_p]),
 }
 

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .moe import MOE_W13_UP_GATE, _check, _stream
+from .moe import MOE_W13_UP_GATE, _check
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
@@ -26,6 +26,14 @@ MOE_NORM_RMS = 0
 MOE_NORM_LAYER = 1
 
 _CODE = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
+
+
+def _stream(stream, t):
+    """Stream handle; without a stream, torch's current one on t's device (its raw handle: a Stream
+    object costs as much as a launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _dev(t, name, dtype=None):
@@ -80,7 +88,7 @@ def moe_router(logits, topk, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk
         p, _code(logits, "logits"), ld, None if bias is None else _whole(bias, "bias", torch.float32, E),
         M, E, topk, score, n_group, topk_group, bool(renormalize), scale,
         _whole(ids, "ids", torch.int32, M * topk), _whole(weights, "weights", torch.float32, M * topk),
-        _stream(stream)), "moe_router")
+        _stream(stream, logits)), "moe_router")
     return ids, weights
 
 
@@ -100,7 +108,7 @@ def moe_group(topk_ids, E, first_expert=0, offsets=None, perm=None, slot_of=None
     _check(_lib.load().moe_group(
         _whole(topk_ids, "topk_ids", torch.int32, n), M, topk, E, first_expert,
         _whole(offsets, "offsets", torch.int32, E + 1), _whole(perm, "perm", torch.int32, n),
-        _whole(slot_of, "slot_of", torch.int32, n), _stream(stream)), "moe_group")
+        _whole(slot_of, "slot_of", torch.int32, n), _stream(stream, topk_ids)), "moe_group")
     return offsets, perm, slot_of
 
 
@@ -122,7 +130,8 @@ def moe_grouped_scratch_bytes(plan) -> int:
 def moe_grouped_get_device_error(plan, scratch, stream=None):
     """(status, code) of the device error word in `scratch`, which is cleared."""
     code = ctypes.c_int()
-    st = _lib.load().moe_grouped_get_device_error(plan, _dev(scratch, "scratch"), _stream(stream),
+    st = _lib.load().moe_grouped_get_device_error(plan, _dev(scratch, "scratch"),
+                                                  _stream(stream, scratch),
                                                   ctypes.byref(code))
     return st, code.value
 
@@ -167,7 +176,7 @@ class MoEGrouped:
             *self._fixed, xp, ldx, x.shape[0], _dev(w, "w", self.dtype), ldw,
             _whole(offsets, "offsets", torch.int32, self.E + 1),
             None if perm is None else _whole(perm, "perm", torch.int32, S), topk, op, ldo, S,
-            _stream(stream)), "moe_grouped_run")
+            _stream(stream, x)), "moe_grouped_run")
         return out
 
     def device_error(self, stream=None):
@@ -254,5 +263,13 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
         a.residual_out, a.ld_residual_out = _rows(residual_out, "residual_out", M, H, residual.dtype)
     elif residual_out is not None:
         raise ValueError("residual_out goes with rows")
-    _check(_lib.load().moe_block_norm(ctypes.byref(a), _stream(stream)), "moe_block_norm")
+    _check(_lib.load().moe_block_norm(ctypes.byref(a), _stream(stream, residual)), "moe_block_norm")
     return residual_out, out
+
+
+def moe_block_norm_get_device_error(stream=None):
+    """(status, code) of the device error word of moe_block_norm's calls, which is cleared."""
+    code = ctypes.c_int()
+    handle = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream, None)
+    st = _lib.load().moe_block_norm_get_device_error(handle, ctypes.byref(code))
+    return st, code.value

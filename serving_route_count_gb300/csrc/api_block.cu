@@ -17,6 +17,7 @@ cudaError_t launch_group(const int32_t* ids, int S, int E, int first, int32_t* o
                          int32_t* perm, int32_t* slot_of, cudaStream_t st);
 // block_norm.cu
 cudaError_t launch_block_norm(const moe_norm_args& a, bool vec, cudaStream_t st);
+cudaError_t norm_device_error(int* code, cudaStream_t st);
 // gemm_grouped_simt.cu
 cudaError_t launch_grouped_simt(const GroupedDims& d, const GroupedCall& c, cudaStream_t st);
 // gemm_grouped_tc.cu
@@ -37,8 +38,6 @@ struct moe_grouped_s {
 namespace {
 
 moe_status status(cudaError_t e) { return static_cast<moe_status>(report_cuda(e)); }
-
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 bool dtype16(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
 
@@ -167,15 +166,27 @@ moe_status moe_block_norm(const moe_norm_args* a, void* stream) {
   if (a->ld_residual < H || (a->rows && a->ld_rows < H) || (a->shared && a->ld_shared < H) ||
       (a->residual_out && a->ld_residual_out < H) || (a->out && a->ld_out < H))
     return MOE_ERR_ARG;
-  // 16-byte rows: bases on 16 bytes, row strides whole vectors of 8 (a gate vector per row too)
-  const auto rows16 = [](const void* p, long long ld) { return !p || (on16(p) && ld % 8 == 0); };
-  const bool vec = H % 8 == 0 && rows16(a->residual, a->ld_residual) &&
-                   rows16(a->rows, a->ld_rows) && rows16(a->shared, a->ld_shared) &&
-                   rows16(a->residual_out, a->ld_residual_out) && rows16(a->out, a->ld_out) &&
-                   rows16(a->post_weight, 0) && rows16(a->post_bias, 0) &&
-                   rows16(a->pre_weight, 0) && rows16(a->pre_bias, 0) &&
-                   (a->gate == nullptr || a->gate_col == 0 || rows16(a->gate, a->gate_row));
+  // whole vectors of eight elements: 16-byte bases (32 where the elements are fp32), row strides
+  // of whole vectors (a gate vector per row too)
+  const auto rows8 = [](const void* p, long long ld, int dtype) {
+    const uintptr_t mask = dtype == MOE_DTYPE_F32 ? 31 : 15;
+    return !p || ((reinterpret_cast<uintptr_t>(p) & mask) == 0 && ld % 8 == 0);
+  };
+  const int rt = a->residual_dtype, wt = a->weight_dtype, t = a->dtype;
+  const bool vec = H % 8 == 0 && rows8(a->residual, a->ld_residual, rt) &&
+                   rows8(a->rows, a->ld_rows, t) && rows8(a->shared, a->ld_shared, t) &&
+                   rows8(a->residual_out, a->ld_residual_out, rt) && rows8(a->out, a->ld_out, t) &&
+                   rows8(a->post_weight, 0, wt) && rows8(a->post_bias, 0, wt) &&
+                   rows8(a->pre_weight, 0, wt) && rows8(a->pre_bias, 0, wt) &&
+                   (a->gate == nullptr || a->gate_col == 0 || rows8(a->gate, a->gate_row, wt));
   return status(launch_block_norm(*a, vec, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_block_norm_get_device_error(void* stream, int* code) {
+  if (code == nullptr) return MOE_ERR_ARG;
+  const cudaError_t e = norm_device_error(code, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return status(e);
+  return *code ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 
 }  // extern "C"

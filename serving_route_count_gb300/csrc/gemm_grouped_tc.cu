@@ -28,9 +28,10 @@
 namespace moe {
 using namespace tc;
 
-constexpr int kGtThreads = 256;
+constexpr int kGtThreads = 384;
 constexpr int kGtK = 64;                 // K step: one 128-byte swizzled row per operand row
 constexpr int kGtMaxPairs = 80;          // pairs that the scratch buffer has partial slots for
+constexpr int kGtTokenWarps = 6;         // warps 2-7
 constexpr int kGtMinSteps = 4;           // K steps below which a piece is not cut further
 
 template <int BN>
@@ -205,7 +206,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   uint64_t* tempty = tfull + 2;        // [2] accumulators read (leader's are used)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
   int* s_flag = reinterpret_cast<int*>(s_tmem + 1);
-  int* s_warp = s_flag + 1;            // [8]
+  int* s_warp = s_flag + 1;            // [warps]
   int* s_off = reinterpret_cast<int*>(st + S * Cfg::kStage + 512);
   int* s_cnt = s_off + 1028;
   int* s_tile = s_cnt + 1028;
@@ -345,18 +346,19 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         ++seg;
       }
     }
-  } else if (warp == 2) {
+  } else if (warp < 2 + kGtTokenWarps) {
+    const int tl = lane * kGtTokenWarps + (warp - 2);
     int it = 0;
     while (ok && work.next(u, k0, len)) {
       const GtUnit un = gt_unit<BN>(u, p.RB, E, s_tile, s_off, s_cnt);
       const int first = un.p0 + (int)rank * un.nhalf;
       int4 rows = make_int4(0, 0, 0, 0);
       if (p.c.perm != nullptr) {
-        // rows 4 lane .. 4 lane + 3 of this CTA's tokens; past the tile its last row again
+        // rows 4 tl .. 4 tl + 3 of this CTA's tokens; past the tile its last row again
         int r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int f = p.c.perm[min(first + 4 * lane + i, un.p0 + un.n - 1)];
+          const int f = p.c.perm[min(first + 4 * tl + i, un.p0 + un.n - 1)];
           r[i] = f < 0 ? -1 : f / p.c.topk;
           if (r[i] < 0 || r[i] >= p.c.x_rows) {
             set_error(err, kErrRouteBounds);
@@ -374,13 +376,13 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         uint8_t* bs = st + s * Cfg::kStage + Cfg::kBytesA;
         const uint32_t bar = map_rank(&full[s], 0);
         if (p.c.perm != nullptr) {
-          if (4 * lane < un.nhalf) tma2_gather4(bs + lane * 512, &p.tm_x, k * kGtK, rows, bar);
-        } else if (lane * Cfg::kChunk < un.nhalf) {
-          tma2_load_2d(bs + lane * Cfg::kChunk * 128, &p.tm_x, k * kGtK, first + lane * Cfg::kChunk, bar);
+          if (tl < un.nhalf / 4) tma2_gather4(bs + tl * 512, &p.tm_x, k * kGtK, rows, bar);
+        } else if (tl * Cfg::kChunk < un.nhalf) {
+          tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, k * kGtK, first + tl * Cfg::kChunk, bar);
         }
       }
     }
-  } else if (warp >= 4) {
+  } else {
     const int q = warp & 3;
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
     int seg = 0;
@@ -422,7 +424,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         asm volatile("bar.sync 1, 128;" ::: "memory");
         int c_lo, c_hi;
         work.owners(u, c_lo, c_hi);
-        if (tid == 128) {
+        if (tid == kGtThreads - 128) {
           int32_t* ticket = p.tickets + 2 * (u - work.first) + rank;
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                        // ready for the next call

@@ -427,6 +427,7 @@ def check_norm(moe, M, H, dtype="bf16", res="same", wide=False, k=0, kind="rms",
         kw["residual_out"] = residual
     got_r, got_z = moe.moe_block_norm(residual, rows, scale=scale, kind=moe.MOE_NORM_LAYER if kind == "layer" else moe.MOE_NORM_RMS,
                                       weight_offset=offset, **kw)
+    assert moe.moe_block_norm_get_device_error() == (0, 0)
     within(got_r, r, dtype if res == "same" else res, er)
     if pre:
         within(got_z, z, dtype, ez)
@@ -459,6 +460,15 @@ def test_norm_strides_zero_rows_and_in_place(moe):
     check_norm(moe, 5, 264, k=2, zero_rows=True)
     check_norm(moe, 5, 264, k=2, inplace=True)
     check_norm(moe, 5, 264, res="f32", inplace=True)
+
+
+@gpu
+@pytest.mark.parametrize("H,res", [(4608, "same"), (7168, "f32"), (7680, "same"), (7688, "same"), (12288, "f32"), (15360, "same")])
+def test_norm_many_tokens(moe, H, res):
+    """More tokens than CTAs, long rows: the ring of rows wraps within and across tokens."""
+    for M, k in ((700, 0), (333, 3), (310, 17)):
+        if M * max(k, 1) * H < 1 << 25:
+            check_norm(moe, M, H, res=res, k=k, kind="layer" if k else "rms", shared=k > 3, gate="full" if k else "token", post=k != 3)
 
 
 @gpu
@@ -549,6 +559,7 @@ def test_refusals_of_the_norm(lib):
         return lib.moe_block_norm(ctypes.byref(a), None)
 
     assert lib.moe_block_norm(None, None) == 1
+    assert lib.moe_block_norm_get_device_error(None, None) == 1
     assert norm(M=0) == 0
     assert norm(H=0) == 2 and norm(H=32769) == 2
     assert norm(dtype=2) == 3 and norm(residual_dtype=1) == 3 and norm(weight_dtype=1) == 3
