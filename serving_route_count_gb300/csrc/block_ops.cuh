@@ -19,12 +19,14 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 }
 
 // Clamped SwiGLU in fp32: g' * sigmoid(alpha g') * (u' + beta), g' = min(g, limit),
-// u' = clamp(u, -limit, limit).
+// u' = clamp(u, -limit, limit).  __expf and __fdividef (2 + 1.2 |alpha g'| and 2 ulp) are far below
+// the rounding of the 16-bit result; with expf and an IEEE division the product's epilogue took 9 %
+// of a tensor-bound call.
 __device__ __forceinline__ float swiglu_f32(float u, float g, float limit, float alpha,
                                             float beta) {
   g = g > limit ? limit : g;              // comparisons, not fminf: NaN stays NaN
   u = u > limit ? limit : (u < -limit ? -limit : u);
-  return g / (1.0f + expf(-alpha * g)) * (u + beta);
+  return __fdividef(g, 1.0f + __expf(-alpha * g)) * (u + beta);
 }
 
 }  // namespace moe

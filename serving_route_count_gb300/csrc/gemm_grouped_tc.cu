@@ -7,7 +7,9 @@
 // up and 128 gate rows, interleaved 16 by 16, so that a warp's 32 accumulator lanes hold both
 // halves of 16 outputs) x up to BN of the expert's tokens.  Each CTA loads its 128 weight rows and
 // half of the tokens per K step of 64; the accumulators are double-buffered in tensor memory, so
-// a unit's epilogue runs under the next unit's loads and MMAs.
+// a unit's epilogue runs under the next unit's loads and MMAs.  At BN = 256, where the tensor cores
+// are the bound, a unit has 512 weight rows in two accumulators instead: the tokens are loaded
+// once for both, a quarter less L2 traffic and half the row gathers per MMA.
 //
 // The grid is persistent, one pair per two SMs.  The number of units is known on the device only
 // (offsets); every CTA builds the table of the experts' tiles in shared memory.  Whole waves of
@@ -15,8 +17,9 @@
 // to the scratch buffer, and the piece that arrives last adds them in K order (bit-stable, nobody
 // waits).
 //
-// Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warp 2 token copies (tiles, or
-// gathers of four rows by index), warp 3 tensor memory, warps 4-7 epilogue.
+// Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-7 token copies (tiles, or
+// gathers of four rows by index, whose issue takes ~70 cycles each: six warps share it; warp 3
+// also allocates the tensor memory), warps 8-15 epilogue.
 #include <type_traits>
 
 #include "block_ops.cuh"
@@ -28,71 +31,100 @@
 namespace moe {
 using namespace tc;
 
-constexpr int kGtThreads = 384;
+constexpr int kGtThreads = 512;
+constexpr int kGtTokenWarps = 6;         // warps 2-7
 constexpr int kGtK = 64;                 // K step: one 128-byte swizzled row per operand row
 constexpr int kGtMaxPairs = 80;          // pairs that the scratch buffer has partial slots for
-constexpr int kGtTokenWarps = 6;         // warps 2-7
 constexpr int kGtMinSteps = 4;           // K steps below which a piece is not cut further
 
 template <int BN>
 struct GtCfg {
+  static constexpr int kAcc = BN > 128 ? 2 : 1;              // accumulators of a unit
   static constexpr int kHalf = BN / 2;                       // tokens a CTA loads
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;     // tokens per tile copy
-  static constexpr int kBytesA = 128 * 128, kBytesB = kHalf * 128, kStage = kBytesA + kBytesB;
+  static constexpr int kBytesW = 128 * 128;                  // weight rows of one accumulator
+  static constexpr int kBytesA = kAcc * kBytesW, kBytesB = kHalf * 128, kStage = kBytesA + kBytesB;
   static constexpr int kTables = 3 * 1028 * 4 + 512;         // expert tables, barriers
   static constexpr int kStages = (227 * 1024 - 1024 - kTables) / kStage > 12
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
   static constexpr int kSmem = 1024 + kStages * kStage + kTables;
-  static constexpr int kCols = 2 * BN;                       // tensor-memory columns
+  static constexpr int kCols = 2 * BN;                       // tensor-memory columns: two buffers
+  // K steps that joining the pieces of a unit costs (its sums through the scratch buffer)
+  static constexpr int kFixSteps = BN <= 32 ? 8 : (BN <= 64 ? 12 : (BN <= 128 ? 24 : 40));
 };
 
 struct GtParams {
   CUtensorMap tm_w, tm_x;
   GroupedDims d;
   GroupedCall c;
-  float* part;          // [pairs][2][2 CTAs][BN][128]
-  int32_t* tickets;     // [pairs][2]
-  int KT, RB, cols, packed;
+  float* part;          // [pairs][2][2 CTAs][accumulators][BN][128]
+  int32_t* tickets;     // [pairs][2 CTAs][2 accumulators]
+  int KT, RB, half, cols, packed;   // RB: row blocks with all accumulators; half: one more with one
+  int whole16;          // SwiGLU weights by whole 16-row groups: one 5-d copy per K step
 };
 
-// Units of one pair: first its range of the leftover units' K steps, then its whole units.
+// Units of one pair: first its range of the leftover units' K steps, then its whole units, round
+// robin.  A unit is a token tile and a weight row block of it.  Numbers: the blocks of a tile
+// adjacent (they share its tokens), and where the last block has only one of two accumulators
+// (half the work) those of all tiles at the end, so that the last wave consists of them.
 struct GtWork {
-  int KT, G, Gs, c, D, first;      // first: units before it are whole
-  uint32_t W, x, x1;
-  int dp;
-  __device__ __forceinline__ void init(int units, int kt, int g, int cta) {
-    KT = kt; G = g; c = cta;
+  int KT, RB, halves, G, Gs, D, first, c;   // RB: blocks with all accumulators; first: units before
+  uint32_t W, x, x1;                        // it are whole
+  int full, u;                              // units of whole blocks; next whole unit
+  __device__ __forceinline__ void init(int tiles, int kt, int rbs, int half, int g, int cta,
+                                       int fix_steps) {
+    KT = kt; RB = rbs; halves = half; G = g;
+    full = tiles * rbs;
+    const int units = full + (half ? tiles : 0);
     D = units / g;
     first = D * g;
     const uint32_t R = (uint32_t)(units - first);
     W = R * (uint32_t)kt;
+    // cut the leftover units when that shortens the longest pair's work by more than the join
+    // costs (both in K steps)
+    if (kt - (int)(W / (uint32_t)g) <= fix_steps) {
+      first = units;
+      D += cta < (int)R;
+      W = 0;
+    }
     // pairs that share the leftover steps: all of them, unless the pieces got too short
     const uint32_t most = W / kGtMinSteps > R ? W / kGtMinSteps : R;
     Gs = most < (uint32_t)g ? (int)most : g;
-    x = cta < Gs ? begin_of(cta) : 0u;
-    x1 = cta < Gs ? begin_of(cta + 1) : 0u;
-    dp = 0;
+    c = cta;
+    x = W && cta < Gs ? begin_of(cta) : 0u;
+    x1 = W && cta < Gs ? begin_of(cta + 1) : 0u;
+    u = cta;
   }
   __device__ __forceinline__ uint32_t begin_of(int cta) const {
     return (uint32_t)cta * W / (uint32_t)Gs;
   }
-  __device__ __forceinline__ bool next(int& u, int& k0, int& len) {
+  __device__ __forceinline__ void place(int unit, int& t, int& r) const {
+    if (unit < full) {
+      t = unit / RB;
+      r = unit - t * RB;
+    } else {
+      t = unit - full;
+      r = RB;
+    }
+  }
+  __device__ __forceinline__ bool next(int& unit, int& t, int& r, int& k0, int& len) {
     if (x < x1) {
       const uint32_t kt = (uint32_t)KT;
-      u = first + (int)(x / kt);
+      unit = first + (int)(x / kt);
       k0 = (int)(x % kt);
       len = (int)min(kt - (uint32_t)k0, x1 - x);
       x += (uint32_t)len;
-      return true;
-    }
-    if (dp < D) {
-      u = c + dp * G;
+    } else if (D > 0) {
+      --D;
+      unit = u;
       k0 = 0;
       len = KT;
-      ++dp;
-      return true;
+      u += G;
+    } else {
+      return false;
     }
-    return false;
+    place(unit, t, r);
+    return true;
   }
   // The pairs that hold unit u's steps are a run of them; [c0, c1] bounds it.
   __device__ __forceinline__ void owners(int u, int& c0, int& c1) const {
@@ -108,36 +140,32 @@ struct GtWork {
   }
 };
 
-// A unit's expert, token range and weight row block.
-struct GtUnit {
-  int e, p0, n, nhalf, rb;
+// A tile's expert and token range (by a whole warp).  s_tile[e]: tiles before expert e, 1024
+// entries; the expert is the last one with s_tile[e] <= tile, found by two 32-way comparisons.
+struct GtTile {
+  int e, p0, n, nhalf;
 };
 template <int BN>
-__device__ __forceinline__ GtUnit gt_unit(int u, int RB, int E, const int* s_tile,
-                                          const int* s_off, const int* s_cnt) {
+__device__ __forceinline__ GtTile gt_tile(int tile, const int* s_tile, const int* s_off,
+                                          const int* s_cnt, int lane) {
   constexpr int kChunk = GtCfg<BN>::kChunk;
-  const int tile = u / RB;
-  int lo = 0, hi = E;                 // last e with s_tile[e] <= tile
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_tile[mid] <= tile) lo = mid; else hi = mid;
-  }
-  GtUnit r;
-  r.e = lo;
-  const int t = tile - s_tile[lo];
-  r.p0 = s_off[lo] + t * BN;
-  r.n = min(BN, s_cnt[lo] - t * BN);
+  const int hi = __popc(__ballot_sync(0xffffffffu, s_tile[32 * lane] <= tile)) - 1;
+  const int lo = __popc(__ballot_sync(0xffffffffu, s_tile[32 * hi + lane] <= tile)) - 1;
+  GtTile r;
+  r.e = 32 * hi + lo;
+  const int t = tile - s_tile[r.e];
+  r.p0 = s_off[r.e] + t * BN;
+  r.n = min(BN, s_cnt[r.e] - t * BN);
   r.nhalf = cdiv(r.n, 2 * kChunk) * kChunk;
-  r.rb = u - tile * RB;
   return r;
 }
 
 // Stores 32 accumulator columns (tokens c0 .. c0 + 31 of the unit, n of them valid) of this
-// lane's row.  A lane and its neighbour exchange every other token, so that each store writes
+// lane's row; col0: output column of the CTA's first row.  A lane and its neighbour exchange every other token, so that each store writes
 // two adjacent output columns.
 template <typename T, bool ACT>
-__device__ __forceinline__ void gt_store(const GtParams& p, float (&v)[32], const GtUnit& un,
-                                         int c0, int rank, int q, int lane) {
+__device__ __forceinline__ void gt_store(const GtParams& p, float (&v)[32], const GtTile& un,
+                                         int col0, int c0, int q, int lane) {
   T* out = static_cast<T*>(p.c.out);
   const int odd = lane & 1;
   if constexpr (ACT) {
@@ -152,7 +180,7 @@ __device__ __forceinline__ void gt_store(const GtParams& p, float (&v)[32], cons
       const float a = hi ? got : v[c], b = hi ? v[c + 16] : got;
       h[c] = swiglu_f32(up_first ? a : b, up_first ? b : a, p.d.limit, p.d.alpha, p.d.beta);
     }
-    const int col = un.rb * 128 + rank * 64 + q * 16 + (lane & 15);
+    const int col = col0 + q * 16 + (lane & 15);
     const int t0 = c0 + (hi ? 16 : 0);
     if (p.packed) {
       T* o = out + (size_t)(un.p0 + t0 + odd) * p.c.ldo + (col & ~1);
@@ -172,7 +200,7 @@ __device__ __forceinline__ void gt_store(const GtParams& p, float (&v)[32], cons
           out[(size_t)(un.p0 + t0 + c) * p.c.ldo + col] = from_f32<T>(h[c]);
     }
   } else {
-    const int col = un.rb * 256 + rank * 128 + q * 32 + lane;
+    const int col = col0 + q * 32 + lane;
     if (p.packed) {
       T* o = out + (size_t)(un.p0 + c0 + odd) * p.c.ldo + (col & ~1);
 #pragma unroll
@@ -205,8 +233,8 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   uint64_t* tfull = empty + S;         // [2] accumulators ready
   uint64_t* tempty = tfull + 2;        // [2] accumulators read (leader's are used)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
-  int* s_flag = reinterpret_cast<int*>(s_tmem + 1);
-  int* s_warp = s_flag + 1;            // [warps]
+  int* s_flag = reinterpret_cast<int*>(s_tmem + 1);   // [2]
+  int* s_warp = s_flag + 2;            // [warps]
   int* s_off = reinterpret_cast<int*>(st + S * Cfg::kStage + 512);
   int* s_cnt = s_off + 1028;
   int* s_tile = s_cnt + 1028;
@@ -227,7 +255,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);
+      mbar_init(&tempty[b], 8);        // four epilogue warps of each CTA
     }
     fence_barrier_init();
   }
@@ -254,6 +282,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
       s_off[e] = a;
       s_cnt[e] = cnt[i];
     }
+    if (e >= E && e < 1024) s_tile[e] = 0x7FFFFFFF;
     tiles += cdiv(cnt[i], BN);
   }
   int incl = tiles;
@@ -283,74 +312,115 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   }
   __syncthreads();
 
+  // Every loop below is taken by whole warps; one lane issues.
+  constexpr int kRows = ACT ? 64 : 128;      // output columns of one CTA and accumulator
   GtWork work;
-  work.init(total * p.RB, p.KT, G, pair);
-  int u, k0, len;
+  work.init(total, p.KT, p.RB, p.half, G, pair, Cfg::kFixSteps);
+  int u, tile, rb, k0, len;
+  int s = 0, issued = 0;             // ring stage, stages filled
+  uint32_t phase = 0;
   bool ok = true;
+  const auto advance = [&]() {
+    if (++s == S) {
+      s = 0;
+      phase ^= 1;
+    }
+  };
+  // first output column of a unit, and how many of its accumulators lie within the matrix
+  const auto unit_col = [&](int rb) { return rb * (2 * kRows * Cfg::kAcc); };
+  const auto accs_of = [&](int rb) { return Cfg::kAcc == 2 && rb < p.RB ? 2 : 1; };
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      while (ok && work.next(u, k0, len)) {
-        const GtUnit un = gt_unit<BN>(u, p.RB, E, s_tile, s_off, s_cnt);
-        const uint32_t bytes = 2u * (Cfg::kBytesA + un.nhalf * 128);
-        const int r0 = ACT ? un.rb * 128 + (int)rank * 64 : un.rb * 256 + (int)rank * 128;
-        for (int k = k0; k < k0 + len; ++k, ++it) {
-          const int s = it % S;
-          if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, err)) {
-            ok = false;
-            break;
-          }
-          uint8_t* a = st + s * Cfg::kStage;
-          const uint32_t bar = map_rank(&full[s], 0);
+    const uint32_t bar0 = map_rank(&full[0], 0);
+    while (ok && work.next(u, tile, rb, k0, len)) {
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      const int accs = accs_of(rb);
+      const uint32_t bytes = 2u * (accs * Cfg::kBytesW + un.nhalf * 128);
+      const int r0 = unit_col(rb) + (int)rank * kRows;
+      for (int x = k0 * kGtK; x < (k0 + len) * kGtK; x += kGtK, ++issued) {
+        if (!mbar_wait_warp(&empty[s], phase ^ 1, err)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t bar = bar0 + 8 * s;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-          if constexpr (ACT) {
+          for (int c = 0; c < accs; ++c) {
+            uint8_t* a = st + s * Cfg::kStage + c * Cfg::kBytesW;
+            const int r = r0 + c * 2 * kRows;
+            if constexpr (!ACT) {
+              tma2_load_3d(a, &p.tm_w, x, r, un.e, bar);
+            } else if (p.whole16) {
+              tma2_load_5d(a, &p.tm_w, x, 0, 0, r >> 4, un.e, bar);
+            } else {
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              tma2_load_4d(a + b * 4096, &p.tm_w, k * kGtK, r0 + 16 * b, 0, un.e, bar);
-          } else {
-            tma2_load_3d(a, &p.tm_w, k * kGtK, r0, un.e, bar);
+              for (int b = 0; b < 4; ++b)
+                tma2_load_4d(a + b * 4096, &p.tm_w, x, r + 16 * b, 0, un.e, bar);
+            }
           }
         }
+        advance();
       }
+    }
+    if (lane == 0) {
       if (ok) {
         // the last fills have been multiplied: nothing arrives at this CTA's barriers any more
-        for (int j = it > S ? it - S : 0; j < it; ++j) mbar_wait(&empty[j % S], (j / S) & 1, err);
+        for (int j = max(0, issued - S); j < issued; ++j)
+          mbar_wait(&empty[j % S], (j / S) & 1, err);
       } else if (rank == 0) {
-        drain_stage_loads<S>(full, it, err);
+        drain_stage_loads<S>(full, issued, err);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      int it = 0, seg = 0;
-      while (ok && work.next(u, k0, len)) {
-        const GtUnit un = gt_unit<BN>(u, p.RB, E, s_tile, s_off, s_cnt);
-        const int b = seg & 1;
-        if (!mbar_wait(&tempty[b], ((seg >> 1) & 1) ^ 1, err)) break;
+    // operand descriptors: only the address changes from stage to stage and from K block to K block
+    const uint64_t desc0 = desc_sw128(st);
+    const uint32_t hi = (uint32_t)(desc0 >> 32), lo0 = (uint32_t)desc0;
+    uint32_t uses[2] = {0, 0};       // units that each accumulator buffer has held
+    int seg = 0;
+    while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      const int accs = accs_of(rb);
+      const int b0 = Cfg::kAcc == 2 ? 0 : seg & 1;
+      for (int c = 0; ok && c < accs; ++c)
+        ok = mbar_wait_warp(&tempty[b0 + c], (uses[b0 + c] & 1) ^ 1, err);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t idesc = idesc_pair16(std::is_same<T, __nv_bfloat16>::value, 2 * un.nhalf);
+      uint32_t accumulate = 0;
+      for (int i = 0; i < len; ++i) {
+        if (!mbar_wait_warp(&full[s], phase, err)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t idesc = idesc_pair16(std::is_same<T, __nv_bfloat16>::value, 2 * un.nhalf);
-        for (int i = 0; i < len; ++i, ++it) {
-          const int s = it % S;
-          if (!mbar_wait(&full[s], (it / S) & 1, err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint8_t* a = st + s * Cfg::kStage;
+        if (lane == 0) {
+          const uint32_t lo = lo0 + s * (Cfg::kStage >> 4);
 #pragma unroll
-          for (int kb = 0; kb < 4; ++kb)
-            mma2_f16(tmem + b * BN, desc_sw128(a + 32 * kb), desc_sw128(a + Cfg::kBytesA + 32 * kb),
-                     idesc, (i > 0 || kb > 0) ? 1u : 0u);
+          for (int c = 0; c < Cfg::kAcc; ++c) {
+            if (c < accs) {
+#pragma unroll
+              for (int kb = 0; kb < 4; ++kb) {
+                const uint64_t da = ((uint64_t)hi << 32) | (lo + c * (Cfg::kBytesW >> 4) + 2 * kb);
+                const uint64_t db = ((uint64_t)hi << 32) | (lo + (Cfg::kBytesA >> 4) + 2 * kb);
+                mma2_f16(tmem + (b0 + c) * BN, da, db, idesc, kb == 0 ? accumulate : 1u);
+              }
+            }
+          }
           tc2_commit(&empty[s]);
         }
-        tc2_commit(&tfull[b]);
-        ++seg;
+        accumulate = 1;
+        advance();
       }
+      for (int c = 0; c < accs; ++c) {
+        if (lane == 0) tc2_commit(&tfull[b0 + c]);
+        ++uses[b0 + c];
+      }
+      ++seg;
     }
   } else if (warp < 2 + kGtTokenWarps) {
     const int tl = lane * kGtTokenWarps + (warp - 2);
-    int it = 0;
-    while (ok && work.next(u, k0, len)) {
-      const GtUnit un = gt_unit<BN>(u, p.RB, E, s_tile, s_off, s_cnt);
+    const uint32_t bar0 = map_rank(&full[0], 0);
+    while (ok && work.next(u, tile, rb, k0, len)) {
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
       const int first = un.p0 + (int)rank * un.nhalf;
       int4 rows = make_int4(0, 0, 0, 0);
       if (p.c.perm != nullptr) {
@@ -367,88 +437,93 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         }
         rows = make_int4(r[0], r[1], r[2], r[3]);
       }
-      for (int k = k0; k < k0 + len; ++k, ++it) {
-        const int s = it % S;
-        if (!mbar_wait_warp(&empty[s], ((it / S) & 1) ^ 1, err)) {
+      const bool gathers = p.c.perm != nullptr && 4 * tl < un.nhalf;
+      const bool copies = p.c.perm == nullptr && tl * Cfg::kChunk < un.nhalf;
+      for (int x = k0 * kGtK; x < (k0 + len) * kGtK; x += kGtK) {
+        if (!mbar_wait_warp(&empty[s], phase ^ 1, err)) {
           ok = false;
           break;
         }
         uint8_t* bs = st + s * Cfg::kStage + Cfg::kBytesA;
-        const uint32_t bar = map_rank(&full[s], 0);
-        if (p.c.perm != nullptr) {
-          if (tl < un.nhalf / 4) tma2_gather4(bs + tl * 512, &p.tm_x, k * kGtK, rows, bar);
-        } else if (tl * Cfg::kChunk < un.nhalf) {
-          tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, k * kGtK, first + tl * Cfg::kChunk, bar);
-        }
+        if (gathers) tma2_gather4(bs + tl * 512, &p.tm_x, x, rows, bar0 + 8 * s);
+        if (copies)
+          tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, x, first + tl * Cfg::kChunk, bar0 + 8 * s);
+        advance();
       }
     }
   } else {
-    const int q = warp & 3;
-    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-    int seg = 0;
-    while (work.next(u, k0, len)) {
-      const GtUnit un = gt_unit<BN>(u, p.RB, E, s_tile, s_off, s_cnt);
-      const int b = seg & 1;
-      if (!mbar_wait_warp(&tfull[b], (seg >> 1) & 1, err)) ok = false;
-      // one verdict for the four warps, whose named barriers below all of them must reach
-      if (lane == 0) s_warp[q] = ok;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      ok = s_warp[0] && s_warp[1] && s_warp[2] && s_warp[3];
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (!ok) break;
-      tc_fence_after();
+    // two groups of four warps, one per accumulator buffer
+    const int q = warp & 3, g = (warp - 2 - kGtTokenWarps) >> 2;
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + g * BN;
+    const uint32_t bempty = map_rank(&tempty[g], 0);
+    uint32_t uses = 0;
+    const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
+    for (int seg = 0; ok && work.next(u, tile, rb, k0, len); ++seg) {
+      if (Cfg::kAcc == 2 ? g >= accs_of(rb) : (seg & 1) != g) continue;
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      const int acc = Cfg::kAcc == 2 ? g : 0;
+      const int col0 = unit_col(rb) + acc * 2 * kRows + (int)rank * kRows;
+      ok = mbar_wait_warp(&tfull[g], uses & 1, err);
+      ++uses;
       float v[32];
-      if (len == p.KT) {
+      if (len == p.KT) {               // no named barrier from here on: pieces come first
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < un.n; c0 += 32) {
-          tmem_ld32(trow + b * BN + c0, v);
-          gt_store<T, ACT>(p, v, un, c0, (int)rank, q, lane);
+          tmem_ld32(trow + c0, v);
+          gt_store<T, ACT>(p, v, un, col0, c0, q, lane);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_rank(&tempty[b], 0));
+        if (lane == 0) mbar_arrive_cluster(bempty);
       } else {
-        const size_t stride = (size_t)2 * BN * 128;     // floats of one slot
-        const size_t at = (size_t)rank * BN * 128 + q * 32 + lane;
+        // one verdict for the four warps: all of them reach the named barriers below, or none
+        if (lane == 0) s_warp[4 * g + q] = ok;
+        sync_group();
+        ok = s_warp[4 * g] && s_warp[4 * g + 1] && s_warp[4 * g + 2] && s_warp[4 * g + 3];
+        if (!ok) break;
+        tc_fence_after();
+        const size_t stride = (size_t)2 * Cfg::kAcc * BN * 128;     // floats of one slot
+        const size_t at = (size_t)(rank * Cfg::kAcc + acc) * BN * 128 + q * 32 + lane;
         float* mine = p.part + (size_t)work.slot_of(pair, u) * stride + at;
 #pragma unroll 1
         for (int c0 = 0; c0 < un.n; c0 += 32) {
-          tmem_ld32(trow + b * BN + c0, v);
+          tmem_ld32(trow + c0, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) __stcg(mine + (size_t)(c0 + j) * 128, v[j]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_rank(&tempty[b], 0));
+        if (lane == 0) mbar_arrive_cluster(bempty);
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        sync_group();
         int c_lo, c_hi;
         work.owners(u, c_lo, c_hi);
-        if (tid == kGtThreads - 128) {
-          int32_t* ticket = p.tickets + 2 * (u - work.first) + rank;
+        if (q == 0 && lane == 0) {
+          int32_t* ticket = p.tickets + 4 * (u - work.first) + 2 * rank + acc;
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                        // ready for the next call
-          *s_flag = last;
+          s_flag[g] = last;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (*s_flag) {
+        sync_group();
+        if (s_flag[g]) {
           __threadfence();
 #pragma unroll 1
           for (int c0 = 0; c0 < un.n; c0 += 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
             for (int c = c_lo; c <= c_hi; ++c) {
               const float* src = p.part + (size_t)work.slot_of(c, u) * stride + at;
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (size_t)(c0 + j) * 128);
             }
-            gt_store<T, ACT>(p, v, un, c0, (int)rank, q, lane);
+            gt_store<T, ACT>(p, v, un, col0, c0, q, lane);
           }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // s_flag read by all
+        sync_group();                                   // s_flag and s_warp read by all
       }
-      ++seg;
     }
   }
   __syncwarp();
@@ -469,9 +544,10 @@ int grouped_tc_bn(int S, int E) {
 }
 
 size_t grouped_tc_part_bytes(int S, int E) {
-  return (size_t)kGtMaxPairs * 2 * 2 * grouped_tc_bn(S, E) * 128 * sizeof(float);
+  const int bn = grouped_tc_bn(S, E);
+  return (size_t)kGtMaxPairs * 2 * 2 * (bn > 128 ? 2 : 1) * bn * 128 * sizeof(float);
 }
-size_t grouped_tc_ticket_bytes() { return (size_t)kGtMaxPairs * 2 * sizeof(int32_t); }
+size_t grouped_tc_ticket_bytes() { return (size_t)kGtMaxPairs * 4 * sizeof(int32_t); }
 
 static bool gt_tmap(CUtensorMap* tm, bool bf16, int rank, const void* base, const cuuint64_t* dims,
                     const cuuint64_t* strides, const cuuint32_t* box) {
@@ -506,7 +582,15 @@ static cudaError_t launch_gt(GtParams& p, cudaStream_t st) {
   const GroupedDims& d = p.d;
   const GroupedCall& c = p.c;
   bool ok;
-  if (ACT) {
+  p.whole16 = ACT && (d.N / 2) % 16 == 0;
+  if (p.whole16) {
+    // [E][I / 16 groups][2 halves][16 rows][K]
+    const cuuint64_t dims[5] = {(cuuint64_t)d.K, 16, 2, (cuuint64_t)(d.N / 32), (cuuint64_t)d.E};
+    const cuuint64_t row = (cuuint64_t)c.ldw * 2;
+    const cuuint64_t str[4] = {row, row * (d.N / 2), row * 16, row * d.N};
+    const cuuint32_t box[5] = {kGtK, 16, 2, 4, 1};
+    ok = gt_tmap(&p.tm_w, bf16, 5, c.w, dims, str, box);
+  } else if (ACT) {
     const cuuint64_t dims[4] = {(cuuint64_t)d.K, (cuuint64_t)(d.N / 2), 2, (cuuint64_t)d.E};
     const cuuint64_t str[3] = {(cuuint64_t)c.ldw * 2, (cuuint64_t)c.ldw * d.N, (cuuint64_t)c.ldw * d.N * 2};
     const cuuint32_t box[4] = {kGtK, 16, 2, 1};
@@ -522,8 +606,11 @@ static cudaError_t launch_gt(GtParams& p, cudaStream_t st) {
   const cuuint32_t xbox[2] = {kGtK, c.perm ? 1u : (cuuint32_t)Cfg::kChunk};
   ok = ok && gt_tmap(&p.tm_x, bf16, 2, c.x, xdims, xstr, xbox);
   if (!ok) return cudaErrorInvalidValue;
+  const int blocks = cdiv(p.cols, ACT ? 128 : 256);
+  p.RB = blocks / Cfg::kAcc;
+  p.half = blocks % Cfg::kAcc;
   // no more pairs than K steps can keep busy
-  const long long units = ((long long)cdiv(c.S, BN) + (d.E < c.S ? d.E : c.S)) * p.RB;
+  const long long units = ((long long)cdiv(c.S, BN) + (d.E < c.S ? d.E : c.S)) * (p.RB + p.half);
   const long long useful = units * (p.KT < kGtMinSteps ? 1 : cdiv(p.KT, kGtMinSteps));
   const int G = useful < pairs ? (int)useful : pairs;
   return launch_kernel(kernel, dim3(2 * G), dim3(kGtThreads), Cfg::kSmem, st, true, p);
@@ -555,7 +642,6 @@ cudaError_t launch_grouped_tc(const GroupedDims& d, const GroupedCall& c, float*
   p.tickets = tickets;
   p.KT = cdiv(d.K, kGtK);
   p.cols = grouped_cols(d);
-  p.RB = cdiv(p.cols, d.act ? 128 : 256);
   p.packed = p.cols % 2 == 0 && c.ldo % 2 == 0 && (reinterpret_cast<uintptr_t>(c.out) & 3) == 0;
   if (d.dtype == MOE_DTYPE_F16)
     return d.act ? launch_gt_bn<__half, true>(p, st) : launch_gt_bn<__half, false>(p, st);

@@ -351,6 +351,14 @@ TC_DEV void tma2_load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, 
       "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
+TC_DEV void tma2_load_5d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, int v,
+                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+      : "memory");
+}
 // Four rows of a matrix (one-row boxes) at column x into consecutive rows of dst.
 TC_DEV void tma2_gather4(void* dst, const CUtensorMap* tm, int x, int4 rows, uint32_t bar) {
   asm volatile(
