@@ -7,6 +7,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 from . import build as _build
 
@@ -29,17 +30,9 @@ class MoeCheckpoint(ctypes.Structure):
                 ("nf_s2", c_void_p), ("a1_gscale", c_void_p), ("a2_gscale", c_void_p)]
 
 
-class MoeNormArgs(ctypes.Structure):
-    _fields_ = [("M", c_int), ("H", c_int), ("dtype", c_int), ("residual_dtype", c_int),
-                ("weight_dtype", c_int), ("kind", c_int), ("eps", c_float), ("scale", c_float),
-                ("weight_offset", c_float), ("residual", c_void_p), ("ld_residual", c_longlong),
-                ("rows", c_void_p), ("ld_rows", c_longlong), ("slot_of", c_void_p),
-                ("topk_weights", c_void_p), ("topk", c_int), ("n_rows", c_int),
-                ("shared", c_void_p), ("ld_shared", c_longlong), ("post_weight", c_void_p),
-                ("post_bias", c_void_p), ("gate", c_void_p), ("gate_row", c_longlong),
-                ("gate_col", c_longlong), ("pre_weight", c_void_p), ("pre_bias", c_void_p),
-                ("residual_out", c_void_p), ("ld_residual_out", c_longlong), ("out", c_void_p),
-                ("ld_out", c_longlong)]
+# moe_norm_args, packed in the compiler's layout: a ctypes structure of 30 fields costs more to fill
+# than the launch
+NORM_ARGS = struct.Struct("@6i3fPqPqPP2iPqPPPqqPPPqPq")
 
 
 # name -> (restype, argtypes)
@@ -97,7 +90,7 @@ SIGNATURES = {
     "moe_grouped_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
     "moe_destroy_grouped": (None, [c_void_p]),
     "moe_block_norm_get_device_error": (c_int, [c_void_p, c_int_p]),
-    "moe_block_norm": (c_int, [ctypes.POINTER(MoeNormArgs), c_void_p]),
+    "moe_block_norm": (c_int, [c_void_p, c_void_p]),
 }
 
 _LIB = None

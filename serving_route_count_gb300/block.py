@@ -49,17 +49,25 @@ def _whole(t, name, dtype, numel):
     """Address of a contiguous CUDA tensor of `numel` elements."""
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {numel} elements")
-    return _dev(t, name, dtype)
+    if t.dtype != dtype or not t.is_cuda:
+        _dev(t, name, dtype)
+    return t.data_ptr()
 
 
 def _rows(t, name, rows, cols, dtype=None):
     """(address, row stride) of a CUDA matrix [rows, cols] whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {cols}], not {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {cols}], not {list(shape)}")
     step, unit = t.stride()
-    if (unit != 1 and cols > 1) or (step < cols and t.shape[0] > 1):
-        raise ValueError(f"the rows of {name} must be contiguous and apart")
-    return _dev(t, name, dtype), (step if t.shape[0] > 1 else max(step, cols))
+    if unit != 1 or step < cols:
+        # the stride of a dimension of one element says nothing
+        if (unit != 1 and cols > 1) or (step < cols and shape[0] > 1):
+            raise ValueError(f"the rows of {name} must be contiguous and apart")
+        step = max(step, cols)
+    if not t.is_cuda or (dtype is not None and t.dtype != dtype):
+        _dev(t, name, dtype)
+    return t.data_ptr(), step
 
 
 def _code(t, name):
@@ -77,18 +85,24 @@ def moe_router(logits, topk, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk
     [M, topk], weights fp32 [M, topk]); see moe_router in include/moe_gb300.h."""
     M, E = logits.shape
     p, ld = _rows(logits, "logits", M, E)
-    topk = int(topk)
     if topk < 0:
         raise ValueError("topk must not be negative")
     if ids is None:
         ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
+        ids_p = ids.data_ptr()
+    else:
+        ids_p = _whole(ids, "ids", torch.int32, M * topk)
     if weights is None:
         weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
-    _check(_lib.load().moe_router(
+        weights_p = weights.data_ptr()
+    else:
+        weights_p = _whole(weights, "weights", torch.float32, M * topk)
+    st = _lib.load().moe_router(
         p, _code(logits, "logits"), ld, None if bias is None else _whole(bias, "bias", torch.float32, E),
-        M, E, topk, score, n_group, topk_group, bool(renormalize), scale,
-        _whole(ids, "ids", torch.int32, M * topk), _whole(weights, "weights", torch.float32, M * topk),
-        _stream(stream, logits)), "moe_router")
+        M, E, topk, score, n_group, topk_group, renormalize, scale, ids_p, weights_p,
+        _stream(stream, logits))
+    if st:
+        _check(st, "moe_router")
     return ids, weights
 
 
@@ -98,17 +112,20 @@ def moe_group(topk_ids, E, first_expert=0, offsets=None, perm=None, slot_of=None
     """Slots of topk_ids [M, topk] (int32) grouped by expert: (offsets [E + 1], perm [M * topk],
     slot_of [M, topk]), all int32; see moe_group in include/moe_gb300.h."""
     M, topk = topk_ids.shape
+    n = M * topk
+    ids_p = _whole(topk_ids, "topk_ids", torch.int32, n)
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=torch.int32, device=topk_ids.device)
     if perm is None:
-        perm = torch.empty(M * topk, dtype=torch.int32, device=topk_ids.device)
+        perm = torch.empty(n, dtype=torch.int32, device=topk_ids.device)
     if slot_of is None:
-        slot_of = torch.empty((M, topk), dtype=torch.int32, device=topk_ids.device)
-    n = M * topk
-    _check(_lib.load().moe_group(
-        _whole(topk_ids, "topk_ids", torch.int32, n), M, topk, E, first_expert,
-        _whole(offsets, "offsets", torch.int32, E + 1), _whole(perm, "perm", torch.int32, n),
-        _whole(slot_of, "slot_of", torch.int32, n), _stream(stream, topk_ids)), "moe_group")
+        slot_of = torch.empty_like(topk_ids)
+    st = _lib.load().moe_group(
+        ids_p, M, topk, E, first_expert, _whole(offsets, "offsets", torch.int32, E + 1),
+        _whole(perm, "perm", torch.int32, n), _whole(slot_of, "slot_of", torch.int32, n),
+        _stream(stream, topk_ids))
+    if st:
+        _check(st, "moe_group")
     return offsets, perm, slot_of
 
 
@@ -172,11 +189,13 @@ class MoEGrouped:
         if out is None:
             out = torch.empty((S, self.cols), dtype=self.dtype, device=x.device)
         op, ldo = _rows(out, "out", S, self.cols, self.dtype)
-        _check(_lib.load().moe_grouped_run(
+        st = _lib.load().moe_grouped_run(
             *self._fixed, xp, ldx, x.shape[0], _dev(w, "w", self.dtype), ldw,
             _whole(offsets, "offsets", torch.int32, self.E + 1),
             None if perm is None else _whole(perm, "perm", torch.int32, S), topk, op, ldo, S,
-            _stream(stream, x)), "moe_grouped_run")
+            _stream(stream, x))
+        if st:
+            _check(st, "moe_grouped_run")
         return out
 
     def device_error(self, stream=None):
@@ -207,8 +226,7 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
     rows, out None without pre_weight.  gate broadcasts over [M, H]; weights, biases and gate are
     of the rows' type or all fp32.  See moe_block_norm in include/moe_gb300.h."""
     M, H = residual.shape
-    a = _lib.MoeNormArgs()
-    a.M, a.H, a.kind, a.eps, a.scale, a.weight_offset = M, H, kind, eps, scale, weight_offset
+    residual_p, ld_residual = _rows(residual, "residual", M, H)
     if rows is not None:
         dtype = rows.dtype
     elif out is not None:
@@ -217,53 +235,61 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
         dtype = residual.dtype
     else:
         dtype = pre_weight.dtype if pre_weight is not None else torch.bfloat16
-    if dtype not in _CODE:
+    code = _CODE.get(dtype)
+    if code is None:
         raise ValueError(f"rows: {dtype} is not supported")
-    a.dtype, a.residual_dtype = _CODE[dtype], _code(residual, "residual")
-    a.residual, a.ld_residual = _rows(residual, "residual", M, H)
-    small = [t for t in (post_weight, post_bias, gate, pre_weight, pre_bias) if t is not None]
-    wt = small[0].dtype if small else dtype
-    a.weight_dtype = _CODE.get(wt, -1)
+    wt = next((t.dtype for t in (pre_weight, post_weight, gate, pre_bias, post_bias) if t is not None), dtype)
+    rows_p = slot_p = weights_p = shared_p = post_p = post_b = gate_p = pre_p = pre_b = res_out_p = out_p = 0
+    ld_rows = ld_shared = ld_res_out = ld_out = gate_row = gate_col = topk = n_rows = 0
     if slot_of is not None:
         if rows is None or topk_weights is None or slot_of.dim() != 2 or slot_of.shape[0] != M:
             raise ValueError("slot_of must be [M, topk], with rows and topk_weights")
-        a.topk, a.n_rows = slot_of.shape[1], rows.shape[0]
-        a.slot_of = _whole(slot_of, "slot_of", torch.int32, M * a.topk)
-        a.topk_weights = _whole(topk_weights, "topk_weights", torch.float32, M * a.topk)
-        a.rows, a.ld_rows = _rows(rows, "rows", None, H, dtype)
+        topk, n_rows = slot_of.shape[1], rows.shape[0]
+        slot_p = _whole(slot_of, "slot_of", torch.int32, M * topk)
+        weights_p = _whole(topk_weights, "topk_weights", torch.float32, M * topk)
+        rows_p, ld_rows = _rows(rows, "rows", None, H)
         if shared is not None:
-            a.shared, a.ld_shared = _rows(shared, "shared", M, H, dtype)
+            shared_p, ld_shared = _rows(shared, "shared", M, H, dtype)
     elif topk_weights is not None or shared is not None:
         raise ValueError("topk_weights and shared go with slot_of")
     elif rows is not None:
-        a.rows, a.ld_rows = _rows(rows, "rows", M, H, dtype)
+        rows_p, ld_rows = _rows(rows, "rows", M, H)
     if post_weight is not None:
-        a.post_weight = _whole(post_weight, "post_weight", wt, H)
+        post_p = _whole(post_weight, "post_weight", wt, H)
     if post_bias is not None:
-        a.post_bias = _whole(post_bias, "post_bias", wt, H)
+        post_b = _whole(post_bias, "post_bias", wt, H)
     if gate is not None:
-        if gate.dim() > 2:
+        gate_p = _dev(gate, "gate", wt)
+        shape, step = gate.shape, gate.stride()
+        if len(shape) == 1:
+            shape, step = (1, shape[0]), (0, step[0])
+        if len(shape) != 2 or shape[0] not in (1, M) or shape[1] not in (1, H):
             raise ValueError("gate must broadcast over [M, H]")
-        g = gate.expand(M, H)
-        a.gate = _dev(gate, "gate", wt)
-        a.gate_row = g.stride(0) if M > 1 else 0
-        a.gate_col = g.stride(1) if H > 1 else 0
+        gate_row = step[0] if shape[0] > 1 else 0
+        gate_col = step[1] if shape[1] > 1 else 0
     if pre_weight is not None:
-        a.pre_weight = _whole(pre_weight, "pre_weight", wt, H)
+        pre_p = _whole(pre_weight, "pre_weight", wt, H)
         if pre_bias is not None:
-            a.pre_bias = _whole(pre_bias, "pre_bias", wt, H)
+            pre_b = _whole(pre_bias, "pre_bias", wt, H)
         if out is None:
             out = torch.empty((M, H), dtype=dtype, device=residual.device)
-        a.out, a.ld_out = _rows(out, "out", M, H, dtype)
+        out_p, ld_out = _rows(out, "out", M, H, dtype)
     elif pre_bias is not None or out is not None:
         raise ValueError("pre_bias and out go with pre_weight")
     if rows is not None:
         if residual_out is None:
             residual_out = torch.empty((M, H), dtype=residual.dtype, device=residual.device)
-        a.residual_out, a.ld_residual_out = _rows(residual_out, "residual_out", M, H, residual.dtype)
+        res_out_p, ld_res_out = _rows(residual_out, "residual_out", M, H, residual.dtype)
     elif residual_out is not None:
         raise ValueError("residual_out goes with rows")
-    _check(_lib.load().moe_block_norm(ctypes.byref(a), _stream(stream, residual)), "moe_block_norm")
+    # moe_norm_args as the compiler lays it out
+    st = _lib.load().moe_block_norm(_lib.NORM_ARGS.pack(
+        M, H, code, _code(residual, "residual"), _CODE.get(wt, -1), kind, eps, scale, weight_offset,
+        residual_p, ld_residual, rows_p, ld_rows, slot_p, weights_p, topk, n_rows, shared_p, ld_shared,
+        post_p, post_b, gate_p, gate_row, gate_col, pre_p, pre_b, res_out_p, ld_res_out, out_p, ld_out),
+        _stream(stream, residual))
+    if st:
+        _check(st, "moe_block_norm")
     return residual_out, out
 
 

@@ -546,17 +546,17 @@ def test_refusals_of_the_grouped_product(lib):
 
 
 def test_refusals_of_the_norm(lib):
-    import ctypes
-
     from serving_route_count_gb300 import _lib
     p = 256
+    fields = ("M H dtype residual_dtype weight_dtype kind eps scale weight_offset residual ld_residual rows ld_rows slot_of topk_weights "
+              "topk n_rows shared ld_shared post_weight post_bias gate gate_row gate_col pre_weight pre_bias residual_out ld_residual_out "
+              "out ld_out").split()
+    good = dict(M=2, H=16, eps=1e-6, scale=1.0, residual=p, ld_residual=16, rows=p, ld_rows=16, pre_weight=p, residual_out=p,
+                ld_residual_out=16, out=p, ld_out=16)
 
     def norm(**kw):
-        a = _lib.MoeNormArgs(M=2, H=16, dtype=0, residual_dtype=0, weight_dtype=0, kind=0, eps=1e-6, scale=1.0, residual=p,
-                             ld_residual=16, rows=p, ld_rows=16, pre_weight=p, residual_out=p, ld_residual_out=16, out=p, ld_out=16)
-        for k, v in kw.items():
-            setattr(a, k, v)
-        return lib.moe_block_norm(ctypes.byref(a), None)
+        a = dict(good, **kw)
+        return lib.moe_block_norm(_lib.NORM_ARGS.pack(*((a.get(f) or 0) for f in fields)), None)
 
     assert lib.moe_block_norm(None, None) == 1
     assert lib.moe_block_norm_get_device_error(None, None) == 1
