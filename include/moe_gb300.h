@@ -418,7 +418,7 @@ moe_status moe_group(const int32_t* topk_ids, int M, int topk, int E, int first_
  * The plan fixes what a layer fixes: E experts of N x K, the operand type (MOE_DTYPE_BF16 or
  * MOE_DTYPE_F16, of x, W and out), the activation, and max_rows, the most positions of a call.
  * Limits: E <= 1024; 1 <= N <= 2^22 (even for SwiGLU), 1 <= K <= 2^24, N * K < 2^40, E * N <
- * 2^31, max_rows <= 2^30.
+ * 2^31, max_rows <= 2^30, (max_rows / 32 + E) * N / 128 < 2^31.
  * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (type, activation). */
 typedef struct moe_grouped_s moe_grouped_t;
 moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout, float limit,
@@ -432,7 +432,8 @@ moe_status moe_grouped_scratch_bytes(const moe_grouped_t* plan, size_t* bytes);
  *   x        [x_rows, K], row stride ldx;  w [E, N, K] with row stride ldw and expert stride
  *            ldw * N;  out [S, N or N / 2], row stride ldo;  offsets [E + 1] and perm [S] as
  *            moe_group writes them (perm entries outside [0, x_rows * topk) and offsets outside
- *            [0, S] or descending set the device error word; such rows are undefined).
+ *            [0, S] or descending set the device error word; such rows are undefined).  out must
+ *            not overlap an input.
  * Rows whose x, w and strides are 16-byte aligned run on the tensor cores; other operands (for
  * instance K % 8 != 0) on the CUDA cores, slower.
  * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (S > max_rows), MOE_ERR_CUDA. */

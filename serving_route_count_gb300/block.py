@@ -173,6 +173,7 @@ class MoEGrouped:
                                      max_rows)
         self.scratch = torch.zeros(moe_grouped_scratch_bytes(self.plan), dtype=torch.uint8,
                                    device=device)
+        torch.cuda.current_stream(self.scratch.device).synchronize()   # calls may use any stream
         self._fixed = (self.plan, self.scratch.data_ptr(), self.scratch.numel())
 
     def __call__(self, x, w, offsets, perm=None, topk=1, out=None, stream=None):

@@ -85,7 +85,7 @@ moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout,
   if (E < 1 || E > 1024 || N < 1 || N > (1 << 22) || K < 1 || max_rows < 0) return MOE_ERR_SHAPE;
   if (act == MOE_ACT_SWIGLU && N % 2 != 0) return MOE_ERR_SHAPE;
   if ((long long)N * K >= (1LL << 40) || (long long)E * N > 0x7FFFFFFFLL || K > (1 << 24) ||
-      max_rows > (1 << 30))
+      max_rows > (1 << 30) || ((long long)max_rows / 32 + E) * cdiv(N, 128) > 0x7FFFFFFFLL)
     return MOE_ERR_SHAPE;
   moe_grouped_s* g = new (std::nothrow) moe_grouped_s();
   if (g == nullptr) return MOE_ERR_ARG;

@@ -257,6 +257,38 @@ def test_product_row_counts(moe, counts):
 
 
 @gpu
+@pytest.mark.parametrize("act", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([1] * 6, 8192, 1544), ([10, 20, 0, 30, 9, 15], 8192, 1544), ([40, 3, 0, 61, 8, 64], 5888, 1800),
+                                        ([700, 256, 300, 1], 8000, 2888), ([513, 0, 90, 1000], 9984, 136), ([300], 5376, 5128)])
+def test_product_many_units(moe, counts, N, K, act):
+    """More units than CTA pairs: whole units, units cut by K steps and joined, row blocks with one of two
+    accumulators, at every token-tile width."""
+    x, w, off, perm, S = product_case(len(counts), N, K, counts, "bf16", True, topk=2, seed=K)
+    a = check_product(moe, x, w, off, perm, S, "bf16", topk=2, act=act, limit=2.0)
+    op = moe.MoEGrouped(len(counts), N, K, max_rows=S, act=moe.MOE_ACT_SWIGLU if act else moe.MOE_ACT_NONE, swiglu_limit=2.0)
+    for _ in range(3):
+        assert torch.equal(op(x, w, off, perm=perm, topk=2), a)
+
+
+@gpu
+def test_product_past_32_bits(moe):
+    """A weight tensor of more than 2^31 elements, and a K of several thousand steps' length."""
+    E, N, K = 5, 21504, 20480
+    assert E * N * K > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
+    w[E - 1] = torch.randn((N, K), generator=g, device="cuda") * K ** -0.5
+    counts = [2, 0, 0, 0, 3]
+    x = torch.randn((5, K), generator=g, device="cuda").bfloat16()
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    got = moe.MoEGrouped(E, N, K, max_rows=5)(x, w, off)
+    assert torch.count_nonzero(got[:2]) == 0
+    xs, ws = x[2:].double(), w[E - 1].double()
+    mag = xs.abs() @ ws.abs().t()
+    within(got[2:], f64(xs @ ws.t()), "bf16", K * EPS32 * f64(mag))
+
+
+@gpu
 @pytest.mark.parametrize("layout", [0, 1])
 def test_product_swiglu_options(moe, layout):
     x, w, off, perm, S = product_case(3, 192, 320, [5, 40, 17], "bf16", False, seed=9)
@@ -482,6 +514,37 @@ def test_norm_before_a_block_only(moe, kind):
     within(z, ref, "bf16", e)
 
 
+# ------------------------------------------------------------------------------------ together
+
+@gpu
+@pytest.mark.parametrize("tokens,topk", [(1, 4), (16, 4), (300, 2)])
+def test_block_example(moe, tokens, topk):
+    """examples/block16.py: a 16-bit block from router to the next block's norm, against 64 bits."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "block16.py")
+    spec = importlib.util.spec_from_file_location("block16", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    b, layer, r0, h0, r1, h1, r2, h2 = ex.run(tokens=tokens, topk=topk)
+    ids, w = b.route(h0)
+    off, perm, slot = B.group(ids.cpu().numpy(), b.E)
+    S = tokens * topk
+    u, _ = B.grouped(f64(h0), f64(b.w13), off, S, perm, topk)
+    # the 16-bit intermediate is rounded: take it from the library, checked by the product's own tests
+    u16 = b.up(h0, b.w13, torch.from_numpy(off).cuda(), perm=torch.from_numpy(perm).cuda(), topk=topk)
+    ref = B.swiglu(u[:, :b.I], u[:, b.I:], b.limit)
+    assert np.linalg.norm(f64(u16) - ref) <= 2.0 ** -8 * np.linalg.norm(ref) + 1e-6
+    y, mag = B.grouped(f64(u16), f64(b.w2), off, S)
+    y16 = b.down(u16, b.w2, torch.from_numpy(off).cuda())
+    within(y16, y, "bf16", b.I * EPS32 * mag)
+    r, z, er, ez = norm_reference(f64(r0), f64(y16), slot, f64(w), post=f64(b.post), gate=f64(b.gate), scale=b.scale, pre=f64(b.next))
+    within(r1, r, "bf16", er)
+    within(h1, z, "bf16", ez)
+    assert torch.isfinite(r2.float()).all() and torch.isfinite(h2.float()).all() and not torch.equal(r1, r2)
+    assert b.up.device_error() == b.down.device_error() == (0, 0) and layer.device_error() == (0, 0)
+
+
 # ------------------------------------------------------------------------------------ refusals
 
 def status_of(call):
@@ -526,7 +589,8 @@ def test_refusals_of_the_grouped_product(lib):
     plan = lambda E=4, N=8, K=16, dt=0, act=0, layout=0, limit=inf, alpha=1.0, beta=0.0, rows=32: m.moe_grouped_plan(  # noqa: E731
         E, N, K, dt, act, layout, limit, alpha, beta, rows)
     for bad, st in (({"E": 0}, 2), ({"E": 1025}, 2), ({"N": 0}, 2), ({"K": 0}, 2), ({"rows": -1}, 2), ({"N": 7, "act": 1}, 2),
-                    ({"N": 2 ** 22, "K": 2 ** 20}, 2), ({"dt": 2}, 3), ({"act": 2}, 3), ({"layout": 2}, 1), ({"limit": 0.0}, 1),
+                    ({"N": 2 ** 22, "K": 2 ** 20}, 2),
+                    ({"E": 1, "N": 2 ** 22, "rows": 2 ** 30}, 2), ({"dt": 2}, 3), ({"act": 2}, 3), ({"layout": 2}, 1), ({"limit": 0.0}, 1),
                     ({"limit": float("nan")}, 1), ({"alpha": inf}, 1), ({"beta": float("nan")}, 1)):
         assert status_of(lambda: plan(**bad)) == st, bad
     h = plan()
