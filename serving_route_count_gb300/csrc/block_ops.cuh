@@ -24,8 +24,9 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // of a tensor-bound call.
 __device__ __forceinline__ float swiglu_f32(float u, float g, float limit, float alpha,
                                             float beta) {
-  g = g > limit ? limit : g;              // comparisons, not fminf: NaN stays NaN
-  u = u > limit ? limit : (u < -limit ? -limit : u);
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(limit));      // NaN stays NaN
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(u) : "f"(limit));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(u) : "f"(-limit));
   return __fdividef(g, 1.0f + __expf(-alpha * g)) * (u + beta);
 }
 

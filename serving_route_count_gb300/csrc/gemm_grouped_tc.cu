@@ -148,15 +148,17 @@ struct GtTile {
 template <int BN>
 __device__ __forceinline__ GtTile gt_tile(int tile, const int* s_tile, const int* s_off,
                                           const int* s_cnt, int lane) {
-  constexpr int kChunk = GtCfg<BN>::kChunk;
   const int hi = __popc(__ballot_sync(0xffffffffu, s_tile[32 * lane] <= tile)) - 1;
   const int lo = __popc(__ballot_sync(0xffffffffu, s_tile[32 * hi + lane] <= tile)) - 1;
   GtTile r;
   r.e = 32 * hi + lo;
-  const int t = tile - s_tile[r.e];
-  r.p0 = s_off[r.e] + t * BN;
-  r.n = min(BN, s_cnt[r.e] - t * BN);
-  r.nhalf = cdiv(r.n, 2 * kChunk) * kChunk;
+  // an expert's tokens in tiles of one size, a multiple of 16 (256 + 24 rows would cost a tile of 24
+  // that streams as many weights as one of 256)
+  const int t = tile - s_tile[r.e], cnt = s_cnt[r.e], tiles = cdiv(cnt, BN);
+  const int size = tiles > 1 ? 16 * cdiv(cdiv(cnt, tiles), 16) : BN;
+  r.p0 = s_off[r.e] + t * size;
+  r.n = min(size, cnt - t * size);
+  r.nhalf = 8 * cdiv(r.n, 16);
   return r;
 }
 
@@ -334,7 +336,8 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     while (ok && work.next(u, tile, rb, k0, len)) {
       const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
       const int accs = accs_of(rb);
-      const uint32_t bytes = 2u * (accs * Cfg::kBytesW + un.nhalf * 128);
+      const int rows = p.c.perm != nullptr ? un.nhalf : cdiv(un.nhalf, Cfg::kChunk) * Cfg::kChunk;
+      const uint32_t bytes = 2u * (accs * Cfg::kBytesW + rows * 128);
       const int r0 = unit_col(rb) + (int)rank * kRows;
       for (int x = k0 * kGtK; x < (k0 + len) * kGtK; x += kGtK, ++issued) {
         if (!mbar_wait_warp(&empty[s], phase ^ 1, err)) {
