@@ -37,9 +37,9 @@ constexpr int kGtK = 64;                 // K step: one 128-byte swizzled row pe
 constexpr int kGtMaxPairs = 80;          // pairs that the scratch buffer has partial slots for
 constexpr int kGtMinSteps = 4;           // K steps below which a piece is not cut further
 
-template <int BN>
+template <int BN, int ACC>
 struct GtCfg {
-  static constexpr int kAcc = BN > 128 ? 2 : 1;              // accumulators of a unit
+  static constexpr int kAcc = ACC;                           // accumulators of a unit
   static constexpr int kHalf = BN / 2;                       // tokens a CTA loads
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;     // tokens per tile copy
   static constexpr int kBytesW = 128 * 128;                  // weight rows of one accumulator
@@ -223,10 +223,10 @@ __device__ __forceinline__ void gt_store(const GtParams& p, float (&v)[32], cons
   }
 }
 
-template <typename T, bool ACT, int BN>
+template <typename T, bool ACT, int BN, int ACC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGtThreads, 1)
 grouped_tc_kernel(const __grid_constant__ GtParams p) {
-  using Cfg = GtCfg<BN>;
+  using Cfg = GtCfg<BN, ACC>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* st = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -563,10 +563,10 @@ static bool gt_tmap(CUtensorMap* tm, bool bf16, int rank, const void* base, cons
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool ACT, int BN>
+template <typename T, bool ACT, int BN, int ACC = 1>
 static cudaError_t launch_gt(GtParams& p, cudaStream_t st) {
-  using Cfg = GtCfg<BN>;
-  auto kernel = grouped_tc_kernel<T, ACT, BN>;
+  using Cfg = GtCfg<BN, ACC>;
+  auto kernel = grouped_tc_kernel<T, ACT, BN, ACC>;
   static int pairs = 0;
   if (pairs == 0) {
     cudaError_t e =
@@ -625,7 +625,14 @@ static cudaError_t launch_gt_bn(GtParams& p, cudaStream_t st) {
     case 32: return launch_gt<T, ACT, 32>(p, st);
     case 64: return launch_gt<T, ACT, 64>(p, st);
     case 128: return launch_gt<T, ACT, 128>(p, st);
-    default: return launch_gt<T, ACT, 256>(p, st);
+    // 256 tokens.  One accumulator, double-buffered, where the tokens are in place and K is short:
+    // the exposed epilogue of two weighs more than the traffic it saves (24,576 rows over 16 experts,
+    // f16: K = 512 147 -> 135 us, 3584 481 -> 454, but 7168 487 -> 501).  Two accumulators
+    // otherwise: with one, the row gathers are the bound (K = 1152 318 against 385 us, 7168 480
+    // against 627).
+    default:
+      return p.c.perm == nullptr && p.KT <= 64 ? launch_gt<T, ACT, 256, 1>(p, st)
+                                               : launch_gt<T, ACT, 256, 2>(p, st);
   }
 }
 
