@@ -4,7 +4,8 @@
 //
 // One CTA of 256 threads per tile of 64 positions of one expert x 64 output columns; a thread
 // owns 4 x 4 sums in fp32 (two sets for a SwiGLU: up and gate), operands pass through shared
-// memory 16 K at a time.  Bound by the fp32 FMA rate and the scalar operand loads.
+// memory 16 K at a time.  Bound by the fp32 FMA rate and the scalar operand loads: fc1 + SwiGLU of
+// 2048 tokens top-8 (E = 256, K = 6144, N = 1024) takes 10.3 ms here, 0.5 ms on the tensor cores.
 #include "block_ops.cuh"
 #include "grouped.cuh"
 #include "../../include/moe_gb300.h"

@@ -17,6 +17,14 @@
 // to the scratch buffer, and the piece that arrives last adds them in K order (bit-stable, nobody
 // waits).
 //
+// Bounds and measurements (GB300, weights read once at the measured 6791 GB/s, bf16 unless stated):
+//   fc1 + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 113 us, HBM floor 106;
+//   fc2 of 16 tokens top-6, E = 384, K = 576, N = 7168: 112-117 us, floor 104 - what is left is the
+//   start (tables 2 us, first loads 2.5 us) and the last units;
+//   fc1 of 2048 tokens top-8: 495-508 us, floor 480; fc2 (K = 512, N = 6144): 275 us, floor 269;
+//   4096 tokens top-6 over 16 experts, K = 7168, N = 2304 (f16): 485-495 us, 1.66 PFLOP/s, bound by
+//   the tensor cores and their power (8192 x 8192 x 8192 in bf16: 1.93 PFLOP/s, cuBLAS 1.98).
+//
 // Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-7 token copies (tiles, or
 // gathers of four rows by index, whose issue takes ~70 cycles each: six warps share it; warp 3
 // also allocates the tensor memory), warps 8-15 epilogue.
@@ -49,7 +57,9 @@ struct GtCfg {
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
   static constexpr int kSmem = 1024 + kStages * kStage + kTables;
   static constexpr int kCols = 2 * BN;                       // tensor-memory columns: two buffers
-  // K steps that joining the pieces of a unit costs (its sums through the scratch buffer)
+  // K steps that joining the pieces of a unit costs (its sums through the scratch buffer; 8192 x
+  // 8192 x 1024 with every leftover unit cut: 134 us, with this rule 100; lower bounds for narrow
+  // tiles under many units cost fc2 of 16 tokens 2 us)
   static constexpr int kFixSteps = BN <= 32 ? 8 : (BN <= 64 ? 12 : (BN <= 128 ? 24 : 40));
 };
 
@@ -538,7 +548,11 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
 
 // ---------------------------------------------------------------------------------- host side
 
-// Token-tile width by the expected positions per expert.
+// Token-tile width by the mean positions per expert: an expert should be one tile while HBM is the
+// bound (its weights pass an SM pair once per tile), and a narrower tile leaves more of the shared
+// memory to weights in flight.  E = 256, K = 6144, N = 1024, SwiGLU, us at widths 32 / 64 / 128 /
+// 256: mean 8: 469 / 471 / 481 / 488;  24: 484 / 478 / 488 / 495;  48: 778 / 493 / 500 / 503;  64:
+// 968 / 591 / 508 / 509;  96: 1346 / 780 / 522 / 521;  128: 1722 / 971 / 696 / 534.
 int grouped_tc_bn(int S, int E) {
   if ((long long)S <= 8LL * E) return 32;
   if ((long long)S <= 24LL * E) return 64;
