@@ -12,6 +12,8 @@ What it computes (plain definitions, slow, obviously correct):
                  per-expert weight dequantisation and the MoE forward
                  out[t] = sum_j w[t,j] * expert_{id[t,j]}(x[t]), in two forms
                  (per-expert dgemm, and a brute-force per-token loop).
+  * block.py   - the 16-bit block around the experts: router top-k, grouping of the slots by
+                 expert, products grouped by expert, norms with gate, residual and combine.
 
 Parity status of each function is stated in its docstring ("pinned by ...");
 every function here is pinned by tests under ``tests/`` that do not re-use it.
