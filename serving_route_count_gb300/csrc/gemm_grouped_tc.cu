@@ -32,7 +32,7 @@
 
 #include "block_ops.cuh"
 #include "grouped.cuh"
-#include "tc_ptx.cuh"
+#include "tc_pair.cuh"
 #include "tc_tile.cuh"
 #include "../../include/moe_gb300.h"
 
