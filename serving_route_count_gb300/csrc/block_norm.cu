@@ -479,10 +479,13 @@ static cudaError_t launch_stream(const NormParams& p, int threads, int slots, cu
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  int n = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads + 32, smem);
-  if (e != cudaSuccess) return e;
-  const int grid = std::min(p.M, std::max(1, n) * sm_count());
+  int grid = p.M;
+  if (grid > sm_count()) {
+    int n = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads + 32, smem);
+    if (e != cudaSuccess) return e;
+    grid = std::min(p.M, std::max(1, n) * sm_count());
+  }
   return launch_kernel(kernel, dim3(grid), dim3(threads + 32), (size_t)smem, st, true, p, slots,
                        slot_bytes);
 }

@@ -78,12 +78,12 @@ struct GtParams {
 // adjacent (they share its tokens), and where the last block has only one of two accumulators
 // (half the work) those of all tiles at the end, so that the last wave consists of them.
 struct GtWork {
-  int KT, RB, halves, G, Gs, D, first, c;   // RB: blocks with all accumulators; first: units before
-  uint32_t W, x, x1;                        // it are whole
-  int full, u;                              // units of whole blocks; next whole unit
+  int KT, RB, G, Gs, D, first;     // RB: blocks with all accumulators; first: units before it are whole
+  uint32_t W, x, x1;               // leftover steps, this pair's range of them
+  int full, u;                     // units of whole blocks; next whole unit
   __device__ __forceinline__ void init(int tiles, int kt, int rbs, int half, int g, int cta,
                                        int fix_steps) {
-    KT = kt; RB = rbs; halves = half; G = g;
+    KT = kt; RB = rbs; G = g;
     full = tiles * rbs;
     const int units = full + (half ? tiles : 0);
     D = units / g;
@@ -100,7 +100,6 @@ struct GtWork {
     // pairs that share the leftover steps: all of them, unless the pieces got too short
     const uint32_t most = W / kGtMinSteps > R ? W / kGtMinSteps : R;
     Gs = most < (uint32_t)g ? (int)most : g;
-    c = cta;
     x = W && cta < Gs ? begin_of(cta) : 0u;
     x1 = W && cta < Gs ? begin_of(cta + 1) : 0u;
     u = cta;
@@ -173,8 +172,8 @@ __device__ __forceinline__ GtTile gt_tile(int tile, const int* s_tile, const int
 }
 
 // Stores 32 accumulator columns (tokens c0 .. c0 + 31 of the unit, n of them valid) of this
-// lane's row; col0: output column of the CTA's first row.  A lane and its neighbour exchange every other token, so that each store writes
-// two adjacent output columns.
+// lane's row; col0: output column of the CTA's first row.  A lane and its neighbour exchange every
+// other token, so that each store writes two adjacent output columns.
 template <typename T, bool ACT>
 __device__ __forceinline__ void gt_store(const GtParams& p, float (&v)[32], const GtTile& un,
                                          int col0, int c0, int q, int lane) {
@@ -247,6 +246,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
   int* s_flag = reinterpret_cast<int*>(s_tmem + 1);   // [2]
   int* s_warp = s_flag + 2;            // [warps]
+  int* s_fills = s_warp + kGtThreads / 32;   // fills whose stage the weight warp has found empty
   int* s_off = reinterpret_cast<int*>(st + S * Cfg::kStage + 512);
   int* s_cnt = s_off + 1028;
   int* s_tile = s_cnt + 1028;
@@ -270,6 +270,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
       mbar_init(&tempty[b], 8);        // four epilogue warps of each CTA
     }
     fence_barrier_init();
+    *s_fills = 0;
   }
   tc_fence_before();
   cluster_sync_all();
@@ -279,8 +280,9 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   pdl_wait_prev();
   pdl_launch_next();
 
-  // the experts' tiles: thread t owns experts 4 t .. 4 t + 3
-  int cnt[4], tiles = 0;
+  // the experts' tiles: thread t owns experts 4 t .. 4 t + 3.  Offsets that are out of order or range
+  // make the call empty (every CTA sees the same ones), so that no tile is ever out of its bounds.
+  int cnt[4], tiles = 0, bad = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = 4 * tid + i;
@@ -288,7 +290,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     if (e < E) {
       const int a = p.c.offsets[e], b = p.c.offsets[e + 1];
       if (a < 0 || b < a || b > p.c.S)
-        set_error(err, kErrRouteBounds);
+        bad = 1;
       else
         cnt[i] = b - a;
       s_off[e] = a;
@@ -303,7 +305,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     if (lane >= o) incl += y;
   }
   if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   int before = incl - tiles, total = 0;
 #pragma unroll
   for (int w = 0; w < kGtThreads / 32; ++w) {
@@ -314,6 +316,10 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   for (int i = 0; i < 4; ++i) {
     if (4 * tid + i < E) s_tile[4 * tid + i] = before;
     before += cdiv(cnt[i], BN);
+  }
+  if (bad) {
+    total = 0;
+    if (tid == 0) set_error(err, kErrRouteBounds);
   }
   // rows past the last group
   {
@@ -355,6 +361,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
           break;
         }
         if (lane == 0) {
+          publish_count(s_fills, issued + 1);
           const uint32_t bar = bar0 + 8 * s;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           for (int c = 0; c < accs; ++c) {
@@ -432,17 +439,33 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   } else if (warp < 2 + kGtTokenWarps) {
     const int tl = lane * kGtTokenWarps + (warp - 2);
     const uint32_t bar0 = map_rank(&full[0], 0);
-    while (ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
-      const int first = un.p0 + (int)rank * un.nhalf;
-      int4 rows = make_int4(0, 0, 0, 0);
+    // rows 4 tl .. 4 tl + 3 of this CTA's tokens by permutation (past the tile its last row again);
+    // a unit's entries are loaded under the copies of the one before it
+    int f[4] = {0, 0, 0, 0};
+    GtTile un = {};
+    const auto look_up = [&](int tile) {
+      un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
       if (p.c.perm != nullptr) {
-        // rows 4 tl .. 4 tl + 3 of this CTA's tokens; past the tile its last row again
+        const int first = un.p0 + (int)rank * un.nhalf + 4 * tl;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = p.c.perm[min(first + i, un.p0 + un.n - 1)];
+      }
+    };
+    // A warp may have no copy in a unit, and then nothing waits for it: it goes by the weight warp's
+    // count of empty stages, which the copies of every fill follow, and not by the barriers' parities
+    // (a warp two phases behind or ahead would take the wrong one).
+    int fill = 0;                    // fills before this unit
+    bool more = work.next(u, tile, rb, k0, len);
+    if (more) look_up(tile);
+    while (ok && more) {
+      int4 rows = make_int4(0, 0, 0, 0);
+      const bool gathers = p.c.perm != nullptr && 4 * tl < un.nhalf;
+      const bool copies = p.c.perm == nullptr && tl * Cfg::kChunk < un.nhalf;
+      if (gathers) {
         int r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int f = p.c.perm[min(first + 4 * tl + i, un.p0 + un.n - 1)];
-          r[i] = f < 0 ? -1 : f / p.c.topk;
+          r[i] = f[i] < 0 ? -1 : f[i] / p.c.topk;
           if (r[i] < 0 || r[i] >= p.c.x_rows) {
             set_error(err, kErrRouteBounds);
             r[i] = 0;
@@ -450,19 +473,26 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         }
         rows = make_int4(r[0], r[1], r[2], r[3]);
       }
-      const bool gathers = p.c.perm != nullptr && 4 * tl < un.nhalf;
-      const bool copies = p.c.perm == nullptr && tl * Cfg::kChunk < un.nhalf;
-      for (int x = k0 * kGtK; x < (k0 + len) * kGtK; x += kGtK) {
-        if (!mbar_wait_warp(&empty[s], phase ^ 1, err)) {
-          ok = false;
-          break;
+      const int first = un.p0 + (int)rank * un.nhalf + tl * Cfg::kChunk;
+      const bool active = __any_sync(0xffffffffu, gathers || copies);
+      const int x0 = k0 * kGtK, steps = len;
+      more = work.next(u, tile, rb, k0, len);
+      if (more) look_up(tile);
+      if (active) {
+        s = fill % S;
+        for (int i = 0; i < steps; ++i) {
+          if (!wait_count_warp(s_fills, fill + i + 1, err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* bs = st + s * Cfg::kStage + Cfg::kBytesA;
+          const int x = x0 + i * kGtK;
+          if (gathers) tma2_gather4(bs + tl * 512, &p.tm_x, x, rows, bar0 + 8 * s);
+          if (copies) tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, x, first, bar0 + 8 * s);
+          if (++s == S) s = 0;
         }
-        uint8_t* bs = st + s * Cfg::kStage + Cfg::kBytesA;
-        if (gathers) tma2_gather4(bs + tl * 512, &p.tm_x, x, rows, bar0 + 8 * s);
-        if (copies)
-          tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, x, first + tl * Cfg::kChunk, bar0 + 8 * s);
-        advance();
       }
+      fill += steps;
     }
   } else {
     // two groups of four warps, one per accumulator buffer

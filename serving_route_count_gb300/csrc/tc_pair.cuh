@@ -29,6 +29,26 @@ TC_DEV void cluster_sync_all() {
 TC_DEV void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A count in shared memory that one thread raises and others wait for.
+TC_DEV void publish_count(int* c, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(c)), "r"(v) : "memory");
+}
+// Waits (bounded as mbar_wait) until the count is at least v; one verdict for the warp.
+TC_DEV bool wait_count_warp(const int* c, int v, int32_t* err) {
+  const auto read = [&]() {
+    int x;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(x) : "r"(smem_u32(c)) : "memory");
+    return x;
+  };
+  bool ok = read() >= v;
+  if (!ok) {
+    const uint64_t t0 = globaltimer();
+    while (!ok && globaltimer() - t0 <= kTimeoutNs)
+      for (int i = 0; !ok && i < 64; ++i) ok = read() >= v;
+    if (!ok) atomicOr(err, kErrTimeout);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
 // Tile loads into this CTA's shared memory that count their bytes on a barrier of either CTA of
 // the pair (`bar`: shared-cluster address).
 TC_DEV void tma2_load_2d(void* dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {

@@ -267,8 +267,12 @@ def test_product_many_units(moe, counts, N, K, act):
     a = check_product(moe, x, w, off, perm, S, "bf16", topk=2, act=act, limit=2.0)
     check_product(moe, x[perm.long() // 2].contiguous(), w, off, None, S, "bf16", act=act, limit=2.0)   # the same rows in place
     op = moe.MoEGrouped(len(counts), N, K, max_rows=S, act=moe.MOE_ACT_SWIGLU if act else moe.MOE_ACT_NONE, swiglu_limit=2.0)
-    for _ in range(3):
+    xs = x[perm.long() // 2].contiguous()
+    b = op(xs, w, off)
+    for _ in range(30):                                     # every schedule gives the same bits, and no wait gives up
         assert torch.equal(op(x, w, off, perm=perm, topk=2), a)
+        assert torch.equal(op(xs, w, off), b)
+    assert op.device_error() == (0, 0)
 
 
 @gpu
