@@ -665,18 +665,22 @@ static cudaError_t launch_gt(GtParams& p, cudaStream_t st) {
 
 template <typename T, bool ACT>
 static cudaError_t launch_gt_bn(GtParams& p, cudaStream_t st) {
+  // expected units of two accumulators, against the pairs of a whole GPU
+  const long long tiles = cdiv(p.c.S, 256) + (p.d.E < p.c.S ? p.d.E : p.c.S) / 2;
+  const bool few = tiles * cdiv(p.cols, ACT ? 256 : 512) < 60;
   switch (grouped_tc_bn(p.c.S, p.d.E)) {
     case 32: return launch_gt<T, ACT, 32>(p, st);
     case 64: return launch_gt<T, ACT, 64>(p, st);
     case 128: return launch_gt<T, ACT, 128>(p, st);
-    // 256 tokens.  One accumulator, double-buffered, where the tokens are in place and K is short:
-    // the exposed epilogue of two weighs more than the traffic it saves (24,576 rows over 16 experts,
-    // f16: K = 512 147 -> 135 us, 3584 481 -> 454, but 7168 487 -> 501).  Two accumulators
-    // otherwise: with one, the row gathers are the bound (K = 1152 318 against 385 us, 7168 480
-    // against 627).
+    // 256 tokens.  One accumulator, double-buffered, where units of two would leave pairs idle (256
+    // rows over 2 experts, K = N = 4096: 27 us against 49; 4000 over 16, K = N = 512: 11.6 against
+    // 14.7), and where the tokens are in place and K is short: the exposed epilogue of two weighs
+    // more than the traffic it saves (24,576 rows over 16 experts, f16: K = 512 147 -> 135 us, 3584
+    // 481 -> 454, but 7168 487 -> 501).  Two accumulators otherwise: with one, the row gathers are
+    // the bound (K = 1152 318 against 385 us, 7168 480 against 627).
     default:
-      return p.c.perm == nullptr && p.KT <= 64 ? launch_gt<T, ACT, 256, 1>(p, st)
-                                               : launch_gt<T, ACT, 256, 2>(p, st);
+      return few || (p.c.perm == nullptr && p.KT <= 64) ? launch_gt<T, ACT, 256, 1>(p, st)
+                                                        : launch_gt<T, ACT, 256, 2>(p, st);
   }
 }
 
