@@ -15,8 +15,10 @@ namespace moe {
 // that order like the floats, with 0 for a masked expert.  The j-th choice is a warp maximum of
 // the lanes' best keys and, among the lanes that hold it, the minimum of their lowest indices
 // (two reductions of the warp's integer unit); the winner's lane clears that key and every lane
-// rescans its own.  8192 tokens x 256 fp32 logits, top-8: 8.4 us, bound by instruction issue (the
-// reads are 1.3 us of HBM time); one token x 384: 4.8 us of latency.
+// rescans its own.  With eight keys a lane and more, the rounds run over the few keys that can be
+// chosen at all.  8192 tokens: 256 fp32 logits, top-8 7.0 us (with all keys in every round 8.3), 512
+// top-10 9.6 (15.9), 1024 top-16 19.5 (43); bound by instruction issue (8192 x 256 are 1.3 us of HBM
+// time).  One token x 384, top-6, sigmoid: 3.2 us of latency.
 constexpr int kRouterWarps = 4;
 
 // Integer that orders like v (0: NaN or -inf, which are never chosen; -0 and +0 alike).
@@ -114,7 +116,58 @@ router_kernel(const T* __restrict__ logits, long long ld, const float* __restric
   }
 
   int id = -1;                                // lane j: the j-th choice
-  for (int j = 0; j < topk; ++j) {
+  bool chosen = false;
+  if (VPL >= 8 && topk <= 16) {
+    // The topk-th largest of the lanes' largest keys bounds the choice from below, and few keys reach
+    // it (about 12 of 256 for top-8): those are packed one to a lane, in ascending index, and the
+    // rounds go over them alone.  Where more than 32 reach it (ties, or topk near 32: 26.5 against 22.9
+    // us at top-32 of 256) the rounds below go over all keys.
+    __shared__ uint2 s_few[kRouterWarps][32];
+    uint2* few = s_few[threadIdx.x >> 5];
+    uint32_t best = 0u;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    uint32_t bound = 1u;                      // every key that is not masked
+    for (int left = topk; left > 0;) {
+      const uint32_t top = __reduce_max_sync(full, best);
+      if (top == 0u) {
+        bound = 1u;
+        break;
+      }
+      bound = top;
+      left -= __popc(__ballot_sync(full, best == top));
+      if (best == top) best = 0u;
+    }
+    unsigned reach[VPL];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      reach[i] = __ballot_sync(full, key[i] >= bound);
+      n += __popc(reach[i]);
+    }
+    if (n <= 32) {
+      n = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (key[i] >= bound)
+          few[n + __popc(reach[i] & ((1u << lane) - 1u))] = make_uint2(key[i], lane + 32 * i);
+        n += __popc(reach[i]);
+      }
+      __syncwarp();
+      const uint2 mine = lane < n ? few[lane] : make_uint2(0u, 0u);
+      uint32_t k = mine.x;
+      for (int j = 0; j < topk; ++j) {
+        const uint32_t top = __reduce_max_sync(full, k);
+        if (top == 0u) break;
+        const int at = __ffs(__ballot_sync(full, k == top)) - 1;   // the lowest index
+        const int e = __shfl_sync(full, (int)mine.y, at);
+        if (lane == j) id = e;
+        if (lane == at) k = 0u;
+      }
+      chosen = true;
+    }
+  }
+  for (int j = 0; !chosen && j < topk; ++j) {
     uint32_t best = 0u;
     int at = 0;
 #pragma unroll

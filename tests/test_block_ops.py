@@ -147,6 +147,21 @@ def test_router_ties_masks_and_extremes(moe, score):
 
 
 @gpu
+@pytest.mark.parametrize("E,topk", [(256, 8), (384, 16), (1000, 16), (256, 17), (512, 1)])
+def test_router_many_equal_keys(moe, E, topk):
+    """Rows of few values: from none to all keys equal, more of them than a warp's lanes reach the choice."""
+    g = torch.Generator().manual_seed(E)
+    rows = [torch.randint(0, v, (E,), generator=g).float() for v in (1, 2, 3, 8, 40, 400)]
+    few = torch.full((E,), -math.inf)
+    few[::61] = 1.0                                             # fewer keys than topk in some cases
+    spread = torch.zeros(E)
+    spread[::32] = 5.0                                          # one lane holds all the largest
+    logits = torch.stack(rows + [few, spread, -spread]).cuda()
+    for score in ("softmax", "sigmoid"):
+        check_router(moe, logits, topk, score)
+
+
+@gpu
 def test_router_strided_rows_and_given_outputs(moe):
     big = torch.randn(20, 77, device="cuda")
     view = big[:, 5:69]
