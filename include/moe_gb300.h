@@ -431,8 +431,9 @@ moe_status moe_grouped_scratch_bytes(const moe_grouped_t* plan, size_t* bytes);
  *            error (below) it has to be zero-filled again.
  *   x        [x_rows, K], row stride ldx;  w [E, N, K] with row stride ldw and expert stride
  *            ldw * N;  out [S, N or N / 2], row stride ldo;  offsets [E + 1] and perm [S] as
- *            moe_group writes them (perm entries outside [0, x_rows * topk) and offsets outside
- *            [0, S] or descending set the device error word; such rows are undefined).  out must
+ *            moe_group writes them (perm entries outside [0, x_rows * topk) set the device error
+ *            word and their rows are undefined; offsets outside [0, S] or descending set it and all
+ *            of out is undefined).  out must
  *            not overlap an input.
  * Rows whose x, w and strides are 16-byte aligned run on the tensor cores; other operands (for
  * instance K % 8 != 0) on the CUDA cores, slower.

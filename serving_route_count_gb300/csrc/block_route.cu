@@ -85,7 +85,7 @@ router_kernel(const T* __restrict__ logits, long long ld, const float* __restric
     float k = v[i];
     if (score == MOE_SCORE_SIGMOID && k > -INFINITY) {
       k = sigmoid_ieee(k);
-      if (bias != nullptr) k = __fadd_rn(k, kHeld ? b[i % (kHeld ? VPL : 1)] : bias[lane + 32 * i]);
+      if (bias != nullptr) k = __fadd_rn(k, kHeld ? b[kHeld ? i : 0] : bias[lane + 32 * i]);
     }
     key[i] = order_key(k);
   }
