@@ -84,22 +84,25 @@ def moe_router(logits, topk, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk
     """Top-k experts and weights of every row of logits [M, E] (bf16, f16 or fp32): (ids int32
     [M, topk], weights fp32 [M, topk]); see moe_router in include/moe_gb300.h."""
     M, E = logits.shape
-    p, ld = _rows(logits, "logits", M, E)
+    ld, unit = logits.stride()
+    dtype = _CODE.get(logits.dtype)
+    if unit != 1 or ld < E or dtype is None or not logits.is_cuda:
+        ld, dtype = _rows(logits, "logits", M, E)[1], _code(logits, "logits")
     if topk < 0:
         raise ValueError("topk must not be negative")
+    # outputs made here need no checks
+    dev = logits.device
     if ids is None:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
-        ids_p = ids.data_ptr()
+        ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
     else:
-        ids_p = _whole(ids, "ids", torch.int32, M * topk)
+        _whole(ids, "ids", torch.int32, M * topk)
     if weights is None:
-        weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
-        weights_p = weights.data_ptr()
+        weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
     else:
-        weights_p = _whole(weights, "weights", torch.float32, M * topk)
+        _whole(weights, "weights", torch.float32, M * topk)
     st = _lib.load().moe_router(
-        p, _code(logits, "logits"), ld, None if bias is None else _whole(bias, "bias", torch.float32, E),
-        M, E, topk, score, n_group, topk_group, renormalize, scale, ids_p, weights_p,
+        logits.data_ptr(), dtype, ld, None if bias is None else _whole(bias, "bias", torch.float32, E),
+        M, E, topk, score, n_group, topk_group, renormalize, scale, ids.data_ptr(), weights.data_ptr(),
         _stream(stream, logits))
     if st:
         _check(st, "moe_router")
@@ -114,16 +117,21 @@ def moe_group(topk_ids, E, first_expert=0, offsets=None, perm=None, slot_of=None
     M, topk = topk_ids.shape
     n = M * topk
     ids_p = _whole(topk_ids, "topk_ids", torch.int32, n)
+    # outputs made here need no checks
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=torch.int32, device=topk_ids.device)
+    else:
+        _whole(offsets, "offsets", torch.int32, E + 1)
     if perm is None:
         perm = torch.empty(n, dtype=torch.int32, device=topk_ids.device)
+    else:
+        _whole(perm, "perm", torch.int32, n)
     if slot_of is None:
         slot_of = torch.empty_like(topk_ids)
-    st = _lib.load().moe_group(
-        ids_p, M, topk, E, first_expert, _whole(offsets, "offsets", torch.int32, E + 1),
-        _whole(perm, "perm", torch.int32, n), _whole(slot_of, "slot_of", torch.int32, n),
-        _stream(stream, topk_ids))
+    else:
+        _whole(slot_of, "slot_of", torch.int32, n)
+    st = _lib.load().moe_group(ids_p, M, topk, E, first_expert, offsets.data_ptr(), perm.data_ptr(),
+                               slot_of.data_ptr(), _stream(stream, topk_ids))
     if st:
         _check(st, "moe_group")
     return offsets, perm, slot_of

@@ -326,6 +326,17 @@ def test_product_strides_and_alignment(moe, ldx, ldw, shift):
 
 
 @gpu
+@pytest.mark.parametrize("K", [1, 3, 63, 65, 129])
+@pytest.mark.parametrize("gather", [False, True])
+def test_product_odd_k_in_aligned_rows(moe, K, gather):
+    """K of any size on the tensor cores, in rows padded (with NaN) to 16 bytes."""
+    ld = (K + 7) // 8 * 8 + 8
+    for act in (False, True):
+        x, w, off, perm, S = product_case(5, 66, K, [4, 0, 33, 1, 90], "bf16", gather, topk=2 if gather else 1, ldx=ld, ldw=ld, seed=K)
+        check_product(moe, x, w, off, perm, S, "bf16", topk=2 if gather else 1, act=act)
+
+
+@gpu
 def test_product_neighbours_do_not_leak(moe):
     """NaN and inf in rows of x and in experts that a position does not use stay out of its result."""
     counts = [5, 6, 7]
