@@ -426,9 +426,9 @@ moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout,
 /* Bytes of the scratch buffer of moe_grouped_run (256-byte aligned, caller-owned). */
 moe_status moe_grouped_scratch_bytes(const moe_grouped_t* plan, size_t* bytes);
 /* One product.
- *   scratch  zero-filled by the caller once, before its first use; every call leaves it ready for
- *            the next.  Calls that share a scratch buffer must be stream-ordered.  After a device
- *            error (below) it has to be zero-filled again.
+ *   scratch  its first 4096 bytes zero-filled by the caller once, before the first use; every call
+ *            leaves them ready for the next.  Calls that share a scratch buffer must be
+ *            stream-ordered.  After a device error (below) those bytes have to be zero-filled again.
  *   x        [x_rows, K], row stride ldx;  w [E, N, K] with row stride ldw and expert stride
  *            ldw * N;  out [S, N or N / 2], row stride ldo;  offsets [E + 1] and perm [S] as
  *            moe_group writes them (perm entries outside [0, x_rows * topk) set the device error

@@ -179,8 +179,9 @@ class MoEGrouped:
         self.cols = N // 2 if act == MOE_ACT_SWIGLU else N
         self.plan = moe_grouped_plan(E, N, K, _CODE[dtype], act, layout, swiglu_limit, alpha, beta,
                                      max_rows)
-        self.scratch = torch.zeros(moe_grouped_scratch_bytes(self.plan), dtype=torch.uint8,
+        self.scratch = torch.empty(moe_grouped_scratch_bytes(self.plan), dtype=torch.uint8,
                                    device=device)
+        self.scratch[:4096].zero_()
         torch.cuda.current_stream(self.scratch.device).synchronize()   # calls may use any stream
         self._fixed = (self.plan, self.scratch.data_ptr(), self.scratch.numel())
 

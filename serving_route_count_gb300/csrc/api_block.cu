@@ -22,7 +22,6 @@ cudaError_t norm_device_error(int* code, cudaStream_t st);
 cudaError_t launch_grouped_simt(const GroupedDims& d, const GroupedCall& c, cudaStream_t st);
 // gemm_grouped_tc.cu
 size_t grouped_tc_part_bytes(int S, int E);
-size_t grouped_tc_ticket_bytes();
 bool grouped_tc_addressable(const GroupedDims& d, const GroupedCall& c);
 cudaError_t launch_grouped_tc(const GroupedDims& d, const GroupedCall& c, float* part,
                               int32_t* tickets, cudaStream_t st);
@@ -32,7 +31,7 @@ using namespace moe;
 
 struct moe_grouped_s {
   GroupedDims d;
-  size_t tickets, part, bytes;            // sections of the scratch buffer after the error word
+  size_t bytes;                           // of the scratch buffer
 };
 
 namespace {
@@ -40,8 +39,6 @@ namespace {
 moe_status status(cudaError_t e) { return static_cast<moe_status>(report_cuda(e)); }
 
 bool dtype16(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
-
-constexpr size_t kErrBytes = 256;         // the error word's section of the scratch buffer
 
 }  // namespace
 
@@ -90,9 +87,7 @@ moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout,
   moe_grouped_s* g = new (std::nothrow) moe_grouped_s();
   if (g == nullptr) return MOE_ERR_ARG;
   g->d = GroupedDims{E, N, K, dtype, act, layout, max_rows, limit, alpha, beta};
-  g->tickets = kErrBytes;
-  g->part = align_up(g->tickets + grouped_tc_ticket_bytes(), 256);
-  g->bytes = g->part + grouped_tc_part_bytes(max_rows, E);
+  g->bytes = kGtPartAt + grouped_tc_part_bytes(max_rows, E);
   *out = g;
   return MOE_OK;
 }
@@ -124,8 +119,8 @@ moe_status moe_grouped_run(const moe_grouped_t* plan, void* scratch, size_t scra
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!grouped_tc_addressable(d, c)) return status(launch_grouped_simt(d, c, st));
   uint8_t* base = static_cast<uint8_t*>(scratch);
-  return status(launch_grouped_tc(d, c, reinterpret_cast<float*>(base + plan->part),
-                                  reinterpret_cast<int32_t*>(base + plan->tickets), st));
+  return status(launch_grouped_tc(d, c, reinterpret_cast<float*>(base + kGtPartAt),
+                                  reinterpret_cast<int32_t*>(base + kGtTicketsAt), st));
 }
 
 moe_status moe_grouped_get_device_error(const moe_grouped_t* plan, void* scratch, void* stream,

@@ -13,9 +13,9 @@
 //
 // The grid is persistent, one pair per two SMs.  The number of units is known on the device only
 // (offsets); every CTA builds the table of the experts' tiles in shared memory.  Whole waves of
-// units go round robin; the units left over are cut evenly by K steps, every piece's fp32 sums go
-// to the scratch buffer, and the piece that arrives last adds them in K order (bit-stable, nobody
-// waits).
+// units go round robin; where it shortens the longest pair's work, the units left over are cut evenly
+// by K steps: every piece's fp32 sums go to the scratch buffer, and the piece that arrives last adds
+// them in K order (bit-stable, nobody waits).
 //
 // Bounds and measurements (GB300, weights read once at the measured 6791 GB/s, bf16 unless stated):
 //   fc1 + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 113 us, HBM floor 106;
@@ -42,7 +42,6 @@ using namespace tc;
 constexpr int kGtThreads = 512;
 constexpr int kGtTokenWarps = 6;         // warps 2-7
 constexpr int kGtK = 64;                 // K step: one 128-byte swizzled row per operand row
-constexpr int kGtMaxPairs = 80;          // pairs that the scratch buffer has partial slots for
 constexpr int kGtMinSteps = 4;           // K steps below which a piece is not cut further
 
 template <int BN, int ACC>
@@ -594,7 +593,6 @@ size_t grouped_tc_part_bytes(int S, int E) {
   const int bn = grouped_tc_bn(S, E);
   return (size_t)kGtMaxPairs * 2 * 2 * (bn > 128 ? 2 : 1) * bn * 128 * sizeof(float);
 }
-size_t grouped_tc_ticket_bytes() { return (size_t)kGtMaxPairs * 4 * sizeof(int32_t); }
 
 static bool gt_tmap(CUtensorMap* tm, bool bf16, int rank, const void* base, const cuuint64_t* dims,
                     const cuuint64_t* strides, const cuuint32_t* box) {

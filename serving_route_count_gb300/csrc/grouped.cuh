@@ -6,6 +6,12 @@
 
 namespace moe {
 
+// Scratch buffer of a plan: the error word, the tickets of the units that are cut along K ([pairs][2
+// CTAs][2 accumulators]), then the partial sums.  What lies before those is zero between calls.
+constexpr int kGtMaxPairs = 80;          // CTA pairs that the buffer serves
+constexpr size_t kGtTicketsAt = 256, kGtPartAt = 4096;
+static_assert(kGtTicketsAt + kGtMaxPairs * 4 * sizeof(int32_t) <= kGtPartAt, "tickets");
+
 struct GroupedDims {
   int E, N, K, dtype, act, layout, max_rows;
   float limit, alpha, beta;
