@@ -18,7 +18,8 @@
 // them in K order (bit-stable, nobody waits).
 //
 // Bounds and measurements (GB300, weights read once at the measured 6791 GB/s, bf16 unless stated):
-//   fc1 + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 113 us, HBM floor 106;
+//   fc1 + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 111-115 us, HBM floor 106; of one
+//   token 21.8, floor 14.8;
 //   fc2 of 16 tokens top-6, E = 384, K = 576, N = 7168: 112-117 us, floor 104 - what is left is the
 //   start (tables 2 us, first loads 2.5 us) and the last units;
 //   fc1 of 2048 tokens top-8: 495-508 us, floor 480; fc2 (K = 512, N = 6144): 275 us, floor 269;
@@ -533,35 +534,57 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         for (int c0 = 0; c0 < un.n; c0 += 32) {
           tmem_ld32(trow + c0, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) __stcg(mine + (size_t)(c0 + j) * 128, v[j]);
+          for (int j = 0; j < 32; ++j)
+            if (c0 + j < un.n) __stcg(mine + (size_t)(c0 + j) * 128, v[j]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(bempty);
-        __threadfence();
         sync_group();
         int c_lo, c_hi;
         work.owners(u, c_lo, c_hi);
         if (q == 0 && lane == 0) {
+          __threadfence();                              // the group's sums, ordered by its barrier
           int32_t* ticket = p.tickets + 4 * (u - work.first) + 2 * rank + acc;
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                        // ready for the next call
+          __threadfence();
           s_flag[g] = last;
         }
         sync_group();
         if (s_flag[g]) {
-          __threadfence();
-#pragma unroll 1
-          for (int c0 = 0; c0 < un.n; c0 += 32) {
+          if (un.n <= 8) {
+            // few tokens: the sums of four pieces in flight at a time (one token top-8, fc1 of the
+            // E = 256 layer: 24.8 -> 21.8 us, most of it here, the rest by writing n columns only)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
-#pragma unroll 2
-            for (int c = c_lo; c <= c_hi; ++c) {
-              const float* src = p.part + (size_t)work.slot_of(c, u) * stride + at;
+            for (int c = c_lo; c <= c_hi; c += 4) {
+              float t[4][8];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (size_t)(c0 + j) * 128);
+              for (int i = 0; i < 4; ++i) {
+                const float* src = p.part + (size_t)work.slot_of(min(c + i, c_hi), u) * stride + at;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[i][j] = __ldcg(src + (size_t)min(j, un.n - 1) * 128);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += c + i <= c_hi ? t[i][j] : 0.f;
             }
-            gt_store<T, ACT>(p, v, un, col0, c0, q, lane);
+            gt_store<T, ACT>(p, v, un, col0, 0, q, lane);
+          } else {
+#pragma unroll 1
+            for (int c0 = 0; c0 < un.n; c0 += 32) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+#pragma unroll 2
+              for (int c = c_lo; c <= c_hi; ++c) {
+                const float* src = p.part + (size_t)work.slot_of(c, u) * stride + at;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (size_t)(c0 + j) * 128);
+              }
+              gt_store<T, ACT>(p, v, un, col0, c0, q, lane);
+            }
           }
         }
         sync_group();                                   // s_flag and s_warp read by all
