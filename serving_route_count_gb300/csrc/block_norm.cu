@@ -6,9 +6,9 @@
 // once, and a norm is one block-wide sum (two for the layer norm: the mean first, then the squares
 // around it).  The arithmetic runs on pairs of channels (the packed fp32 instructions).  Two
 // kernels: norm_stream_kernel, whose rows arrive by asynchronous copies in a shared-memory ring
-// ahead of the arithmetic, and block_norm_kernel, plain loads, for rows that do not start on 16
-// bytes or are too long for a ring.  Bound by HBM: 4096 x 7168 with a top-6 combine 91 us (85 % of the
-// measured copy bandwidth), 8192 x 6144 with an fp32 residual 102 us (87 %); one token 5.6 us.
+// ahead of the arithmetic, and block_norm_kernel, plain loads, for short rows, rows that do not
+// start on 16 bytes and rows too long for a ring.  Bound by HBM: 4096 x 7168 with a top-6 combine 91 us (85 % of the
+// measured copy bandwidth), 8192 x 6144 with an fp32 residual 102 us (87 %); one token 4.8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -18,7 +18,9 @@
 
 namespace moe {
 
-constexpr int kNormMostSmem = 200 * 1024;   // ring buffers of an SM's CTAs (the rest is L1: weights)
+// Ring buffers of all of an SM's CTAs; what is left of its shared memory serves as L1 for the weights
+// (4096 x 7168 top-6, us with 100 / 132 / 170 / 200 KB: 94 / 91 / 100 / 105).
+constexpr int kNormRings = 132 * 1024;
 
 struct NormParams {
   int M, H, kind, wide;             // wide: weights, biases and gate are fp32
@@ -475,17 +477,14 @@ static cudaError_t launch_stream(const NormParams& p, int threads, int slots, cu
   auto kernel = norm_stream_kernel<T, R, NCH, MAXT, MINB>;
   static bool attr = false;
   if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMostSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRings);
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  int grid = p.M;
-  if (grid > sm_count()) {
-    int n = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads + 32, smem);
-    if (e != cudaSuccess) return e;
-    grid = std::min(p.M, std::max(1, n) * sm_count());
-  }
+  int n = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads + 32, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(p.M, std::max(1, n) * sm_count());
   return launch_kernel(kernel, dim3(grid), dim3(threads + 32), (size_t)smem, st, true, p, slots,
                        slot_bytes);
 }
@@ -494,14 +493,19 @@ template <typename T, typename R, bool VEC>
 static cudaError_t launch_norm_v(const NormParams& p, cudaStream_t st) {
   const int chunks = cdiv(p.H, 8);
   if constexpr (VEC) {
-    // Long rows: the ring.  Measured at 8192 x 6144 (fp32 residual) and 4096 x 7168 top-6: 103 / 92
-    // us against 118 / 193 with plain loads; at H = 2048 and 512 the copying warp costs more than
-    // it hides (85 against 72 us, 89 against 39 at 32 M elements), so shorter rows are loaded.
-    // Ring buffers for a third of an SM's shared memory: what is left serves as L1 for the weights
-    // (with half of it 105 and 108 us).
-    const int slots = std::min(kNormSlots, kNormMostSmem / 3 / (p.H * (int)sizeof(R)));
+    // The ring, but for short rows, where the copying warp costs more than it hides.  us with the ring
+    // and with plain loads: 4096 x 7168 top-6 91 / 193, 8192 x 2048 top-6 56 / 70, 16384 x 1024 top-6
+    // 62 / 68; without a combine 8192 x 6144 (fp32 residual) 102 / 118, 16384 x 2048 67 / 73, 32768 x
+    // 1024 74 / 70, 32768 x 512 52 / 38.
     const int nch = chunks <= 960 ? 2 : 4, threads = (int)align_up((size_t)cdiv(chunks, nch), 32);
-    if (chunks > 512 && threads <= 480 && slots >= 2)
+    const int ctas = std::max(1, 65536 / 64 / (threads + 32));       // an SM's registers hold
+    const int slots = std::min(kNormSlots, kNormRings / ctas / (p.H * (int)sizeof(R)));
+    // And for few tokens, a CTA each and all of them at once or nearly: 1 x 7168 top-6 4.8 us with
+    // plain loads, 5.7 with the ring; 152: 5.2 / 5.9; 304: 9.5 / 7.7; 912 x 4096: 11.1 / 12.2; 1216:
+    // 18.1 / 17.6.
+    const int at_once = std::max(1, 65536 / 40 / (int)align_up((size_t)chunks, 32));
+    const bool few = p.M <= sm_count() * (2 * at_once - 1);
+    if (!few && chunks >= (p.slot_of != nullptr ? 128 : 192) && threads <= 480 && slots >= 2)
       return nch == 2 ? launch_stream<T, R, 2, 480, 2>(p, threads, slots, st)
                       : launch_stream<T, R, 4, 480, 1>(p, threads, slots, st);
   }

@@ -535,6 +535,12 @@ def test_norm_many_tokens(moe, H, res):
 
 
 @gpu
+@pytest.mark.parametrize("M,H,k,res", [(800, 4096, 2, "same"), (1700, 2048, 1, "f32"), (3600, 1032, 2, "same"), (2500, 1544, 0, "f32")])
+def test_norm_many_short_tokens(moe, M, H, k, res):
+    check_norm(moe, M, H, k=k, res=res, kind="layer" if k == 1 else "rms", shared=k == 2)
+
+
+@gpu
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_norm_before_a_block_only(moe, kind):
     residual = torch.randn(7, 640, device="cuda")
