@@ -471,7 +471,7 @@ typedef struct {
   float eps, scale, weight_offset;
   const void* residual;
   long long ld_residual;
-  const void* rows;
+  const void* rows;             /* not NULL with slot_of, also where n_rows is 0 */
   long long ld_rows;
   const int32_t* slot_of;       /* [M, topk] or NULL */
   const float* topk_weights;    /* [M, topk], with slot_of */

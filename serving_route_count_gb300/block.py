@@ -258,6 +258,8 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
         slot_p = _whole(slot_of, "slot_of", torch.int32, M * topk)
         weights_p = _whole(topk_weights, "topk_weights", torch.float32, M * topk)
         rows_p, ld_rows = _rows(rows, "rows", None, H)
+        if n_rows == 0:
+            rows_p = residual_p        # an empty tensor has no address; no slot reaches it
         if shared is not None:
             shared_p, ld_shared = _rows(shared, "shared", M, H, dtype)
     elif topk_weights is not None or shared is not None:

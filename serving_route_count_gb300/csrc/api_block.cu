@@ -145,6 +145,7 @@ moe_status moe_block_norm(const moe_norm_args* a, void* stream) {
   if (a->weight_dtype != a->dtype && a->weight_dtype != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
   if (a->kind != MOE_NORM_RMS && a->kind != MOE_NORM_LAYER) return MOE_ERR_ARG;
   if (!(a->eps >= 0.f) || std::isinf(a->eps)) return MOE_ERR_ARG;
+  if (a->M == 0) return MOE_OK;           // addresses of nothing say nothing
   if (a->gate != nullptr && a->gate_col != 0 && a->gate_col != 1) return MOE_ERR_ARG;
   if (a->rows == nullptr &&
       (a->slot_of || a->shared || a->post_weight || a->gate || a->residual_out))
@@ -155,7 +156,6 @@ moe_status moe_block_norm(const moe_norm_args* a, void* stream) {
   if ((a->post_bias && !a->post_weight) || (a->pre_bias && !a->pre_weight)) return MOE_ERR_ARG;
   if (a->residual_out == nullptr && a->pre_weight == nullptr) return MOE_ERR_ARG;
   if ((a->pre_weight != nullptr) != (a->out != nullptr)) return MOE_ERR_ARG;
-  if (a->M == 0) return MOE_OK;
   if (a->residual == nullptr) return MOE_ERR_ARG;
   const long long H = a->H;
   if (a->ld_residual < H || (a->rows && a->ld_rows < H) || (a->shared && a->ld_shared < H) ||

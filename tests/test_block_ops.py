@@ -662,6 +662,11 @@ def test_refusals_of_the_norm(lib):
     assert lib.moe_block_norm(None, None) == 1
     assert lib.moe_block_norm_get_device_error(None, None) == 1
     assert norm(M=0) == 0
+    # the addresses of tensors without a row are 0
+    gone = dict(M=0, residual=None, rows=None, residual_out=None, out=None)
+    assert norm(**gone) == 0 and norm(**gone, post_weight=p, gate=p, gate_col=1) == 0
+    assert norm(**gone, slot_of=None, topk_weights=None, topk=2, shared=None) == 0
+    assert norm(M=0, kind=2) == 1 and norm(M=0, H=0) == 2 and norm(M=0, dtype=2) == 3
     assert norm(H=0) == 2 and norm(H=32769) == 2
     assert norm(dtype=2) == 3 and norm(residual_dtype=1) == 3 and norm(weight_dtype=1) == 3
     for bad in ({"M": -1}, {"kind": 2}, {"eps": -1.0}, {"eps": float("nan")}, {"eps": float("inf")}, {"residual": None}, {"rows": None},
@@ -670,6 +675,36 @@ def test_refusals_of_the_norm(lib):
                 {"pre_weight": None, "out": None, "residual_out": None}, {"ld_residual": 15}, {"ld_rows": 15}, {"ld_residual_out": 15},
                 {"ld_out": 15}, {"gate": p, "gate_col": 2}):
         assert norm(**bad) == 1, bad
+
+
+@gpu
+@pytest.mark.parametrize("combine", [False, True])
+def test_a_block_without_tokens(moe, combine):
+    H, dt = 64, torch.bfloat16
+    none = lambda *shape, dtype=dt: torch.empty(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    ids, wt = moe.moe_router(none(0, 8), 2)
+    offsets, perm, slot_of = moe.moe_group(ids, 8)
+    assert offsets.tolist() == [0] * 9 and perm.numel() == 0 and slot_of.shape == (0, 2)
+    y = moe.MoEGrouped(8, H, H, max_rows=0)(none(0, H), none(8, H, H), offsets, perm=perm, topk=2)
+    args = dict(slot_of=slot_of, topk_weights=wt, shared=none(0, H)) if combine else {}
+    w = torch.ones(H, dtype=dt, device="cuda")
+    r, o = moe.moe_block_norm(none(0, H), y, post_weight=w, gate=none(0, 1), pre_weight=w, **args)
+    assert y.shape == r.shape == o.shape == (0, H)
+
+
+@gpu
+@pytest.mark.parametrize("M,H,shared", [(3, 64, False), (3, 64, True), (2, 1536, True), (2, 33, True), (700, 2048, False)])
+def test_norm_of_a_rank_without_expert_rows(moe, M, H, shared):
+    """No slot of any token here, and rows without a row: the sum is the shared row, or zero."""
+    g = torch.Generator().manual_seed(M)
+    dt = torch.bfloat16
+    res, sh = (torch.randn(M, H, generator=g).to(dt).cuda() for _ in range(2))
+    w = torch.ones(H, dtype=dt, device="cuda")
+    slot_of = torch.full((M, 2), -1, dtype=torch.int32, device="cuda")
+    r, o = moe.moe_block_norm(res, res[:0], slot_of=slot_of, topk_weights=torch.full((M, 2), float("nan"), device="cuda"),
+                              shared=sh if shared else None, pre_weight=w)
+    r0, o0 = moe.moe_block_norm(res, sh if shared else torch.zeros_like(sh), pre_weight=w)
+    assert torch.equal(r, r0) and torch.equal(o, o0)
 
 
 @gpu
