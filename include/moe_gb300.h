@@ -428,7 +428,8 @@ moe_status moe_grouped_scratch_bytes(const moe_grouped_t* plan, size_t* bytes);
 /* One product.
  *   scratch  its first 4096 bytes zero-filled by the caller once, before the first use; every call
  *            leaves them ready for the next.  Calls that share a scratch buffer must be
- *            stream-ordered.  After a device error (below) those bytes have to be zero-filled again.
+ *            stream-ordered.  After a device error (below) those bytes have to be zero-filled again, which
+ *            moe_grouped_get_device_error does.
  *   x        [x_rows, K], row stride ldx;  w [E, N, K] with row stride ldw and expert stride
  *            ldw * N;  out [S, N or N / 2], row stride ldo;  offsets [E + 1] and perm [S] as
  *            moe_group writes them (perm entries outside [0, x_rows * topk) set the device error
@@ -442,8 +443,8 @@ moe_status moe_grouped_run(const moe_grouped_t* plan, void* scratch, size_t scra
                            const void* x, long long ldx, int x_rows, const void* w, long long ldw,
                            const int32_t* offsets, const int32_t* perm, int topk, void* out,
                            long long ldo, int S, void* stream);
-/* Reads and clears the device error word in `scratch` (synchronises `stream`): *code as
- * moe_get_device_error. */
+/* Reads the device error word in `scratch` and makes the buffer ready for the next call
+ * (synchronises `stream`): *code as moe_get_device_error. */
 moe_status moe_grouped_get_device_error(const moe_grouped_t* plan, void* scratch, void* stream,
                                         int* code);
 void moe_destroy_grouped(moe_grouped_t* plan);

@@ -129,7 +129,8 @@ moe_status moe_grouped_get_device_error(const moe_grouped_t* plan, void* scratch
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t word = 0;
   cudaError_t e = cudaMemcpyAsync(&word, scratch, sizeof(word), cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(scratch, 0, sizeof(word), st);
+  // with the word the tickets, which a call that gave up may have left anywhere
+  if (e == cudaSuccess) e = cudaMemsetAsync(scratch, 0, kGtPartAt, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return status(e);
   *code = word;

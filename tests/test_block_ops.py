@@ -678,6 +678,19 @@ def test_refusals_of_the_norm(lib):
 
 
 @gpu
+def test_reading_the_error_word_readies_the_scratch(moe):
+    """A unit cut along K counts its pieces in the buffer's first 4096 bytes; whatever is left there is cleared."""
+    x, w = (torch.randn(*s, device="cuda").bfloat16() for s in ((3, 4096), (1, 512, 4096)))
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    op = moe.MoEGrouped(1, 512, 4096, max_rows=3)
+    want = op(x, w, off).clone()
+    op.scratch[:4096] = 1
+    status, code = op.device_error()
+    assert status != 0 and code == 0x01010101
+    assert op.device_error() == (0, 0) and torch.equal(op(x, w, off), want)
+
+
+@gpu
 @pytest.mark.parametrize("combine", [False, True])
 def test_a_block_without_tokens(moe, combine):
     H, dt = 64, torch.bfloat16
