@@ -44,6 +44,7 @@ constexpr int kGtThreads = 512;
 constexpr int kGtTokenWarps = 6;         // warps 2-7
 constexpr int kGtK = 64;                 // K step: one 128-byte swizzled row per operand row
 constexpr int kGtMinSteps = 4;           // K steps below which a piece is not cut further
+constexpr int kGtSortSteps = 56;         // K steps from which tiles are ordered by size (below)
 
 template <int BN, int ACC>
 struct GtCfg {
@@ -52,7 +53,8 @@ struct GtCfg {
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;     // tokens per tile copy
   static constexpr int kBytesW = 128 * 128;                  // weight rows of one accumulator
   static constexpr int kBytesA = kAcc * kBytesW, kBytesB = kHalf * 128, kStage = kBytesA + kBytesB;
-  static constexpr int kTables = 3 * 1028 * 4 + 512;         // expert tables, barriers
+  static constexpr bool kSorts = BN == 256;                  // tiles ordered by size
+  static constexpr int kTables = (kSorts ? 4 : 3) * 1028 * 4 + 512;   // expert tables, barriers
   static constexpr int kStages = (227 * 1024 - 1024 - kTables) / kStage > 12
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
   static constexpr int kSmem = 1024 + kStages * kStage + kTables;
@@ -74,19 +76,23 @@ struct GtParams {
 };
 
 // Units of one pair: first its range of the leftover units' K steps, then its whole units, round
-// robin.  A unit is a token tile and a weight row block of it.  Numbers: the blocks of a tile
+// robin (sorted: to and fro).  A unit is a token tile and a weight row block of it.  Numbers: the blocks of a tile
 // adjacent (they share its tokens), and where the last block has only one of two accumulators
 // (half the work) those of all tiles at the end, so that the last wave consists of them.
 struct GtWork {
   int KT, RB, G, Gs, D, first;     // RB: blocks with all accumulators; first: units before it are whole
   uint32_t W, x, x1;               // leftover steps, this pair's range of them
-  int full, u;                     // units of whole blocks; next whole unit
+  int full, w;                     // units of whole blocks; next wave
+  int at, back;                    // this pair's place in even and in odd waves
   __device__ __forceinline__ void init(int tiles, int kt, int rbs, int half, int g, int cta,
-                                       int fix_steps) {
+                                       int fix_steps, bool sorted) {
     KT = kt; RB = rbs; G = g;
     full = tiles * rbs;
     const int units = full + (half ? tiles : 0);
     D = units / g;
+    w = 0;
+    at = cta;
+    back = sorted ? g - 1 - cta : cta;
     first = D * g;
     const uint32_t R = (uint32_t)(units - first);
     W = R * (uint32_t)kt;
@@ -94,7 +100,7 @@ struct GtWork {
     // costs (both in K steps)
     if (kt - (int)(W / (uint32_t)g) <= fix_steps) {
       first = units;
-      D += cta < (int)R;
+      D += ((D & 1) ? back : at) < (int)R;
       W = 0;
     }
     // pairs that share the leftover steps: all of them, unless the pieces got too short
@@ -102,7 +108,6 @@ struct GtWork {
     Gs = most < (uint32_t)g ? (int)most : g;
     x = W && cta < Gs ? begin_of(cta) : 0u;
     x1 = W && cta < Gs ? begin_of(cta + 1) : 0u;
-    u = cta;
   }
   __device__ __forceinline__ uint32_t begin_of(int cta) const {
     return (uint32_t)cta * W / (uint32_t)Gs;
@@ -125,10 +130,10 @@ struct GtWork {
       x += (uint32_t)len;
     } else if (D > 0) {
       --D;
-      unit = u;
+      unit = w * G + ((w & 1) ? back : at);
+      ++w;
       k0 = 0;
       len = KT;
-      u += G;
     } else {
       return false;
     }
@@ -149,23 +154,28 @@ struct GtWork {
   }
 };
 
-// A tile's expert and token range (by a whole warp).  s_tile[e]: tiles before expert e, 1024
-// entries; the expert is the last one with s_tile[e] <= tile, found by two 32-way comparisons.
+// A tile's expert and token range (by a whole warp).  s_tile[i]: tiles before the
+// tables' expert i, 1024 entries; the tile's is the last one with s_tile[i] <= tile, found by two
+// 32-way comparisons.  s_expert: the experts' numbers (BN = 256; else the tables are in their order).
 struct GtTile {
   int e, p0, n, nhalf;
 };
+// An expert's tokens go in tiles of one size, a multiple of 16 (256 + 24 rows would cost a tile of
+// 24 that streams as many weights as one of 256).
+template <int BN>
+__device__ __forceinline__ int gt_size(int cnt, int tiles) {
+  return tiles > 1 ? 16 * cdiv(cdiv(cnt, tiles), 16) : BN;
+}
 template <int BN>
 __device__ __forceinline__ GtTile gt_tile(int tile, const int* s_tile, const int* s_off,
-                                          const int* s_cnt, int lane) {
+                                          const int* s_cnt, const int* s_expert, int lane) {
   const int hi = __popc(__ballot_sync(0xffffffffu, s_tile[32 * lane] <= tile)) - 1;
   const int lo = __popc(__ballot_sync(0xffffffffu, s_tile[32 * hi + lane] <= tile)) - 1;
   GtTile r;
-  r.e = 32 * hi + lo;
-  // an expert's tokens in tiles of one size, a multiple of 16 (256 + 24 rows would cost a tile of 24
-  // that streams as many weights as one of 256)
-  const int t = tile - s_tile[r.e], cnt = s_cnt[r.e], tiles = cdiv(cnt, BN);
-  const int size = tiles > 1 ? 16 * cdiv(cdiv(cnt, tiles), 16) : BN;
-  r.p0 = s_off[r.e] + t * size;
+  const int i = 32 * hi + lo;
+  r.e = BN == 256 ? s_expert[i] : i;
+  const int t = tile - s_tile[i], cnt = s_cnt[i], size = gt_size<BN>(cnt, cdiv(cnt, BN));
+  r.p0 = s_off[i] + t * size;
   r.n = min(size, cnt - t * size);
   r.nhalf = 8 * cdiv(r.n, 16);
   return r;
@@ -261,6 +271,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   int* s_off = reinterpret_cast<int*>(st + S * Cfg::kStage + 512);
   int* s_cnt = s_off + 1028;
   int* s_tile = s_cnt + 1028;
+  int* s_expert = s_tile + 1028;       // where tiles are ordered by size
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, G = gridDim.x >> 1;
@@ -293,7 +304,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
 
   // the experts' tiles: thread t owns experts 4 t .. 4 t + 3.  Offsets that are out of order or range
   // make the call empty (every CTA sees the same ones), so that no tile is ever out of its bounds.
-  int cnt[4], tiles = 0, bad = 0;
+  int cnt[4], bad = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = 4 * tid + i;
@@ -306,27 +317,70 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
         cnt[i] = b - a;
       s_off[e] = a;
       s_cnt[e] = cnt[i];
+      if (Cfg::kSorts) s_expert[e] = e;
     }
     if (e >= E && e < 1024) s_tile[e] = 0x7FFFFFFF;
-    tiles += cdiv(cnt[i], BN);
   }
-  int incl = tiles;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_warp[warp] = incl;
   bad = __syncthreads_or(bad);
-  int before = incl - tiles, total = 0;
+  // numbers the tiles in the tables' order; their total
+  const auto number = [&]() {
+    int tiles = 0;
 #pragma unroll
-  for (int w = 0; w < kGtThreads / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
+    for (int i = 0; i < 4; ++i) tiles += cdiv(cnt[i], BN);
+    int incl = tiles;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int before = incl - tiles, total = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (4 * tid + i < E) s_tile[4 * tid + i] = before;
-    before += cdiv(cnt[i], BN);
+    for (int w = 0; w < kGtThreads / 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * tid + i < E) s_tile[4 * tid + i] = before;
+      before += cdiv(cnt[i], BN);
+    }
+    return total;
+  };
+  int total = number();
+  bool sorted = false;
+  if constexpr (Cfg::kSorts) {
+    // More units than pairs, and long ones: the experts in descending order of their tiles' size, and
+    // every other wave in reverse, so that a wave's units are alike, the pairs' sums of them too, and
+    // the last ones the smallest.  us without / with: 100 experts of 164 rows, K = 5120 436 / 384;
+    // 384 of 128, skewed, K = 7168 1348 / 1255; 8 of 1500, K = 4096 280 / 270, 3584 243 / 238; 16 of
+    // 1536, K = 7168 485 / 473; 256 of 128 alike, K = 6144 536 / 543.  At K = 2560 and less the
+    // epilogues weigh more, and pairs out of step overlap them better: 32 of 768, K = 2560 235 / 237;
+    // 16 of 1536, K = 2048 466 / 475, 1152 284 / 288.
+    if (!bad && E > 1 && E <= kGtThreads && p.KT >= kGtSortSteps && total * (p.RB + p.half) > G) {
+      int n = 0, off = 0, key = 0, at = 0;
+      if (tid < E) {
+        n = s_cnt[tid];
+        off = s_off[tid];
+        const int tiles = cdiv(n, BN);
+        key = tiles > 1 ? gt_size<BN>(n, tiles) : n;
+        s_expert[tid] = key;
+      }
+      __syncthreads();
+      if (tid < E)
+        for (int j = 0; j < E; ++j) at += s_expert[j] > key || (s_expert[j] == key && j < tid);
+      __syncthreads();
+      if (tid < E) {
+        s_cnt[at] = n;
+        s_off[at] = off;
+        s_expert[at] = tid;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cnt[i] = 4 * tid + i < E ? s_cnt[4 * tid + i] : 0;
+      total = number();
+      sorted = true;
+    }
   }
   if (bad) {
     total = 0;
@@ -344,7 +398,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   // Every loop below is taken by whole warps; one lane issues.
   constexpr int kRows = ACT ? 64 : 128;      // output columns of one CTA and accumulator
   GtWork work;
-  work.init(total, p.KT, p.RB, p.half, G, pair, Cfg::kFixSteps);
+  work.init(total, p.KT, p.RB, p.half, G, pair, Cfg::kFixSteps, sorted);
   int u, tile, rb, k0, len;
   int s = 0, issued = 0;             // ring stage, stages filled
   uint32_t phase = 0;
@@ -361,7 +415,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   if (warp == 0) {
     const uint32_t bar0 = map_rank(&full[0], 0);
     while (ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
       const int accs = accs_of(rb);
       const int rows = p.c.perm != nullptr ? un.nhalf : cdiv(un.nhalf, Cfg::kChunk) * Cfg::kChunk;
       const uint32_t bytes = 2u * (accs * Cfg::kBytesW + rows * 128);
@@ -408,7 +462,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     uint32_t uses[2] = {0, 0};       // units that each accumulator buffer has held
     int seg = 0;
     while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
       const int accs = accs_of(rb);
       const int b0 = Cfg::kAcc == 2 ? 0 : seg & 1;
       for (int c = 0; ok && c < accs; ++c)
@@ -455,7 +509,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     int f[4] = {0, 0, 0, 0};
     GtTile un = {};
     const auto look_up = [&](int tile) {
-      un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
       if (p.c.perm != nullptr) {
         const int first = un.p0 + (int)rank * un.nhalf + 4 * tl;
 #pragma unroll
@@ -514,7 +568,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
     for (int seg = 0; ok && work.next(u, tile, rb, k0, len); ++seg) {
       if (Cfg::kAcc == 2 ? g >= accs_of(rb) : (seg & 1) != g) continue;
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, lane);
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
       const int acc = Cfg::kAcc == 2 ? g : 0;
       const int col0 = unit_col(rb) + acc * 2 * kRows + (int)rank * kRows;
       ok = mbar_wait_warp(&tfull[g], uses & 1, err);

@@ -291,6 +291,23 @@ def test_product_many_units(moe, counts, N, K, act):
 
 
 @gpu
+@pytest.mark.parametrize("act", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([0, 300, 70, 513, 16, 257, 0, 70, 256], 5376, 3592), ([70, 300], 9984, 3600),
+                                        ([(37 * e * e + 11) % 151 for e in range(130)], 330, 3600),
+                                        ([(53 * e + 5) % 140 for e in range(513)], 34, 3584)])
+def test_product_uneven_tiles(moe, counts, N, K, act):
+    """Long units of uneven sizes, more of them than CTA pairs, some experts without rows, some alike: the order in which
+    they are taken shows in no result."""
+    assert sum(counts) > 64 * len(counts)
+    x, w, off, perm, S = product_case(len(counts), N, K, counts, "f16", True, topk=2, pad=3, seed=N)
+    got = check_product(moe, x, w, off, perm, S, "f16", topk=2, act=act)
+    op = moe.MoEGrouped(len(counts), N, K, max_rows=S, dtype=torch.float16, act=moe.MOE_ACT_SWIGLU if act else moe.MOE_ACT_NONE)
+    for _ in range(30):
+        assert torch.equal(op(x, w, off, perm=perm, topk=2), got)
+    assert op.device_error() == (0, 0)
+
+
+@gpu
 def test_product_past_32_bits(moe):
     """A weight tensor of more than 2^31 elements, and a K of several thousand steps' length."""
     E, N, K = 5, 21504, 20480
