@@ -18,12 +18,12 @@
 // them in K order (bit-stable, nobody waits).
 //
 // Bounds and measurements (GB300, weights read once at the measured 6791 GB/s, bf16 unless stated):
-//   fc1 + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 111-115 us, HBM floor 106; of one
+//   fc1 + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 107-117 us, HBM floor 106; of one
 //   token 21.8, floor 14.8;
 //   fc2 of 16 tokens top-6, E = 384, K = 576, N = 7168: 112-117 us, floor 104 - what is left is the
 //   start (tables 2 us, first loads 2.5 us) and the last units;
 //   fc1 of 2048 tokens top-8: 495-508 us, floor 480; fc2 (K = 512, N = 6144): 275 us, floor 269;
-//   4096 tokens top-6 over 16 experts, K = 7168, N = 2304 (f16): 485-495 us, 1.66 PFLOP/s, bound by
+//   4096 tokens top-6 over 16 experts, K = 7168, N = 2304 (f16): 473-480 us, 1.7 PFLOP/s, bound by
 //   the tensor cores and their power (8192 x 8192 x 8192 in bf16: 1.93 PFLOP/s, cuBLAS 1.98).
 //
 // Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-7 token copies (tiles, or
