@@ -404,6 +404,7 @@ moe_status moe_router(const void* logits, int dtype, long long ld_logits, const 
  *   perm [M * topk]  flat slot of each position, -1 at and beyond offsets[E];
  *   slot_of [M * topk]  position of each flat slot, -1 for ids outside
  *                       [first_expert, first_expert + E), which are dropped.
+ * M == 0 writes the offsets (zeros) alone.
  * Limits: E <= 1024, M * topk <= 2^30.  Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_CUDA. */
 moe_status moe_group(const int32_t* topk_ids, int M, int topk, int E, int first_expert,
                      int32_t* offsets, int32_t* perm, int32_t* slot_of, void* stream);

@@ -1,0 +1,34 @@
+// block_launch.cuh - launch shapes of the 16-bit block's kernels: host arithmetic alone, without
+// CUDA, so that it can be checked on any host.
+#pragma once
+
+#include <algorithm>
+
+namespace moe {
+
+inline int ceil_to(int v, int a) { return (v + a - 1) / a * a; }
+
+// ---------------------------------------------------------------------------------- group
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWarps = kGroupThreads / 32;
+
+// CTAs of the cluster, slots of each CTA and of each warp (multiples of 32), warps that own slots
+// (at least one, also of a call without slots, which still writes the offsets).
+struct GroupShape {
+  int ctas, per_cta, per_warp, warps;
+};
+
+// widest: the largest cluster the device can hold (8 or 16).
+// Few slots: the cluster's barriers cost more than they share out (1 / 4 / 8 / 16 CTAs at 256
+// experts: 96 slots 3.0 / 3.1 / 3.6 us; 512: 3.8 / 3.5 / 3.7; 2048: 6.6 / 4.1 / 4.1 / 4.4; 8192:
+// 12.7 / 6.8 / 5.5 / 5.1; 16384: 21.9 / 8.5 / 7.1 / 6.3).
+inline GroupShape group_shape(int S, int widest) {
+  GroupShape g;
+  g.ctas = S <= 256 ? 1 : (S <= 1024 ? 4 : (S <= 8192 ? 8 : widest));
+  g.per_cta = std::max(32, ceil_to((S + g.ctas - 1) / g.ctas, 32));
+  g.per_warp = ceil_to((g.per_cta + kGroupWarps - 1) / kGroupWarps, 32);
+  g.warps = (g.per_cta + g.per_warp - 1) / g.per_warp;
+  return g;
+}
+
+}  // namespace moe

@@ -4,6 +4,7 @@
 
 #include <cmath>
 
+#include "block_launch.cuh"
 #include "block_ops.cuh"
 #include "../../include/moe_gb300.h"
 
@@ -257,8 +258,6 @@ cudaError_t launch_router(const void* logits, int dtype, long long ld, const flo
 // their ranges again, ranking equal experts of 32 slots by a warp match.  Bound by the second walk
 // (the 4-byte stores of perm in expert order) per CTA: 8192 tokens top-8 over 256 experts take 77 /
 // 40 / 22 / 13 / 9.6 us on 1 / 2 / 4 / 8 / 16 CTAs; 16 tokens top-6 3.3 us.
-constexpr int kGroupThreads = 1024;
-constexpr int kGroupWarps = kGroupThreads / 32;
 constexpr int kGroupMaxExperts = 1024;
 
 inline size_t group_smem(int warps, int E) { return (size_t)(warps + 3) * E * sizeof(int); }
@@ -385,30 +384,24 @@ cudaError_t launch_group(const int32_t* ids, int S, int E, int first, int32_t* o
     (void)cudaGetLastError();
     attr = true;
   }
-  // Few slots: the cluster's barriers cost more than they share out (1 / 4 / 8 / 16 CTAs at 256
-  // experts: 96 slots 3.0 / 3.1 / 3.6 us; 512: 3.8 / 3.5 / 3.7; 2048: 6.6 / 4.1 / 4.1 / 4.4; 8192:
-  // 12.7 / 6.8 / 5.5 / 5.1; 16384: 21.9 / 8.5 / 7.1 / 6.3).
-  const int C = S <= 256 ? 1 : (S <= 1024 ? 4 : (S <= 8192 ? 8 : widest));
-  const int per_cta = (int)align_up((size_t)cdiv(S, C), 32);
-  const int per_warp = (int)align_up((size_t)cdiv(per_cta, kGroupWarps), 32);
-  const int warps = cdiv(per_cta, per_warp);
-  const size_t smem = group_smem(warps, E);
+  const GroupShape g = group_shape(S, widest);
+  const size_t smem = group_smem(g.warps, E);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C);
+  cfg.gridDim = dim3(g.ctas);
   cfg.blockDim = dim3(kGroupThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.x = g.ctas;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, group_kernel, ids, S, E, first, per_cta, per_warp, warps, offsets,
-                            perm, slot_of);
+  return cudaLaunchKernelEx(&cfg, group_kernel, ids, S, E, first, g.per_cta, g.per_warp, g.warps,
+                            offsets, perm, slot_of);
 }
 
 }  // namespace moe
