@@ -19,15 +19,18 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 }
 
 // Clamped SwiGLU in fp32: g' * sigmoid(alpha g') * (u' + beta), g' = min(g, limit),
-// u' = clamp(u, -limit, limit).  __expf and __fdividef (2 + 1.2 |alpha g'| and 2 ulp) are far below
-// the rounding of the 16-bit result; with expf and an IEEE division the product's epilogue took 9 %
-// of a tensor-bound call.
+// u' = clamp(u, -limit, limit).  sigmoid(a) = 1 / (1 + e) or e / (1 + e), e = exp(-|a|): the divisor
+// stays within [1, 2], where __fdividef is within 2 ulp (above 2^126 it returns 0, which lost every
+// gate of a in -88.7 .. -87.3, values that bf16 can hold).  With __expf (2 + 1.2 |a| ulp) that is far
+// below the rounding of the 16-bit result; with expf and an IEEE division the product's epilogue
+// took 9 % of a tensor-bound call.
 __device__ __forceinline__ float swiglu_f32(float u, float g, float limit, float alpha,
                                             float beta) {
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(limit));      // NaN stays NaN
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(u) : "f"(limit));
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(u) : "f"(-limit));
-  return __fdividef(g, 1.0f + __expf(-alpha * g)) * (u + beta);
+  const float a = alpha * g, e = __expf(-fabsf(a));
+  return __fdividef(a < 0.f ? g * e : g, 1.0f + e) * (u + beta);
 }
 
 }  // namespace moe

@@ -1,0 +1,51 @@
+"""Calls of the 16-bit block's operators at the edges of their ranges, against the formulas in 64 bits."""
+import numpy as np
+import pytest
+
+from oracle import block as B
+
+torch = pytest.importorskip("torch")
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from serving_route_count_gb300 import build
+    build.build()
+    import serving_route_count_gb300 as m
+    return m
+
+
+# ------------------------------------------------------------------------------------ products
+
+@gpu
+@pytest.mark.parametrize("K", [8, 7])                           # tensor cores, CUDA cores
+@pytest.mark.parametrize("alpha", [1.0, 1.702, -1.0])
+def test_swiglu_of_large_gates(moe, K, alpha):
+    """Gates whose sigmoid is near the end of fp32's range, and of bf16's.  x = (1, 0, ..), so the products are the
+    weights' first column, exactly; |u| = 3."""
+    g = np.concatenate([np.arange(-128, -40, 0.5), np.arange(40, 128, 0.5), [0.0, -0.0, -1e30, 1e30, -np.inf, np.inf]])
+    g = torch.from_numpy(g).bfloat16().double().numpy()
+    n = g.size
+    u = np.where(np.arange(n) % 2, 3.0, -3.0)
+    w = torch.zeros((1, 2 * n, K), dtype=torch.bfloat16)
+    w[0, :n, 0], w[0, n:, 0] = torch.from_numpy(u).bfloat16(), torch.from_numpy(g).bfloat16()
+    x = torch.zeros((1, K), dtype=torch.bfloat16)
+    x[0, 0] = 1
+    off = torch.tensor([0, 1], dtype=torch.int32)
+    finite = np.isfinite(g)                                     # 0 * inf of the row's other columns stays out: they are 0 * 0
+    op = moe.MoEGrouped(1, 2 * n, K, max_rows=1, act=moe.MOE_ACT_SWIGLU, alpha=alpha)
+    got = op(x.cuda(), w.cuda(), off.cuda()).double().cpu().numpy()[0]
+    assert op.device_error() == (0, 0)
+    with np.errstate(invalid="ignore", over="ignore"):
+        a = np.abs(np.float64(np.float32(alpha)) * g)
+        ref = B.swiglu(u, g, np.inf, np.float64(np.float32(alpha)))
+        # exp: 2 + 1.173 |a| ulp of 2^-23, its argument's rounding |a| 2^-24, four operations; its last place where it is below
+        # fp32's normal range; then the rounding to bf16, in units of 2^-133 below its normal range
+        tol = np.abs(ref) * (2.0 ** -8 + (4 + 1.7 * a) * 2.0 ** -23) + np.abs(g * u) * 2.0 ** -149 + 2.0 ** -134
+        near = np.abs(got - ref) <= tol
+    assert np.all(near[finite]), (g[finite & ~near], got[finite & ~near])
+    same = (got == ref) | (np.isnan(got) & np.isnan(ref))
+    assert np.all(same[~finite])
