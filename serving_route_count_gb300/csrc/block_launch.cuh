@@ -31,4 +31,19 @@ inline GroupShape group_shape(int S, int widest) {
   return g;
 }
 
+// ---------------------------------------------------------------------------------- products
+// On the CUDA cores: tiles of 64 positions of one expert (at most one partial one per expert that
+// has a position) in x, tiles of 64 output columns in y, as far as a launch counts there: a CTA
+// takes every y-th of them.
+constexpr int kGsTile = 64;
+
+struct GsGrid {
+  unsigned x, y;
+};
+
+inline GsGrid grouped_simt_grid(int S, int E, int cols) {
+  return {(unsigned)((S + kGsTile - 1) / kGsTile) + (unsigned)std::min(E, S),
+          (unsigned)std::min((cols + kGsTile - 1) / kGsTile, 65535)};
+}
+
 }  // namespace moe

@@ -5,14 +5,15 @@
 // One CTA of 256 threads per tile of 64 positions of one expert x 64 output columns; a thread
 // owns 4 x 4 sums in fp32 (two sets for a SwiGLU: up and gate), operands pass through shared
 // memory 16 K at a time.  Bound by the fp32 FMA rate and the scalar operand loads: fc1 + SwiGLU of
-// 2048 tokens top-8 (E = 256, K = 6144, N = 1024) takes 10.3 ms here, 0.5 ms on the tensor cores.
+// 2048 tokens top-8 (E = 256, K = 6144, N = 1024) takes 9.9 ms here, 0.5 ms on the tensor cores.
+#include "block_launch.cuh"
 #include "block_ops.cuh"
 #include "grouped.cuh"
 #include "../../include/moe_gb300.h"
 
 namespace moe {
 
-constexpr int kGsTile = 64, kGsK = 16, kGsThreads = 256;
+constexpr int kGsK = 16, kGsThreads = 256;
 
 struct GsParams {
   GroupedDims d;
@@ -66,14 +67,15 @@ grouped_simt_kernel(const GsParams p) {
     if (tid == 0) s_tile[3] = max(0, min(S, p.c.offsets[E]));
   }
   __syncthreads();
-  const int c0 = blockIdx.y * kGsTile;
   T* out = static_cast<T*>(p.c.out);
+  const int c_first = blockIdx.y * kGsTile, c_step = gridDim.y * kGsTile;
   // rows past the last group: this CTA's share of them
-  for (int i = tid; i < kGsTile * kGsTile; i += kGsThreads) {
-    const long long r = (long long)s_tile[3] + (long long)blockIdx.x * kGsTile + i / kGsTile;
-    const int col = c0 + i % kGsTile;
-    if (r < S && col < p.cols) out[r * p.c.ldo + col] = from_f32<T>(0.f);
-  }
+  for (int c0 = c_first; c0 < p.cols; c0 += c_step)
+    for (int i = tid; i < kGsTile * kGsTile; i += kGsThreads) {
+      const long long r = (long long)s_tile[3] + (long long)blockIdx.x * kGsTile + i / kGsTile;
+      const int col = c0 + i % kGsTile;
+      if (r < S && col < p.cols) out[r * p.c.ldo + col] = from_f32<T>(0.f);
+    }
   const int e = s_tile[0];
   if (e < 0) return;
   const int p0 = s_tile[1], n = s_tile[2];
@@ -93,56 +95,57 @@ grouped_simt_kernel(const GsParams p) {
   const int K = p.d.K, half = p.d.N / 2;
   const T* x = static_cast<const T*>(p.c.x);
   const T* w = static_cast<const T*>(p.c.w) + (size_t)e * p.d.N * p.c.ldw;
-  float acc[ACT ? 2 : 1][4][4] = {};
   const int tr = tid / 16, tc = tid % 16;       // 4 positions x 4 columns of this thread
-  for (int k0 = 0; k0 < K; k0 += kGsK) {
-    for (int i = tid; i < kGsTile * kGsK; i += kGsThreads) {
-      const int r = i / kGsK, k = i % kGsK;
-      sx[k][r] = k0 + k < K ? to_f32(x[s_row[r] * p.c.ldx + k0 + k]) : 0.f;
+  for (int c0 = c_first; c0 < p.cols; c0 += c_step) {
+    float acc[ACT ? 2 : 1][4][4] = {};
+    for (int k0 = 0; k0 < K; k0 += kGsK) {
+      for (int i = tid; i < kGsTile * kGsK; i += kGsThreads) {
+        const int r = i / kGsK, k = i % kGsK;
+        sx[k][r] = k0 + k < K ? to_f32(x[s_row[r] * p.c.ldx + k0 + k]) : 0.f;
 #pragma unroll
-      for (int h = 0; h < (ACT ? 2 : 1); ++h)
-        sw[h][k][r] = (k0 + k < K && c0 + r < p.cols)
-                          ? to_f32(w[(size_t)(c0 + r + h * half) * p.c.ldw + k0 + k]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kGsK; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(&sx[k][4 * tr]);
-      const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int h = 0; h < (ACT ? 2 : 1); ++h) {
-        const float4 b = *reinterpret_cast<const float4*>(&sw[h][k][4 * tc]);
-        const float bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(av[i], bv[j], acc[h][i][j]);
+        for (int h = 0; h < (ACT ? 2 : 1); ++h)
+          sw[h][k][r] = (k0 + k < K && c0 + r < p.cols)
+                            ? to_f32(w[(size_t)(c0 + r + h * half) * p.c.ldw + k0 + k]) : 0.f;
       }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kGsK; ++k) {
+        const float4 a = *reinterpret_cast<const float4*>(&sx[k][4 * tr]);
+        const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int h = 0; h < (ACT ? 2 : 1); ++h) {
+          const float4 b = *reinterpret_cast<const float4*>(&sw[h][k][4 * tc]);
+          const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(av[i], bv[j], acc[h][i][j]);
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 4 * tr + i, col = c0 + 4 * tc + j;
+        if (r >= n || col >= p.cols) continue;
+        float v = acc[0][i][j];
+        if constexpr (ACT) {
+          const float u = p.d.layout == MOE_W13_UP_GATE ? acc[0][i][j] : acc[1][i][j];
+          const float g = p.d.layout == MOE_W13_UP_GATE ? acc[1][i][j] : acc[0][i][j];
+          v = swiglu_f32(u, g, p.d.limit, p.d.alpha, p.d.beta);
+        }
+        out[(size_t)(p0 + r) * p.c.ldo + col] = from_f32<T>(v);
+      }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = 4 * tr + i, col = c0 + 4 * tc + j;
-      if (r >= n || col >= p.cols) continue;
-      float v = acc[0][i][j];
-      if constexpr (ACT) {
-        const float u = p.d.layout == MOE_W13_UP_GATE ? acc[0][i][j] : acc[1][i][j];
-        const float g = p.d.layout == MOE_W13_UP_GATE ? acc[1][i][j] : acc[0][i][j];
-        v = swiglu_f32(u, g, p.d.limit, p.d.alpha, p.d.beta);
-      }
-      out[(size_t)(p0 + r) * p.c.ldo + col] = from_f32<T>(v);
-    }
 }
 
 cudaError_t launch_grouped_simt(const GroupedDims& d, const GroupedCall& c, cudaStream_t st) {
   GsParams p{d, c, grouped_cols(d)};
-  const long long tiles = cdiv(c.S, kGsTile) + (long long)(d.E < c.S ? d.E : c.S);
-  const dim3 grid((unsigned)tiles, cdiv(p.cols, kGsTile));
+  const GsGrid g = grouped_simt_grid(c.S, d.E, p.cols);
   auto go = [&](auto kernel) {
-    return launch_kernel(kernel, grid, dim3(kGsThreads), 0, st, true, p);
+    return launch_kernel(kernel, dim3(g.x, g.y), dim3(kGsThreads), 0, st, true, p);
   };
   if (d.dtype == MOE_DTYPE_F16)
     return d.act ? go(grouped_simt_kernel<__half, true>) : go(grouped_simt_kernel<__half, false>);

@@ -49,3 +49,20 @@ def test_swiglu_of_large_gates(moe, K, alpha):
     assert np.all(near[finite]), (g[finite & ~near], got[finite & ~near])
     same = (got == ref) | (np.isnan(got) & np.isnan(ref))
     assert np.all(same[~finite])
+
+
+@gpu
+def test_widest_product_on_the_cuda_cores(moe):
+    """N = 2^22, the most a plan takes, with rows off 16 bytes: one column tile more than a launch counts in y.  Rows past the
+    last group are zeros here too."""
+    N, K = 1 << 22, 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((3, K), (1, N, K)))
+    out = torch.full((3, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    op = moe.MoEGrouped(1, N, K, max_rows=3)
+    op(x, w, torch.tensor([0, 2], dtype=torch.int32, device="cuda"), out=out)
+    assert op.device_error() == (0, 0)
+    ref, mag = x[:2].double() @ w[0].double().t(), x[:2].double().abs() @ w[0].double().abs().t()
+    # rounded once to bf16, from an fp32 sum of K terms
+    assert torch.all((out[:2].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2 * K * 2.0 ** -24 * mag)
+    assert torch.count_nonzero(out[2]) == 0

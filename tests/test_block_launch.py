@@ -12,6 +12,10 @@ extern "C" void group_shape(int S, int widest, int* o) {
   const moe::GroupShape g = moe::group_shape(S, widest);
   o[0] = g.ctas; o[1] = g.per_cta; o[2] = g.per_warp; o[3] = g.warps;
 }
+extern "C" void grouped_simt_grid(int S, int E, int cols, unsigned* o) {
+  const moe::GsGrid g = moe::grouped_simt_grid(S, E, cols);
+  o[0] = g.x; o[1] = g.y;
+}
 """
 
 
@@ -34,3 +38,16 @@ def test_group_shape(shapes, S, widest):
     assert per_cta > 0 and per_cta % 32 == 0 and per_warp > 0 and per_warp % 32 == 0
     assert ctas * per_cta >= S and warps * per_warp >= per_cta > (warps - 1) * per_warp     # every slot has one owner
     assert ctas * per_cta + 32 * per_warp < 1 << 31                                         # a warp's first slot is an int
+
+
+@pytest.mark.parametrize("cols", [1, 64, 65, 4194240, 4194241, 1 << 22])
+@pytest.mark.parametrize("S,E", [(1, 1), (63, 4), (65, 1024), (1 << 20, 3), (1 << 30, 1024)])
+def test_grouped_simt_grid(shapes, S, E, cols):
+    """Every size that a plan takes launches: x up to 2^31 - 1, y up to 65535, and enough of both."""
+    o = (ctypes.c_uint * 2)()
+    shapes.grouped_simt_grid(S, E, cols, o)
+    x, y = o
+    assert -(-S // 64) <= x < 1 << 31 and 1 <= y <= 65535 and y == min(65535, -(-cols // 64))
+    # the most tiles: E - 1 experts of one position, the rest in the last one
+    rest = S - (E - 1)
+    assert x >= ((E - 1) + -(-rest // 64) if rest > 0 else S)
