@@ -3,8 +3,10 @@ the slots by expert, products grouped by expert, norms around the block.
 
 Argument checks and marshalling only, like ``moe``; the computation runs in the library's CUDA
 kernels.  Matrices may have a row stride (their rows must be contiguous); everything else is
-contiguous.  Work goes to ``stream``, or to torch's current stream; tensors that are not created on
-that stream are the caller's to order and keep alive, as for any stream.
+contiguous.  A call's operands are on one device, the current one (the library launches there); a
+``ValueError`` says where they are not.  Work goes to ``stream``, or to torch's current stream;
+tensors that are not created on that stream are the caller's to order and keep alive, as for any
+stream.
 """
 from __future__ import annotations
 
@@ -28,34 +30,48 @@ MOE_NORM_LAYER = 1
 _CODE = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
 
 
-def _stream(stream, t):
-    """Stream handle; without a stream, torch's current one on t's device (its raw handle: a Stream
+_current_device = torch._C._cuda_getDevice      # without the look at lazy initialisation: operands exist
+
+
+def _stream(stream, dev):
+    """Stream handle; without a stream, torch's current one on device `dev` (its raw handle: a Stream
     object costs as much as a launch)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the operands on cuda:{dev}")
+        return stream.cuda_stream
+    return int(stream)
 
 
-def _dev(t, name, dtype=None):
-    """Address of a CUDA tensor (of `dtype`)."""
-    if not t.is_cuda:
+def _elsewhere(t, name):
+    """The error of a call whose first operand is not on the current device."""
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+
+
+def _dev(t, name, dev, dtype=None):
+    """Address of a tensor on device `dev` (of `dtype`)."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}, not on {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     return t.data_ptr()
 
 
-def _whole(t, name, dtype, numel):
-    """Address of a contiguous CUDA tensor of `numel` elements."""
+def _whole(t, name, dev, dtype, numel):
+    """Address of a contiguous tensor of `numel` elements on device `dev`."""
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {numel} elements")
-    if t.dtype != dtype or not t.is_cuda:
-        _dev(t, name, dtype)
+    if t.dtype != dtype or t.get_device() != dev:
+        _dev(t, name, dev, dtype)
     return t.data_ptr()
 
 
-def _rows(t, name, rows, cols, dtype=None):
-    """(address, row stride) of a CUDA matrix [rows, cols] whose rows are contiguous."""
+def _rows(t, name, dev, rows, cols, dtype=None):
+    """(address, row stride) of a matrix [rows, cols] on device `dev` whose rows are contiguous."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {cols}], not {list(shape)}")
@@ -65,8 +81,8 @@ def _rows(t, name, rows, cols, dtype=None):
         if (unit != 1 and cols > 1) or (step < cols and shape[0] > 1):
             raise ValueError(f"the rows of {name} must be contiguous and apart")
         step = max(step, cols)
-    if not t.is_cuda or (dtype is not None and t.dtype != dtype):
-        _dev(t, name, dtype)
+    if t.get_device() != dev or (dtype is not None and t.dtype != dtype):
+        _dev(t, name, dev, dtype)
     return t.data_ptr(), step
 
 
@@ -83,27 +99,30 @@ def moe_router(logits, topk, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk
                renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
     """Top-k experts and weights of every row of logits [M, E] (bf16, f16 or fp32): (ids int32
     [M, topk], weights fp32 [M, topk]); see moe_router in include/moe_gb300.h."""
+    dev = logits.get_device()
+    if dev < 0 or dev != _current_device():
+        _elsewhere(logits, "logits")
     M, E = logits.shape
     ld, unit = logits.stride()
     dtype = _CODE.get(logits.dtype)
-    if unit != 1 or ld < E or dtype is None or not logits.is_cuda:
-        ld, dtype = _rows(logits, "logits", M, E)[1], _code(logits, "logits")
+    if unit != 1 or ld < E or dtype is None:
+        ld, dtype = _rows(logits, "logits", dev, M, E)[1], _code(logits, "logits")
     if topk < 0:
         raise ValueError("topk must not be negative")
     # outputs made here need no checks
-    dev = logits.device
+    on = logits.device
     if ids is None:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+        ids = torch.empty((M, topk), dtype=torch.int32, device=on)
     else:
-        _whole(ids, "ids", torch.int32, M * topk)
+        _whole(ids, "ids", dev, torch.int32, M * topk)
     if weights is None:
-        weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+        weights = torch.empty((M, topk), dtype=torch.float32, device=on)
     else:
-        _whole(weights, "weights", torch.float32, M * topk)
+        _whole(weights, "weights", dev, torch.float32, M * topk)
     st = _lib.load().moe_router(
-        logits.data_ptr(), dtype, ld, None if bias is None else _whole(bias, "bias", torch.float32, E),
+        logits.data_ptr(), dtype, ld, None if bias is None else _whole(bias, "bias", dev, torch.float32, E),
         M, E, topk, score, n_group, topk_group, renormalize, scale, ids.data_ptr(), weights.data_ptr(),
-        _stream(stream, logits))
+        _stream(stream, dev))
     if st:
         _check(st, "moe_router")
     return ids, weights
@@ -114,24 +133,27 @@ def moe_router(logits, topk, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk
 def moe_group(topk_ids, E, first_expert=0, offsets=None, perm=None, slot_of=None, stream=None):
     """Slots of topk_ids [M, topk] (int32) grouped by expert: (offsets [E + 1], perm [M * topk],
     slot_of [M, topk]), all int32; see moe_group in include/moe_gb300.h."""
+    dev = topk_ids.get_device()
+    if dev < 0 or dev != _current_device():
+        _elsewhere(topk_ids, "topk_ids")
     M, topk = topk_ids.shape
     n = M * topk
-    ids_p = _whole(topk_ids, "topk_ids", torch.int32, n)
+    ids_p = _whole(topk_ids, "topk_ids", dev, torch.int32, n)
     # outputs made here need no checks
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=torch.int32, device=topk_ids.device)
     else:
-        _whole(offsets, "offsets", torch.int32, E + 1)
+        _whole(offsets, "offsets", dev, torch.int32, E + 1)
     if perm is None:
         perm = torch.empty(n, dtype=torch.int32, device=topk_ids.device)
     else:
-        _whole(perm, "perm", torch.int32, n)
+        _whole(perm, "perm", dev, torch.int32, n)
     if slot_of is None:
         slot_of = torch.empty_like(topk_ids)
     else:
-        _whole(slot_of, "slot_of", torch.int32, n)
+        _whole(slot_of, "slot_of", dev, torch.int32, n)
     st = _lib.load().moe_group(ids_p, M, topk, E, first_expert, offsets.data_ptr(), perm.data_ptr(),
-                               slot_of.data_ptr(), _stream(stream, topk_ids))
+                               slot_of.data_ptr(), _stream(stream, dev))
     if st:
         _check(st, "moe_group")
     return offsets, perm, slot_of
@@ -155,8 +177,10 @@ def moe_grouped_scratch_bytes(plan) -> int:
 def moe_grouped_get_device_error(plan, scratch, stream=None):
     """(status, code) of the device error word in `scratch`, which is cleared."""
     code = ctypes.c_int()
-    st = _lib.load().moe_grouped_get_device_error(plan, _dev(scratch, "scratch"),
-                                                  _stream(stream, scratch),
+    dev = scratch.get_device()
+    if dev < 0 or dev != _current_device():
+        _elsewhere(scratch, "scratch")
+    st = _lib.load().moe_grouped_get_device_error(plan, scratch.data_ptr(), _stream(stream, dev),
                                                   ctypes.byref(code))
     return st, code.value
 
@@ -167,8 +191,8 @@ def moe_destroy_grouped(plan):
 
 class MoEGrouped:
     """Products grouped by expert with ragged sizes, 16-bit operands: the plan of one layer's
-    matrices [E, N, K] and its scratch buffer (moe_grouped_plan, moe_grouped_run).  Calls that
-    share a MoEGrouped must be stream-ordered."""
+    matrices [E, N, K] and its scratch buffer on `device` (moe_grouped_plan, moe_grouped_run).  Calls
+    that share a MoEGrouped must be stream-ordered."""
 
     def __init__(self, E, N, K, max_rows, dtype=torch.bfloat16, act=MOE_ACT_NONE,
                  layout=MOE_W13_UP_GATE, swiglu_limit=float("inf"), alpha=1.0, beta=0.0,
@@ -183,13 +207,19 @@ class MoEGrouped:
                                    device=device)
         self.scratch[:4096].zero_()
         torch.cuda.current_stream(self.scratch.device).synchronize()   # calls may use any stream
+        self._dev = self.scratch.get_device()
         self._fixed = (self.plan, self.scratch.data_ptr(), self.scratch.numel())
 
     def __call__(self, x, w, offsets, perm=None, topk=1, out=None, stream=None):
         """out[p] = act(w[e] . x[row(p)]) for the positions p of every expert e.  offsets [E + 1]
         and perm [S] as moe_group gives them; with perm, x holds one row per token (row(p) =
         perm[p] // topk), without it one row per position."""
-        xp, ldx = _rows(x, "x", None, self.K, self.dtype)
+        dev = x.get_device()
+        if dev < 0 or dev != _current_device():
+            _elsewhere(x, "x")
+        if dev != self._dev:
+            raise ValueError(f"x is on cuda:{dev}, the scratch buffer on {self.scratch.device}")
+        xp, ldx = _rows(x, "x", dev, None, self.K, self.dtype)
         S = x.shape[0] if perm is None else perm.numel()
         if w.dim() != 3 or w.shape[0] != self.E or w.shape[1] != self.N or w.shape[2] != self.K:
             raise ValueError(f"w must be [{self.E}, {self.N}, {self.K}], not {list(w.shape)}")
@@ -198,12 +228,12 @@ class MoEGrouped:
             raise ValueError("the rows of w must be contiguous and evenly apart over all experts")
         if out is None:
             out = torch.empty((S, self.cols), dtype=self.dtype, device=x.device)
-        op, ldo = _rows(out, "out", S, self.cols, self.dtype)
+        op, ldo = _rows(out, "out", dev, S, self.cols, self.dtype)
         st = _lib.load().moe_grouped_run(
-            *self._fixed, xp, ldx, x.shape[0], _dev(w, "w", self.dtype), ldw,
-            _whole(offsets, "offsets", torch.int32, self.E + 1),
-            None if perm is None else _whole(perm, "perm", torch.int32, S), topk, op, ldo, S,
-            _stream(stream, x))
+            *self._fixed, xp, ldx, x.shape[0], _dev(w, "w", dev, self.dtype), ldw,
+            _whole(offsets, "offsets", dev, torch.int32, self.E + 1),
+            None if perm is None else _whole(perm, "perm", dev, torch.int32, S), topk, op, ldo, S,
+            _stream(stream, dev))
         if st:
             _check(st, "moe_grouped_run")
         return out
@@ -235,8 +265,11 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
     top-k combination is taken here too.  Returns (residual_out, out): residual_out None without
     rows, out None without pre_weight.  gate broadcasts over [M, H]; weights, biases and gate are
     of the rows' type or all fp32.  See moe_block_norm in include/moe_gb300.h."""
+    dev = residual.get_device()
+    if dev < 0 or dev != _current_device():
+        _elsewhere(residual, "residual")
     M, H = residual.shape
-    residual_p, ld_residual = _rows(residual, "residual", M, H)
+    residual_p, ld_residual = _rows(residual, "residual", dev, M, H)
     if rows is not None:
         dtype = rows.dtype
     elif out is not None:
@@ -255,23 +288,23 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
         if rows is None or topk_weights is None or slot_of.dim() != 2 or slot_of.shape[0] != M:
             raise ValueError("slot_of must be [M, topk], with rows and topk_weights")
         topk, n_rows = slot_of.shape[1], rows.shape[0]
-        slot_p = _whole(slot_of, "slot_of", torch.int32, M * topk)
-        weights_p = _whole(topk_weights, "topk_weights", torch.float32, M * topk)
-        rows_p, ld_rows = _rows(rows, "rows", None, H)
+        slot_p = _whole(slot_of, "slot_of", dev, torch.int32, M * topk)
+        weights_p = _whole(topk_weights, "topk_weights", dev, torch.float32, M * topk)
+        rows_p, ld_rows = _rows(rows, "rows", dev, None, H)
         if n_rows == 0:
             rows_p = residual_p        # an empty tensor has no address; no slot reaches it
         if shared is not None:
-            shared_p, ld_shared = _rows(shared, "shared", M, H, dtype)
+            shared_p, ld_shared = _rows(shared, "shared", dev, M, H, dtype)
     elif topk_weights is not None or shared is not None:
         raise ValueError("topk_weights and shared go with slot_of")
     elif rows is not None:
-        rows_p, ld_rows = _rows(rows, "rows", M, H)
+        rows_p, ld_rows = _rows(rows, "rows", dev, M, H)
     if post_weight is not None:
-        post_p = _whole(post_weight, "post_weight", wt, H)
+        post_p = _whole(post_weight, "post_weight", dev, wt, H)
     if post_bias is not None:
-        post_b = _whole(post_bias, "post_bias", wt, H)
+        post_b = _whole(post_bias, "post_bias", dev, wt, H)
     if gate is not None:
-        gate_p = _dev(gate, "gate", wt)
+        gate_p = _dev(gate, "gate", dev, wt)
         shape, step = gate.shape, gate.stride()
         if len(shape) == 1:
             shape, step = (1, shape[0]), (0, step[0])
@@ -280,18 +313,18 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
         gate_row = step[0] if shape[0] > 1 else 0
         gate_col = step[1] if shape[1] > 1 else 0
     if pre_weight is not None:
-        pre_p = _whole(pre_weight, "pre_weight", wt, H)
+        pre_p = _whole(pre_weight, "pre_weight", dev, wt, H)
         if pre_bias is not None:
-            pre_b = _whole(pre_bias, "pre_bias", wt, H)
+            pre_b = _whole(pre_bias, "pre_bias", dev, wt, H)
         if out is None:
             out = torch.empty((M, H), dtype=dtype, device=residual.device)
-        out_p, ld_out = _rows(out, "out", M, H, dtype)
+        out_p, ld_out = _rows(out, "out", dev, M, H, dtype)
     elif pre_bias is not None or out is not None:
         raise ValueError("pre_bias and out go with pre_weight")
     if rows is not None:
         if residual_out is None:
             residual_out = torch.empty((M, H), dtype=residual.dtype, device=residual.device)
-        res_out_p, ld_res_out = _rows(residual_out, "residual_out", M, H, residual.dtype)
+        res_out_p, ld_res_out = _rows(residual_out, "residual_out", dev, M, H, residual.dtype)
     elif residual_out is not None:
         raise ValueError("residual_out goes with rows")
     # moe_norm_args as the compiler lays it out
@@ -299,15 +332,16 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
         M, H, code, _code(residual, "residual"), _CODE.get(wt, -1), kind, eps, scale, weight_offset,
         residual_p, ld_residual, rows_p, ld_rows, slot_p, weights_p, topk, n_rows, shared_p, ld_shared,
         post_p, post_b, gate_p, gate_row, gate_col, pre_p, pre_b, res_out_p, ld_res_out, out_p, ld_out),
-        _stream(stream, residual))
+        _stream(stream, dev))
     if st:
         _check(st, "moe_block_norm")
     return residual_out, out
 
 
 def moe_block_norm_get_device_error(stream=None):
-    """(status, code) of the device error word of moe_block_norm's calls, which is cleared."""
+    """(status, code) of the device error word of moe_block_norm's calls on the current device, which
+    is cleared."""
     code = ctypes.c_int()
-    handle = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream, None)
-    st = _lib.load().moe_block_norm_get_device_error(handle, ctypes.byref(code))
+    st = _lib.load().moe_block_norm_get_device_error(_stream(stream, torch.cuda.current_device()),
+                                                     ctypes.byref(code))
     return st, code.value

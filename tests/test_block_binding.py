@@ -1,0 +1,110 @@
+"""The binding of the 16-bit block before it calls the library: devices of the operands.  No GPU: the tensors say that they are on one,
+and the library records its arguments."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from serving_route_count_gb300 import _lib, block  # noqa: E402
+
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+class On0(torch.Tensor):
+    at = 0
+
+    def get_device(self):
+        return self.at
+
+
+class On1(On0):
+    at = 1
+
+
+class FakeLibrary:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name != "moe_destroy_grouped":                   # of other tests' plans, collected here
+                self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    fake = FakeLibrary()
+    monkeypatch.setattr(_lib, "load", lambda: fake)
+    monkeypatch.setattr(block, "_current_device", lambda: 0)
+    return fake
+
+
+def t(shape, dtype=BF16, on=On0):
+    return torch.zeros(shape, dtype=dtype).as_subclass(on)
+
+
+def grouped(on=0):
+    op = block.MoEGrouped.__new__(block.MoEGrouped)
+    op.E, op.N, op.K, op.cols, op.dtype, op._dev = 2, 8, 16, 8, BF16, on
+    op.scratch, op.plan = t(4096, torch.uint8, On1 if on else On0), None
+    op._fixed = (1, op.scratch.data_ptr(), 4096)
+    return op
+
+
+def operands():
+    """{entry point: (its tensors by argument, other arguments)}"""
+    return {
+        block.moe_router: (dict(logits=t((4, 8), F32), bias=t(8, F32), ids=t((4, 2), I32), weights=t((4, 2), F32)),
+                           dict(topk=2, score=block.MOE_SCORE_SIGMOID)),
+        block.moe_group: (dict(topk_ids=t((4, 2), I32), offsets=t(9, I32), perm=t(8, I32), slot_of=t((4, 2), I32)), dict(E=8)),
+        grouped(): (dict(x=t((4, 16)), w=t((2, 8, 16)), offsets=t(3, I32), perm=t(8, I32), out=t((8, 8))), dict(topk=2)),
+        block.moe_block_norm: (dict(residual=t((4, 16)), rows=t((8, 16)), slot_of=t((4, 2), I32), topk_weights=t((4, 2), F32), shared=t((4, 16)),
+                                    post_weight=t(16), post_bias=t(16), gate=t((4, 1)), pre_weight=t(16), pre_bias=t(16),
+                                    residual_out=t((4, 16)), out=t((4, 16))), {}),
+    }
+
+
+def test_operands_of_one_device(lib):
+    for call, (tensors, other) in operands().items():
+        n = len(lib.calls)
+        call(**tensors, **other, stream=7)
+        assert len(lib.calls) == n + 1 and 7 in lib.calls[-1][1]
+        for name, v in tensors.items():
+            for moved in (v.as_subclass(On1), v.as_subclass(torch.Tensor)):             # another GPU; the host
+                with pytest.raises(ValueError, match=name):
+                    call(**{**tensors, name: moved}, **other, stream=7)
+        assert len(lib.calls) == n + 1
+
+
+def test_the_operands_device_is_the_current_one(lib, monkeypatch):
+    for call, (tensors, other) in operands().items():
+        if isinstance(call, block.MoEGrouped):
+            call = grouped(1)
+        elsewhere = {k: v.as_subclass(On1) for k, v in tensors.items()}
+        with pytest.raises(ValueError, match="current device"):
+            call(**elsewhere, **other, stream=7)
+        assert not lib.calls
+    monkeypatch.setattr(block, "_current_device", lambda: 1)
+    for call, (tensors, other) in operands().items():
+        if isinstance(call, block.MoEGrouped):
+            with pytest.raises(ValueError, match="scratch"):
+                call(**{k: v.as_subclass(On1) for k, v in tensors.items()}, **other, stream=7)
+            call = grouped(1)
+        call(**{k: v.as_subclass(On1) for k, v in tensors.items()}, **other, stream=7)
+    assert len(lib.calls) == 4
+    with pytest.raises(ValueError, match="current device"):
+        block.moe_grouped_get_device_error(1, t(4096, torch.uint8), stream=7)
+
+
+def test_the_stream_is_of_the_operands_device(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+
+        def __init__(self, device_index):
+            self.device_index = device_index
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    assert block._stream(Stream(0), 0) == 77 and block._stream(5, 0) == 5
+    with pytest.raises(ValueError, match="stream"):
+        block._stream(Stream(1), 0)
