@@ -3,8 +3,38 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 namespace moe {
+
+// What a kernel's first launch on a device sets or finds out there (its attributes, how many CTAs
+// fit): one value per device, from any thread.  init(&value) returns 0 or an error, which is not
+// kept; a device number past the table is asked anew every time.
+template <typename V>
+class PerDevice {
+ public:
+  template <typename Init>
+  int get(int dev, V* out, Init init) {
+    if (dev < 0 || dev >= kDevices) return init(out);
+    if (!ready_[dev].load(std::memory_order_acquire)) {
+      std::lock_guard<std::mutex> lock(mutex_);
+      if (!ready_[dev].load(std::memory_order_relaxed)) {
+        const int e = init(&value_[dev]);
+        if (e != 0) return e;
+        ready_[dev].store(true, std::memory_order_release);
+      }
+    }
+    *out = value_[dev];
+    return 0;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<bool> ready_[kDevices] = {};
+  V value_[kDevices] = {};
+  std::mutex mutex_;
+};
 
 inline int ceil_to(int v, int a) { return (v + a - 1) / a * a; }
 

@@ -458,31 +458,31 @@ norm_stream_kernel(const NormParams p, const int slots, const int slot_bytes) {
 // ---------------------------------------------------------------------------------- host side
 
 static int sm_count() {
-  static int sms = 0;
-  if (sms == 0) {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-      (void)cudaGetLastError();
-      return 152;
-    }
-    sms = n;
+  static PerDevice<int> per;
+  int n = 0;
+  if (on_device(per, &n, [](int* v) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        return e != cudaSuccess ? e : cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+      }) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return 152;
   }
-  return sms;
+  return n;
 }
 
 template <typename T, typename R, int NCH, int MAXT, int MINB>
 static cudaError_t launch_stream(const NormParams& p, int threads, int slots, cudaStream_t st) {
   const int slot_bytes = p.H * (int)sizeof(R), smem = slots * slot_bytes;
   auto kernel = norm_stream_kernel<T, R, NCH, MAXT, MINB>;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRings);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static PerDevice<bool> per;
+  bool set = false;
+  cudaError_t e = on_device(per, &set, [&](bool*) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRings);
+  });
+  if (e != cudaSuccess) return e;
   int n = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads + 32, smem);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads + 32, smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(p.M, std::max(1, n) * sm_count());
   return launch_kernel(kernel, dim3(grid), dim3(threads + 32), (size_t)smem, st, true, p, slots,

@@ -2,9 +2,18 @@
 // block reductions.
 #pragma once
 
+#include "block_launch.cuh"
 #include "moe_common.cuh"
 
 namespace moe {
+
+// PerDevice's value of the current device; init as there, with CUDA's error codes.
+template <typename V, typename Init>
+cudaError_t on_device(PerDevice<V>& per, V* out, Init init) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : static_cast<cudaError_t>(per.get(dev, out, init));
+}
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }

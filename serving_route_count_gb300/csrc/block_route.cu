@@ -4,7 +4,6 @@
 
 #include <cmath>
 
-#include "block_launch.cuh"
 #include "block_ops.cuh"
 #include "../../include/moe_gb300.h"
 
@@ -360,12 +359,13 @@ group_kernel(const int32_t* __restrict__ ids, int S, int E, int first, int per_c
 
 cudaError_t launch_group(const int32_t* ids, int S, int E, int first, int32_t* offsets,
                          int32_t* perm, int32_t* slot_of, cudaStream_t st) {
-  static bool attr = false;
-  static int widest = 8;
-  if (!attr) {
+  static PerDevice<int> per;
+  int widest = 8;
+  cudaError_t err = on_device(per, &widest, [](int* w) {
     cudaError_t e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)group_smem(kGroupWarps, kGroupMaxExperts));
     if (e != cudaSuccess) return e;
+    *w = 8;
     // 16 CTAs are beyond the portable cluster size: used where the device can hold one
     if (cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
       cudaLaunchConfig_t q = {};
@@ -379,11 +379,12 @@ cudaError_t launch_group(const int32_t* ids, int S, int E, int first, int32_t* o
       q.attrs = &at;
       q.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, group_kernel, &q) == cudaSuccess && n > 0) widest = 16;
+      if (cudaOccupancyMaxActiveClusters(&n, group_kernel, &q) == cudaSuccess && n > 0) *w = 16;
     }
     (void)cudaGetLastError();
-    attr = true;
-  }
+    return cudaSuccess;
+  });
+  if (err != cudaSuccess) return err;
   const GroupShape g = group_shape(S, widest);
   const size_t smem = group_smem(g.warps, E);
   cudaLaunchConfig_t cfg = {};

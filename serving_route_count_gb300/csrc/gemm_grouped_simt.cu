@@ -6,7 +6,6 @@
 // owns 4 x 4 sums in fp32 (two sets for a SwiGLU: up and gate), operands pass through shared
 // memory 16 K at a time.  Bound by the fp32 FMA rate and the scalar operand loads: fc1 + SwiGLU of
 // 2048 tokens top-8 (E = 256, K = 6144, N = 1024) takes 9.9 ms here, 0.5 ms on the tensor cores.
-#include "block_launch.cuh"
 #include "block_ops.cuh"
 #include "grouped.cuh"
 #include "../../include/moe_gb300.h"

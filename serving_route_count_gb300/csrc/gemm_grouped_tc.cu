@@ -697,8 +697,9 @@ template <typename T, bool ACT, int BN, int ACC = 1>
 static cudaError_t launch_gt(GtParams& p, cudaStream_t st) {
   using Cfg = GtCfg<BN, ACC>;
   auto kernel = grouped_tc_kernel<T, ACT, BN, ACC>;
-  static int pairs = 0;
-  if (pairs == 0) {
+  static PerDevice<int> per;
+  int pairs = 0;
+  cudaError_t err = on_device(per, &pairs, [&](int* v) {
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
@@ -708,9 +709,10 @@ static cudaError_t launch_gt(GtParams& p, cudaStream_t st) {
     q.dynamicSmemBytes = Cfg::kSmem;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
-    if (e != cudaSuccess) return e;
-    pairs = n < 1 ? 1 : (n < kGtMaxPairs ? n : kGtMaxPairs);
-  }
+    *v = n < 1 ? 1 : (n < kGtMaxPairs ? n : kGtMaxPairs);
+    return e;
+  });
+  if (err != cudaSuccess) return err;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const GroupedDims& d = p.d;
   const GroupedCall& c = p.c;
