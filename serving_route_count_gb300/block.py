@@ -263,8 +263,10 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
     """Norm after a block (post_weight), gate, residual scale and the norm before the next block
     (pre_weight) in one pass; with slot_of and topk_weights the rows are the experts' and their
     top-k combination is taken here too.  Returns (residual_out, out): residual_out None without
-    rows, out None without pre_weight.  gate broadcasts over [M, H]; weights, biases and gate are
-    of the rows' type or all fp32.  See moe_block_norm in include/moe_gb300.h."""
+    rows, out None without pre_weight.  out is of the rows' type; without rows, and unless it is given,
+    of the residual's, of pre_weight's where the residual is fp32, bf16 where both are.  gate broadcasts
+    over [M, H]; weights, biases and gate are of out's type or all fp32.  See moe_block_norm in
+    include/moe_gb300.h."""
     dev = residual.get_device()
     if dev < 0 or dev != _current_device():
         _elsewhere(residual, "residual")
@@ -277,7 +279,7 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
     elif residual.dtype != torch.float32:
         dtype = residual.dtype
     else:
-        dtype = pre_weight.dtype if pre_weight is not None else torch.bfloat16
+        dtype = torch.bfloat16 if pre_weight is None or pre_weight.dtype == torch.float32 else pre_weight.dtype
     code = _CODE.get(dtype)
     if code is None:
         raise ValueError(f"rows: {dtype} is not supported")

@@ -108,3 +108,15 @@ def test_the_stream_is_of_the_operands_device(monkeypatch):
     assert block._stream(Stream(0), 0) == 77 and block._stream(5, 0) == 5
     with pytest.raises(ValueError, match="stream"):
         block._stream(Stream(1), 0)
+
+
+@pytest.mark.parametrize("residual,weight,out", [(F32, F32, BF16), (F32, BF16, BF16), (F32, torch.float16, torch.float16), (BF16, F32, BF16),
+                                                 (torch.float16, F32, torch.float16), (torch.float16, torch.float16, torch.float16)])
+def test_type_of_a_norm_before_a_block(lib, monkeypatch, residual, weight, out):
+    """Without rows and without out, something has to name out's 16-bit type: the residual, the weight, else bf16."""
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: empty(*a, **kw).as_subclass(On0))
+    r, z = block.moe_block_norm(t((4, 16), residual), pre_weight=t(16, weight), stream=7)
+    assert r is None and z.dtype == out
+    code = {BF16: 0, torch.float16: 1, F32: 2}
+    assert _lib.NORM_ARGS.unpack(lib.calls[0][1][0])[2:5] == (code[out], code[residual], code[weight])

@@ -66,3 +66,20 @@ def test_widest_product_on_the_cuda_cores(moe):
     # rounded once to bf16, from an fp32 sum of K terms
     assert torch.all((out[:2].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2 * K * 2.0 ** -24 * mag)
     assert torch.count_nonzero(out[2]) == 0
+
+
+# ------------------------------------------------------------------------------------ norms
+
+@gpu
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_of_an_fp32_residual_with_fp32_weights(moe, kind):
+    """A norm before a block where nothing is of 16 bits: out is bf16, or of the type of the one given."""
+    g = torch.Generator().manual_seed(3)
+    residual, w = torch.randn(7, 640, generator=g), 1 + 0.1 * torch.randn(640, generator=g)
+    k = moe.MOE_NORM_LAYER if kind == "layer" else moe.MOE_NORM_RMS
+    ref = B.norm(residual.double().numpy(), w.double().numpy(), kind=kind)
+    for out, rel in ((None, 2.0 ** -8), (torch.empty(7, 640, dtype=torch.float16, device="cuda"), 2.0 ** -11)):
+        r, z = moe.moe_block_norm(residual.cuda(), pre_weight=w.cuda(), kind=k, out=out)
+        assert r is None and z.dtype == (torch.bfloat16 if out is None else torch.float16)
+        # one rounding; sums of 640 squares and a handful of operations in fp32, at most 80 ulps of the row's largest value
+        assert np.all(np.abs(z.double().cpu().numpy() - ref) <= rel * np.abs(ref) + 80 * 2.0 ** -24 * np.abs(ref).max(1, keepdims=True) + 2.0 ** -25)
