@@ -224,6 +224,8 @@ class MoEGrouped:
         if w.dim() != 3 or w.shape[0] != self.E or w.shape[1] != self.N or w.shape[2] != self.K:
             raise ValueError(f"w must be [{self.E}, {self.N}, {self.K}], not {list(w.shape)}")
         per, ldw, unit = w.stride()
+        if self.N == 1:                # the stride of a dimension of one element says nothing
+            ldw = per if self.E > 1 else self.K
         if (unit != 1 and self.K > 1) or ldw < self.K or (per != self.N * ldw and self.E > 1):
             raise ValueError("the rows of w must be contiguous and evenly apart over all experts")
         if out is None:

@@ -120,3 +120,19 @@ def test_type_of_a_norm_before_a_block(lib, monkeypatch, residual, weight, out):
     assert r is None and z.dtype == out
     code = {BF16: 0, torch.float16: 1, F32: 2}
     assert _lib.NORM_ARGS.unpack(lib.calls[0][1][0])[2:5] == (code[out], code[residual], code[weight])
+
+
+@pytest.mark.parametrize("E,N,K,of,ldw", [(2, 1, 16, lambda: t((2, 24))[:, :16].unsqueeze(1), 24), (2, 1, 16, lambda: t((2, 5, 16))[:, :1], 80),
+                                          (1, 1, 16, lambda: t((1, 1, 16)).as_strided((1, 1, 16), (3, 2, 1)), 16), (1, 8, 16, lambda: t((1, 8, 24))[..., :16], 24),
+                                          (2, 8, 16, lambda: t((2, 8, 16)), 16)])
+def test_stride_of_weight_rows(lib, E, N, K, of, ldw):
+    """An expert of one row: rows are as far apart as experts are, whatever the middle dimension's stride is."""
+    op = grouped()
+    op.E, op.N, op.K, op.cols = E, N, K, N
+    w = of()
+    assert w.shape == (E, N, K)
+    op(t((4, K)), w, t(E + 1, I32), out=t((4, N)), stream=7)
+    assert lib.calls[0][1][7] == ldw
+    if E > 1 and N > 1:
+        with pytest.raises(ValueError, match="apart"):
+            op(t((4, K)), t((E, N + 1, K))[:, :N], t(E + 1, I32), out=t((4, N)), stream=7)

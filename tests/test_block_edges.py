@@ -68,6 +68,19 @@ def test_widest_product_on_the_cuda_cores(moe):
     assert torch.count_nonzero(out[2]) == 0
 
 
+@gpu
+@pytest.mark.parametrize("ld", [24, 19])                        # tensor cores, CUDA cores
+def test_experts_of_one_row(moe, ld):
+    g = torch.Generator().manual_seed(2)
+    w = torch.randn(3, ld, generator=g).bfloat16().cuda()[:, :16].unsqueeze(1)
+    x = torch.randn(5, 16, generator=g).bfloat16().cuda()
+    op = moe.MoEGrouped(3, 1, 16, max_rows=5)
+    got = op(x, w, torch.tensor([0, 2, 2, 5], dtype=torch.int32, device="cuda")).double()
+    e = torch.tensor([0, 0, 2, 2, 2], device="cuda")
+    terms = x.double() * w[e, 0].double()
+    assert torch.all((got[:, 0] - terms.sum(1)).abs() <= 2.0 ** -8 * terms.sum(1).abs() + 2 * 16 * 2.0 ** -24 * terms.abs().sum(1))
+
+
 # ------------------------------------------------------------------------------------ norms
 
 @gpu
