@@ -76,4 +76,44 @@ inline GsGrid grouped_simt_grid(int S, int E, int cols) {
           (unsigned)std::min((cols + kGsTile - 1) / kGsTile, 65535)};
 }
 
+// ---------------------------------------------------------------------------------- norms
+constexpr int kNormSlots = 16;          // most ring buffers of a CTA
+
+// Ring buffers of all of an SM's CTAs; what is left of its shared memory serves as L1 for the weights
+// (4096 x 7168 top-6, us with 100 / 132 / 170 / 200 KB: 94 / 91 / 100 / 105).
+constexpr int kNormRings = 132 * 1024;
+
+// The row ring (chunks of eight channels a thread, summing threads, buffers of a CTA) or plain
+// loads (no slots).
+struct NormShape {
+  bool ring;
+  int nch, threads, slots;
+};
+
+// vec: rows of whole vectors (H % 8 == 0 among it); res_bytes: of a residual element; combine: rows
+// come by slots.
+inline NormShape norm_shape(int M, int H, int res_bytes, bool vec, bool combine, int sms) {
+  const int chunks = (H + 7) / 8;
+  if (vec) {
+    // The ring, but for short rows, where the copying warp costs more than it hides.  us with the ring
+    // and with plain loads: 4096 x 7168 top-6 91 / 193, 8192 x 2048 top-6 56 / 70, 16384 x 1024 top-6
+    // 62 / 68; without a combine 8192 x 6144 (fp32 residual) 102 / 118, 16384 x 2048 67 / 73, 32768 x
+    // 1024 74 / 70, 32768 x 512 52 / 38.  Measured up to H = 7168.  ctas: what an SM's registers hold
+    // at the two-chunk kernel's 64 a thread; of the four-chunk kernel (126 a thread, H > 7680) it holds
+    // one, whose ring is then half of what the SM could give or less.
+    const int nch = chunks <= 960 ? 2 : 4, threads = ceil_to((chunks + nch - 1) / nch, 32);
+    const int ctas = std::max(1, 65536 / 64 / (threads + 32));
+    const int slots = std::min(kNormSlots, kNormRings / ctas / (H * res_bytes));
+    // And for few tokens, a CTA each and all of them at once or nearly: 1 x 7168 top-6 4.8 us with
+    // plain loads, 5.7 with the ring; 152: 5.2 / 5.9; 304: 9.5 / 7.7; 912 x 4096: 11.1 / 12.2; 1216:
+    // 18.1 / 17.6.
+    const int at_once = std::max(1, 65536 / 40 / ceil_to(chunks, 32));
+    const bool few = M <= sms * (2 * at_once - 1);
+    if (!few && chunks >= (combine ? 128 : 192) && threads <= 480 && slots >= 2)
+      return {true, nch, threads, slots};
+  }
+  const int nch = chunks <= 1024 ? 1 : (chunks <= 2048 ? 2 : 4);
+  return {false, nch, ceil_to((chunks + nch - 1) / nch, 32), 0};
+}
+
 }  // namespace moe

@@ -18,10 +18,6 @@
 
 namespace moe {
 
-// Ring buffers of all of an SM's CTAs; what is left of its shared memory serves as L1 for the weights
-// (4096 x 7168 top-6, us with 100 / 132 / 170 / 200 KB: 94 / 91 / 100 / 105).
-constexpr int kNormRings = 132 * 1024;
-
 struct NormParams {
   int M, H, kind, wide;             // wide: weights, biases and gate are fp32
   float eps, scale, woff, inv_h;
@@ -290,7 +286,6 @@ block_norm_kernel(const NormParams p) {
 // spend no instructions on addresses (with those in every thread the kernel was bound by
 // instruction issue), and the copies of the next tokens are in flight while this one is summed,
 // normalised and stored.
-constexpr int kNormSlots = 16;          // most ring buffers
 
 // Error word of the row copies' bounded waits (moe_block_norm_get_device_error).
 __device__ int32_t g_norm_error;
@@ -491,29 +486,18 @@ static cudaError_t launch_stream(const NormParams& p, int threads, int slots, cu
 
 template <typename T, typename R, bool VEC>
 static cudaError_t launch_norm_v(const NormParams& p, cudaStream_t st) {
-  const int chunks = cdiv(p.H, 8);
+  const NormShape n = norm_shape(p.M, p.H, (int)sizeof(R), VEC, p.slot_of != nullptr, sm_count());
   if constexpr (VEC) {
-    // The ring, but for short rows, where the copying warp costs more than it hides.  us with the ring
-    // and with plain loads: 4096 x 7168 top-6 91 / 193, 8192 x 2048 top-6 56 / 70, 16384 x 1024 top-6
-    // 62 / 68; without a combine 8192 x 6144 (fp32 residual) 102 / 118, 16384 x 2048 67 / 73, 32768 x
-    // 1024 74 / 70, 32768 x 512 52 / 38.
-    const int nch = chunks <= 960 ? 2 : 4, threads = (int)align_up((size_t)cdiv(chunks, nch), 32);
-    const int ctas = std::max(1, 65536 / 64 / (threads + 32));       // an SM's registers hold
-    const int slots = std::min(kNormSlots, kNormRings / ctas / (p.H * (int)sizeof(R)));
-    // And for few tokens, a CTA each and all of them at once or nearly: 1 x 7168 top-6 4.8 us with
-    // plain loads, 5.7 with the ring; 152: 5.2 / 5.9; 304: 9.5 / 7.7; 912 x 4096: 11.1 / 12.2; 1216:
-    // 18.1 / 17.6.
-    const int at_once = std::max(1, 65536 / 40 / (int)align_up((size_t)chunks, 32));
-    const bool few = p.M <= sm_count() * (2 * at_once - 1);
-    if (!few && chunks >= (p.slot_of != nullptr ? 128 : 192) && threads <= 480 && slots >= 2)
-      return nch == 2 ? launch_stream<T, R, 2, 480, 2>(p, threads, slots, st)
-                      : launch_stream<T, R, 4, 480, 1>(p, threads, slots, st);
+    if (n.ring && n.nch == 2) return launch_stream<T, R, 2, 480, 2>(p, n.threads, n.slots, st);
+    // (two buffers of an fp32 residual's size do not fit where rows take four chunks)
+    if constexpr (sizeof(R) == 2)
+      if (n.ring) return launch_stream<T, R, 4, 480, 1>(p, n.threads, n.slots, st);
   }
-  const int nch = chunks <= 1024 ? 1 : (chunks <= 2048 ? 2 : 4);
-  const dim3 block((unsigned)align_up((size_t)cdiv(chunks, nch), 32));
-  auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(p.M), block, 0, st, true, p); };
-  if (nch == 1) return go(block_norm_kernel<T, R, VEC, 1>);
-  if (nch == 2) return go(block_norm_kernel<T, R, VEC, 2>);
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, dim3(p.M), dim3(n.threads), 0, st, true, p);
+  };
+  if (n.nch == 1) return go(block_norm_kernel<T, R, VEC, 1>);
+  if (n.nch == 2) return go(block_norm_kernel<T, R, VEC, 2>);
   return go(block_norm_kernel<T, R, VEC, 4>);
 }
 template <typename T, typename R>

@@ -1,57 +1,14 @@
-"""Launch shapes of the 16-bit block's kernels (csrc/block_launch.cuh), compiled for this host."""
+"""Launch shapes of the 16-bit block's kernels: every call that is taken fits its launch."""
 import ctypes
-import os
-import subprocess
 
 import pytest
 
-CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "serving_route_count_gb300", "csrc")
-SHIM = """
-#include "block_launch.cuh"
-#include <thread>
-#include <vector>
-// 16 threads ask for devices 0 .. 3, over and over; o[d]: how often device d was asked.  Its first two answers are errors.
-extern "C" int per_device(int* o) {
-  moe::PerDevice<int> per;
-  std::atomic<int> asked[4] = {}, errors{0}, wrong{0};
-  std::vector<std::thread> threads;
-  for (int i = 0; i < 16; ++i)
-    threads.emplace_back([&, i] {
-      for (int j = 0; j < 2000; ++j) {
-        const int dev = (unsigned)(i + j) % 4u;
-        int v = -1;
-        if (per.get(dev, &v, [&](int* p) { *p = 100 + dev; return asked[dev]++ < 2 ? 7 : 0; }) != 0)
-          ++errors;
-        else if (v != 100 + dev)
-          ++wrong;
-      }
-    });
-  for (auto& t : threads) t.join();
-  for (int d = 0; d < 4; ++d) o[d] = asked[d];
-  o[4] = errors;
-  int past = 0;
-  for (int j = 0; j < 3; ++j) per.get(j < 2 ? 64 : -1, &o[5], [&](int* p) { *p = 5; ++past; return 0; });
-  o[6] = past;
-  return wrong;
-}
-extern "C" void group_shape(int S, int widest, int* o) {
-  const moe::GroupShape g = moe::group_shape(S, widest);
-  o[0] = g.ctas; o[1] = g.per_cta; o[2] = g.per_warp; o[3] = g.warps;
-}
-extern "C" void grouped_simt_grid(int S, int E, int cols, unsigned* o) {
-  const moe::GsGrid g = moe::grouped_simt_grid(S, E, cols);
-  o[0] = g.x; o[1] = g.y;
-}
-"""
+import block_shapes
 
 
 @pytest.fixture(scope="module")
 def shapes(tmp_path_factory):
-    d = tmp_path_factory.mktemp("shapes")
-    (d / "shim.cpp").write_text(SHIM)
-    so = str(d / "shim.so")
-    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-fPIC", "-shared", "-pthread", "-I", CSRC, str(d / "shim.cpp"), "-o", so], check=True)
-    return ctypes.CDLL(so)
+    return block_shapes.build(tmp_path_factory.mktemp("shapes"))
 
 
 @pytest.mark.parametrize("widest", [8, 16])
@@ -84,3 +41,30 @@ def test_facts_of_each_device(shapes):
     o = (ctypes.c_int * 7)()
     assert shapes.per_device(o) == 0
     assert list(o) == [3, 3, 3, 3, 8, 5, 3]
+
+
+@pytest.mark.parametrize("res", [2, 4])
+@pytest.mark.parametrize("combine", [0, 1])
+def test_norm_shape(shapes, combine, res):
+    o = (ctypes.c_int * 3)()
+    rings = set()
+    for H in [*range(1, 1100, 3), *range(1096, 32769, 8), 32767, 32768]:
+        for M in (1, 152, 153, 1000, 2000, 40000):
+            for vec in (0, 1) if H % 8 == 0 else (0,):
+                ring = shapes.norm_shape(M, H, res, vec, combine, 152, o)
+                nch, threads, slots = o
+                assert threads % 32 == 0 and nch * threads * 8 >= H                         # every channel has a thread
+                if ring:
+                    assert vec and nch in (2, 4) and threads <= 480 and 2 <= slots <= 16
+                    assert slots * H * res <= shapes.norm_rings()
+                    rings.add(nch)
+                else:
+                    assert nch in (1, 2, 4) and threads <= 1024 and slots == 0
+    assert rings == ({2, 4} if res == 2 else {2})
+
+
+@pytest.mark.parametrize("M,H,res,combine,ring", [(4096, 7168, 2, 1, 1), (8192, 6144, 4, 0, 1), (1, 7168, 2, 1, 0), (152, 7168, 2, 1, 0), (153, 7168, 2, 1, 1),
+                                                  (8192, 2048, 2, 1, 1), (16384, 1024, 2, 1, 1), (32768, 1024, 2, 0, 0), (32768, 512, 2, 1, 0)])
+def test_norm_kernel_of_a_size(shapes, M, H, res, combine, ring):
+    """The sizes whose times decide between the two kernels, on 152 SMs."""
+    assert shapes.norm_shape(M, H, res, 1, combine, 152, (ctypes.c_int * 3)()) == ring
