@@ -444,6 +444,12 @@ moe_status moe_grouped_run(const moe_grouped_t* plan, void* scratch, size_t scra
                            const void* x, long long ldx, int x_rows, const void* w, long long ldw,
                            const int32_t* offsets, const int32_t* perm, int topk, void* out,
                            long long ldo, int S, void* stream);
+/* Test hook, as moe_plan_set_wait_probe: with ns > 0 the tensor-core kernel's first CTA pair makes
+ * its MMA issuer wait up to ns nanoseconds on a barrier that nothing arrives on.  The wait runs out,
+ * sets the timeout bit of the device error word, and the pair's other roles give up their own waits
+ * (1 s) and return: the call's output is undefined, and the plan is usable again after
+ * moe_grouped_get_device_error.  ns = 0 (default) turns it off.  Errors: MOE_ERR_ARG (ns > 1 s). */
+moe_status moe_grouped_set_wait_probe(moe_grouped_t* plan, unsigned long long ns);
 /* Reads the device error word in `scratch` and makes the buffer ready for the next call
  * (synchronises `stream`): *code as moe_get_device_error. */
 moe_status moe_grouped_get_device_error(const moe_grouped_t* plan, void* scratch, void* stream,

@@ -87,6 +87,7 @@ SIGNATURES = {
     "moe_grouped_run": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_int, c_void_p,
                                 c_longlong, c_void_p, c_void_p, c_int, c_void_p, c_longlong, c_int,
                                 c_void_p]),
+    "moe_grouped_set_wait_probe": (c_int, [c_void_p, ctypes.c_ulonglong]),
     "moe_grouped_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
     "moe_destroy_grouped": (None, [c_void_p]),
     "moe_block_norm_get_device_error": (c_int, [c_void_p, c_int_p]),

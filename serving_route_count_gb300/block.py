@@ -174,6 +174,10 @@ def moe_grouped_scratch_bytes(plan) -> int:
     return n.value
 
 
+def moe_grouped_set_wait_probe(plan, ns):
+    _check(_lib.load().moe_grouped_set_wait_probe(plan, int(ns)), "moe_grouped_set_wait_probe")
+
+
 def moe_grouped_get_device_error(plan, scratch, stream=None):
     """(status, code) of the device error word in `scratch`, which is cleared."""
     code = ctypes.c_int()

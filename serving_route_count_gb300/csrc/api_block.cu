@@ -86,9 +86,15 @@ moe_status moe_grouped_plan(int E, int N, int K, int dtype, int act, int layout,
     return MOE_ERR_SHAPE;
   moe_grouped_s* g = new (std::nothrow) moe_grouped_s();
   if (g == nullptr) return MOE_ERR_ARG;
-  g->d = GroupedDims{E, N, K, dtype, act, layout, max_rows, limit, alpha, beta};
+  g->d = GroupedDims{E, N, K, dtype, act, layout, max_rows, limit, alpha, beta, 0};
   g->bytes = kGtPartAt + grouped_tc_part_bytes(max_rows, E);
   *out = g;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_set_wait_probe(moe_grouped_t* plan, unsigned long long ns) {
+  if (plan == nullptr || ns > 1000000000ull) return MOE_ERR_ARG;
+  plan->d.probe_ns = ns;
   return MOE_OK;
 }
 

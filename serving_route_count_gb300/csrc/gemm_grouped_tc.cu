@@ -447,13 +447,10 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
       }
     }
     if (lane == 0) {
-      if (ok) {
-        // the last fills have been multiplied: nothing arrives at this CTA's barriers any more
-        for (int j = max(0, issued - S); j < issued; ++j)
-          mbar_wait(&empty[j % S], (j / S) & 1, err);
-      } else if (rank == 0) {
-        drain_stage_loads<S>(full, issued, err);
-      }
+      // the last fills have been multiplied: nothing arrives at this CTA's barriers any more
+      for (int j = max(0, issued - S); ok && j < issued; ++j)
+        ok = mbar_wait(&empty[j % S], (j / S) & 1, err);
+      if (!ok && rank == 0) drain_stage_loads<S>(full, issued, err);
     }
   } else if (warp == 1) {
     // operand descriptors: only the address changes from stage to stage and from K block to K block
@@ -461,6 +458,9 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     const uint32_t hi = (uint32_t)(desc0 >> 32), lo0 = (uint32_t)desc0;
     uint32_t uses[2] = {0, 0};       // units that each accumulator buffer has held
     int seg = 0;
+    // nothing commits to this phase before the first unit's MMAs
+    if (p.d.probe_ns != 0 && blockIdx.x == 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(&tfull[0], 0, err, p.d.probe_ns));
     while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
       const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
       const int accs = accs_of(rb);

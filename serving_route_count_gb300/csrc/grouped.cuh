@@ -15,6 +15,7 @@ static_assert(kGtTicketsAt + kGtMaxPairs * 4 * sizeof(int32_t) <= kGtPartAt, "ti
 struct GroupedDims {
   int E, N, K, dtype, act, layout, max_rows;
   float limit, alpha, beta;
+  unsigned long long probe_ns;         // test hook (0: off), see moe_grouped_set_wait_probe
 };
 
 struct GroupedCall {

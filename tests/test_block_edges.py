@@ -81,6 +81,58 @@ def test_experts_of_one_row(moe, ld):
     assert torch.all((got[:, 0] - terms.sum(1)).abs() <= 2.0 ** -8 * terms.sum(1).abs() + 2 * 16 * 2.0 ** -24 * terms.abs().sum(1))
 
 
+@gpu
+def test_many_k_steps(moe):
+    """4100 steps of 64 along K, cut among the CTA pairs.  Small whole numbers: every partial sum is exact in fp32."""
+    E, N, K = 2, 40, 262400
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, w = (torch.randint(-1, 2, s, generator=g, device="cuda").bfloat16() for s in ((5, K), (E, N, K)))
+    op = moe.MoEGrouped(E, N, K, max_rows=5)
+    off = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    got = op(x, w, off)
+    assert op.device_error() == (0, 0)
+    ref = torch.cat([x[:3].double() @ w[0].double().t(), x[3:].double() @ w[1].double().t()])
+    assert torch.equal(got, ref.bfloat16())
+
+
+def test_refusals_of_the_wait_probe():
+    import serving_route_count_gb300 as m
+    from serving_route_count_gb300 import build
+    build.build()
+    h = m.moe_grouped_plan(2, 8, 16, 0, 0, 0, float("inf"), 1.0, 0.0, 4)
+    m.moe_grouped_set_wait_probe(h, 1_000_000_000)
+    m.moe_grouped_set_wait_probe(h, 0)
+    for plan, ns in ((h, 1_000_000_001), (None, 0)):
+        with pytest.raises(m.MoEError) as e:
+            m.moe_grouped_set_wait_probe(plan, ns)
+        assert e.value.status == 1
+    m.moe_destroy_grouped(h)
+
+
+@gpu
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,N,K,act", [([3, 0, 2], 512, 4096, True),             # units cut by K steps
+                                            ([40, 300, 7], 8192, 512, False)])        # more units than CTA pairs, whole ones first
+def test_a_wait_that_runs_out(moe, counts, N, K, act, gather):
+    """The first CTA pair's MMA issuer gives up a wait of 2 ms: the call ends with MOE_ERR_TIMEOUT in the error word, and the
+    next one gives the result of a plan that never saw it."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    S = sum(counts)
+    x = torch.randn((S, K), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((len(counts), N, K), generator=g, device="cuda") * K ** -0.5).bfloat16()
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    perm = torch.arange(S, dtype=torch.int32, device="cuda") if gather else None
+    new = lambda: moe.MoEGrouped(len(counts), N, K, max_rows=S, act=moe.MOE_ACT_SWIGLU if act else moe.MOE_ACT_NONE)  # noqa: E731
+    want, op = new()(x, w, off, perm=perm), new()
+    moe.moe_grouped_set_wait_probe(op.plan, 2_000_000)
+    op(x, w, off, perm=perm)
+    assert op.device_error() == (7, 2)
+    moe.moe_grouped_set_wait_probe(op.plan, 0)
+    for _ in range(3):
+        assert torch.equal(op(x, w, off, perm=perm), want)
+    assert op.device_error() == (0, 0)
+
+
 # ------------------------------------------------------------------------------------ norms
 
 @gpu
