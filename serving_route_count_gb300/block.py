@@ -314,8 +314,8 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
     if gate is not None:
         gate_p = _dev(gate, "gate", dev, wt)
         shape, step = gate.shape, gate.stride()
-        if len(shape) == 1:
-            shape, step = (1, shape[0]), (0, step[0])
+        if len(shape) < 2:
+            shape, step = (1, *(shape or (1,))), (0, *(step or (0,)))
         if len(shape) != 2 or shape[0] not in (1, M) or shape[1] not in (1, H):
             raise ValueError("gate must broadcast over [M, H]")
         gate_row = step[0] if shape[0] > 1 else 0

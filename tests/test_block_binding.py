@@ -136,3 +136,19 @@ def test_stride_of_weight_rows(lib, E, N, K, of, ldw):
     if E > 1 and N > 1:
         with pytest.raises(ValueError, match="apart"):
             op(t((4, K)), t((E, N + 1, K))[:, :N], t(E + 1, I32), out=t((4, N)), stream=7)
+
+
+@pytest.mark.parametrize("shape,row,col", [((), 0, 0), ((1,), 0, 0), ((16,), 0, 1), ((1, 1), 0, 0), ((1, 16), 0, 1), ((4, 1), 1, 0), ((4, 16), 16, 1)])
+def test_gates_that_broadcast(lib, shape, row, col):
+    """Any shape that broadcasts over [M, H], a scalar among them."""
+    block.moe_block_norm(t((4, 16)), t((4, 16)), gate=t(shape), residual_out=t((4, 16)), stream=7)
+    names = ("M H dtype residual_dtype weight_dtype kind eps scale weight_offset residual ld_residual rows ld_rows slot_of topk_weights topk n_rows "
+             "shared ld_shared post_weight post_bias gate gate_row gate_col").split()
+    args = dict(zip(names, _lib.NORM_ARGS.unpack(lib.calls[0][1][0])))
+    assert args["gate"] and (args["gate_row"], args["gate_col"]) == (row, col)
+
+
+@pytest.mark.parametrize("shape", [(4,), (2, 16), (4, 8), (1, 4, 16)])
+def test_gates_that_do_not(lib, shape):
+    with pytest.raises(ValueError, match="gate"):
+        block.moe_block_norm(t((4, 16)), t((4, 16)), gate=t(shape), residual_out=t((4, 16)), stream=7)
