@@ -98,9 +98,9 @@ inline NormShape norm_shape(int M, int H, int res_bytes, bool vec, bool combine,
     // The ring, but for short rows, where the copying warp costs more than it hides.  us with the ring
     // and with plain loads: 4096 x 7168 top-6 91 / 193, 8192 x 2048 top-6 56 / 70, 16384 x 1024 top-6
     // 62 / 68; without a combine 8192 x 6144 (fp32 residual) 102 / 118, 16384 x 2048 67 / 73, 32768 x
-    // 1024 74 / 70, 32768 x 512 52 / 38.  Measured up to H = 7168.  ctas: what an SM's registers hold
-    // at the two-chunk kernel's 64 a thread; of the four-chunk kernel (126 a thread, H > 7680) it holds
-    // one, whose ring is then half of what the SM could give or less.
+    // 1024 74 / 70, 32768 x 512 52 / 38.  ctas: what an SM's registers hold at the two-chunk kernel's 64
+    // a thread; of the four-chunk kernel (126 a thread, H > 7680) it holds one, whose ring is then half
+    // of what the SM could give or less (4096 x 8192 top-6 163 us, 54 % of the copy bandwidth).
     const int nch = chunks <= 960 ? 2 : 4, threads = ceil_to((chunks + nch - 1) / nch, 32);
     const int ctas = std::max(1, 65536 / 64 / (threads + 32));
     const int slots = std::min(kNormSlots, kNormRings / ctas / (H * res_bytes));

@@ -8,7 +8,10 @@
 // kernels: norm_stream_kernel, whose rows arrive by asynchronous copies in a shared-memory ring
 // ahead of the arithmetic, and block_norm_kernel, plain loads, for short rows, rows that do not
 // start on 16 bytes and rows too long for a ring.  Bound by HBM: 4096 x 7168 with a top-6 combine 91 us (85 % of the
-// measured copy bandwidth), 8192 x 6144 with an fp32 residual 102 us (87 %); one token 4.8 us.
+// measured copy bandwidth), 8192 x 6144 with an fp32 residual 102 us (87 %); one token 4.9 us.  Further
+// from it: a combine with an fp32 residual, whose ring holds fewer rows (4096 x 7168 117 us, 81 %), and
+// rows above 7680 channels (4096 x 8192 top-6 163 us, 54 %; 12288 191 us, 70 %; with an fp32 residual,
+// plain loads, 206 and 265 us, 53 and 62 %).
 #include <algorithm>
 #include <type_traits>
 

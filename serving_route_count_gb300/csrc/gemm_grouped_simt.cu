@@ -1,6 +1,6 @@
-// gemm_grouped_simt.cu - products grouped by expert on the CUDA cores, for operands that the
-// tensor-core kernel's tile copies cannot address (rows that do not start on 16-byte
-// boundaries).
+// gemm_grouped_simt.cu - products grouped by expert on the CUDA cores, for operands whose rows do not
+// start on 16-byte boundaries, as the tensor-core kernel's tile copies need.  Such operands are taken,
+// and not meant to be fast.
 //
 // One CTA of 256 threads per tile of 64 positions of one expert x 64 output columns; a thread
 // owns 4 x 4 sums in fp32 (two sets for a SwiGLU: up and gate), operands pass through shared

@@ -23,8 +23,12 @@
 //   fc2 of 16 tokens top-6, E = 384, K = 576, N = 7168: 112-117 us, floor 104 - what is left is the
 //   start (tables 2 us, first loads 2.5 us) and the last units;
 //   fc1 of 2048 tokens top-8: 495-508 us, floor 480; fc2 (K = 512, N = 6144): 275 us, floor 269;
-//   4096 tokens top-6 over 16 experts, K = 7168, N = 2304 (f16): 473-480 us, 1.7 PFLOP/s, bound by
-//   the tensor cores and their power (8192 x 8192 x 8192 in bf16: 1.93 PFLOP/s, cuBLAS 1.98).
+//   4096 tokens top-6 over 16 experts, K = 7168, N = 2304 (f16): 473-485 us (1.7 PFLOP/s) in short
+//   runs, 552-574 (1.41-1.47 PFLOP/s) in runs of seconds, where the power limit takes the clocks to 1.5
+//   GHz: bound by the tensor cores and their power (floor 422 burst, 473 sustained; 8192 x 8192 x 8192
+//   in bf16: 568 us, 1.94 PFLOP/s; cuBLAS 538-552).
+//   A call with dropped slots writes their rows as zeros before the first weight copy: 4096 tokens top-8,
+//   one of eight ranks (4,027 of 32,768 rows its own, N = 7168, K = 512) 144 us, its rows alone 53.
 //
 // Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-7 token copies (tiles, or
 // gathers of four rows by index, whose issue takes ~70 cycles each: six warps share it; warp 3
@@ -665,7 +669,9 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
 
 // ---------------------------------------------------------------------------------- host side
 
-// Token-tile width by the mean positions per expert: an expert should be one tile while HBM is the
+// Token-tile width by the mean positions per expert (of S, dropped slots among them: the rows that
+// belong here are known on the device only; a rank of eight may get a tile up to eight times as wide
+// as its rows ask for, 2-4 % by the table): an expert should be one tile while HBM is the
 // bound (its weights pass an SM pair once per tile), and a narrower tile leaves more of the shared
 // memory to weights in flight.  E = 256, K = 6144, N = 1024, SwiGLU, us at widths 32 / 64 / 128 /
 // 256: mean 8: 469 / 471 / 481 / 488;  24: 484 / 478 / 488 / 495;  48: 778 / 493 / 500 / 503;  64:
