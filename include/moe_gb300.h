@@ -498,6 +498,11 @@ typedef struct {
   long long ld_out;
 } moe_norm_args;
 moe_status moe_block_norm(const moe_norm_args* args, void* stream);
+/* Test hook, as moe_plan_set_wait_probe, for every later call of the process: the first CTA of the
+ * kernel of many tokens makes the warp that copies its rows give up a wait of ns nanoseconds and copy
+ * nothing; its summing threads give up theirs (1 s) and end.  0 (default) turns it off.
+ * Errors: MOE_ERR_ARG (ns > 1 s). */
+moe_status moe_block_norm_set_wait_probe(unsigned long long ns);
 /* Reads and clears the device error word of moe_block_norm's calls on the current device
  * (synchronises `stream`): *code = 0 unless a bounded wait of one of them gave up, in which case
  * the status is MOE_ERR_TIMEOUT and that call's outputs are undefined. */

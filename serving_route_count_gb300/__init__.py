@@ -17,7 +17,7 @@ from .moe import (  # noqa: F401
 from .block import (  # noqa: F401
     MoEGrouped, moe_router, moe_group, moe_grouped_plan, moe_grouped_scratch_bytes,
     moe_grouped_set_wait_probe, moe_grouped_get_device_error, moe_destroy_grouped, moe_block_norm,
-    moe_block_norm_get_device_error,
+    moe_block_norm_set_wait_probe, moe_block_norm_get_device_error,
     MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID,
     MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_NORM_RMS, MOE_NORM_LAYER,
 )

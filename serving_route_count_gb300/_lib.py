@@ -90,6 +90,7 @@ SIGNATURES = {
     "moe_grouped_set_wait_probe": (c_int, [c_void_p, ctypes.c_ulonglong]),
     "moe_grouped_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
     "moe_destroy_grouped": (None, [c_void_p]),
+    "moe_block_norm_set_wait_probe": (c_int, [ctypes.c_ulonglong]),
     "moe_block_norm_get_device_error": (c_int, [c_void_p, c_int_p]),
     "moe_block_norm": (c_int, [c_void_p, c_void_p]),
 }

@@ -346,6 +346,10 @@ def moe_block_norm(residual, rows=None, slot_of=None, topk_weights=None, shared=
     return residual_out, out
 
 
+def moe_block_norm_set_wait_probe(ns):
+    _check(_lib.load().moe_block_norm_set_wait_probe(int(ns)), "moe_block_norm_set_wait_probe")
+
+
 def moe_block_norm_get_device_error(stream=None):
     """(status, code) of the device error word of moe_block_norm's calls on the current device, which
     is cleared."""

@@ -18,6 +18,7 @@ cudaError_t launch_group(const int32_t* ids, int S, int E, int first, int32_t* o
 // block_norm.cu
 cudaError_t launch_block_norm(const moe_norm_args& a, bool vec, cudaStream_t st);
 cudaError_t norm_device_error(int* code, cudaStream_t st);
+void set_norm_probe(unsigned long long ns);
 // gemm_grouped_simt.cu
 cudaError_t launch_grouped_simt(const GroupedDims& d, const GroupedCall& c, cudaStream_t st);
 // gemm_grouped_tc.cu
@@ -182,6 +183,12 @@ moe_status moe_block_norm(const moe_norm_args* a, void* stream) {
                    rows8(a->pre_weight, 0, wt) && rows8(a->pre_bias, 0, wt) &&
                    (a->gate == nullptr || a->gate_col == 0 || rows8(a->gate, a->gate_row, wt));
   return status(launch_block_norm(*a, vec, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_block_norm_set_wait_probe(unsigned long long ns) {
+  if (ns > 1000000000ull) return MOE_ERR_ARG;
+  set_norm_probe(ns);
+  return MOE_OK;
 }
 
 moe_status moe_block_norm_get_device_error(void* stream, int* code) {

@@ -13,6 +13,7 @@
 // rows above 7680 channels (4096 x 8192 top-6 163 us, 54 %; 12288 191 us, 70 %; with an fp32 residual,
 // plain loads, 206 and 265 us, 53 and 62 %).
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "block_ops.cuh"
@@ -36,6 +37,7 @@ struct NormParams {
   const void *pre_w, *pre_b;
   void *res_out, *out;
   long long ld_res_out, ld_out;
+  unsigned long long probe_ns;      // test hook (0: off), see moe_block_norm_set_wait_probe
 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -319,6 +321,9 @@ norm_stream_kernel(const NormParams p, const int slots, const int slot_bytes) {
     const int per = n_rows + 1;
     int b = 0, phase = 1, issued = 0;
     bool ok = true;
+    // no buffer is freed before one is filled
+    if (p.probe_ns != 0 && blockIdx.x == 0)
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[0], 0, &g_norm_error, p.probe_ns));
     // 32 rows at a time: lane l finds row l of them, then the rows are copied in order
     int t = blockIdx.x, j = 0;             // the first of the 32
     while (ok && t < p.M) {
@@ -527,6 +532,9 @@ cudaError_t norm_device_error(int* code, cudaStream_t st) {
   return e;
 }
 
+static std::atomic<unsigned long long> g_norm_probe{0};
+void set_norm_probe(unsigned long long ns) { g_norm_probe = ns; }
+
 // vec: every row of every operand starts on a boundary of eight elements and H % 8 == 0.
 cudaError_t launch_block_norm(const moe_norm_args& a, bool vec, cudaStream_t st) {
   NormParams p;
@@ -539,6 +547,7 @@ cudaError_t launch_block_norm(const moe_norm_args& a, bool vec, cudaStream_t st)
   p.gate_row = a.gate_row; p.gate_col = a.gate_col;
   p.pre_w = a.pre_weight; p.pre_b = a.pre_bias;
   p.res_out = a.residual_out; p.out = a.out; p.ld_res_out = a.ld_residual_out; p.ld_out = a.ld_out;
+  p.probe_ns = g_norm_probe;
   const bool wide_res = a.residual_dtype == MOE_DTYPE_F32;
   return a.dtype == MOE_DTYPE_F16 ? launch_norm_t<__half>(p, wide_res, vec, st)
                                   : launch_norm_t<__nv_bfloat16>(p, wide_res, vec, st);

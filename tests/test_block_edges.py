@@ -107,6 +107,10 @@ def test_refusals_of_the_wait_probe():
             m.moe_grouped_set_wait_probe(plan, ns)
         assert e.value.status == 1
     m.moe_destroy_grouped(h)
+    m.moe_block_norm_set_wait_probe(0)
+    with pytest.raises(m.MoEError) as e:
+        m.moe_block_norm_set_wait_probe(1_000_000_001)
+    assert e.value.status == 1
 
 
 @gpu

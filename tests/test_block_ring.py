@@ -89,3 +89,29 @@ def test_no_expert_rows(moe, ring, M, H, shared):
     r0, o0 = moe.moe_block_norm(res, sh if shared else torch.zeros_like(sh), pre_weight=w)
     assert moe.moe_block_norm_get_device_error() == (0, 0)
     assert torch.equal(r, r0) and torch.equal(o, o0)
+
+
+@gpu
+@pytest.mark.parametrize("M,H,k", [(1800, 2048, 2), (200, 7168, 0), (200, 15360, 1)])
+def test_a_wait_that_runs_out(moe, ring, M, H, k):
+    """The first CTA's copying warp gives up a wait of 2 ms: the call ends with MOE_ERR_TIMEOUT in the error word, other CTAs' tokens
+    are right, and so is the next call."""
+    ring(M, H, k, "same")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    residual, rows = (torch.randn(n, H, generator=g, device="cuda").bfloat16() for n in (M, M * max(1, k)))
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    kw = dict(post_weight=w, pre_weight=w)
+    if k:
+        kw |= dict(slot_of=torch.randperm(M * k, generator=g, device="cuda").int().view(M, k), topk_weights=torch.rand(M, k, generator=g, device="cuda"))
+    want = moe.moe_block_norm(residual, rows, **kw)
+    try:
+        moe.moe_block_norm_set_wait_probe(2_000_000)
+        got = moe.moe_block_norm(residual, rows, **kw)
+        assert moe.moe_block_norm_get_device_error() == (7, 2)
+    finally:
+        moe.moe_block_norm_set_wait_probe(0)
+    assert all(torch.equal(a[1:150], b[1:150]) for a, b in zip(got, want))      # token t of the first 150 is CTA t's
+    for _ in range(2):
+        got = moe.moe_block_norm(residual, rows, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert moe.moe_block_norm_get_device_error() == (0, 0)
