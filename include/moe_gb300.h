@@ -508,6 +508,96 @@ moe_status moe_block_norm_set_wait_probe(unsigned long long ns);
  * the status is MOE_ERR_TIMEOUT and that call's outputs are undefined. */
 moe_status moe_block_norm_get_device_error(void* stream, int* code);
 
+/* ------------------------------------------------------------------------------------------
+ * Products of 8-bit operands with a scale for each block of 128 (conventions of the 16-bit block).
+ * A value is an e4m3 code (4 exponent bits, bias 7, 3 mantissa bits, no infinities, 0x7F / 0xFF NaN)
+ * times its block's fp32 scale.  Rows of activations have a scale for each 128 values along K, weights
+ * one for each tile of 128 rows x 128 values; the last block of a dimension may be short.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum { MOE_FP8_ROWS = 0, MOE_FP8_TILES = 1 } moe_fp8_form;
+
+/* Quantisation of x to that form:
+ *   scale = max(max |x| / 448, 2^-126) of the block, code = e4m3(x / scale)
+ * (fp32 quotients; to nearest, ties to even, saturating).  A NaN takes no part in its block's scale and
+ * gets a NaN code; an infinity makes the scale infinite, its own code NaN and the block's others 0.
+ *   MOE_FP8_ROWS (E = 1): x [rows, K], scale [rows, KB], KB = ceil(K / 128).
+ *   MOE_FP8_TILES: E matrices x [E, rows, K] with evenly spaced rows, ldx apart over all of them, q
+ *   likewise; scale [E, ceil(rows / 128), KB], rows of scales lds apart over all matrices.
+ *   dtype of x: MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32.  Row strides ldx, ldq, lds in elements.
+ * E == 0 or rows == 0 is a no-op.  Limits: K <= 2^24, E * rows < 2^31, fewer than 2^31 tiles.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (type), MOE_ERR_CUDA. */
+moe_status moe_fp8_quant(const void* x, int dtype, long long ldx, int E, int rows, int K, int form,
+                         uint8_t* q, long long ldq, float* scale, long long lds, void* stream);
+
+/* Products of such operands, dense or grouped by expert, fp32 sums:
+ *   out[p, n] = act(sum_b x_scale[row(p), b] * w_scale[e, t(n), b] * sum_{k in block b} x[row(p), k] w[e, n, k])
+ * with groups, row(p), act and the rows past the last group as for moe_grouped_run; without offsets
+ * (E = 1) all S positions are the one matrix's.  t(n) = n / 128; with MOE_ACT_SWIGLU each half of N / 2
+ * rows has tiles of its own: half h's row i is in tile row h * ceil(N / 2 / 128) + i / 128.
+ * The plan's arguments, limits and errors are moe_grouped_plan's; dtype is the type of out. */
+typedef struct moe_fp8_s moe_fp8_t;
+moe_status moe_fp8_plan(int E, int N, int K, int dtype, int act, int layout, float limit, float alpha,
+                        float beta, int max_rows, moe_fp8_t** out);
+/* Bytes of the scratch buffer of moe_fp8_run (256-byte aligned, caller-owned). */
+moe_status moe_fp8_scratch_bytes(const moe_fp8_t* plan, size_t* bytes);
+/* One product; scratch, offsets (or NULL where E = 1), perm and topk as for moe_grouped_run.
+ *   x [x_rows, K] codes, row stride ldx, x_scale [x_rows, KB], row stride ldxs;  w [E, N, K] codes with
+ *   row stride ldw and expert stride ldw * N, w_scale [E, tile rows, KB] contiguous;  out [S, N or
+ *   N / 2], row stride ldo.  out must not overlap an input.
+ * Rows whose x, w and strides are 16-byte aligned run on the tensor cores; other operands (for
+ * instance K % 16 != 0) on the CUDA cores, slower.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (S > max_rows), MOE_ERR_CUDA. */
+moe_status moe_fp8_run(const moe_fp8_t* plan, void* scratch, size_t scratch_bytes, const uint8_t* x,
+                       long long ldx, int x_rows, const float* x_scale, long long ldxs, const uint8_t* w,
+                       long long ldw, const float* w_scale, const int32_t* offsets, const int32_t* perm,
+                       int topk, void* out, long long ldo, int S, void* stream);
+/* As moe_grouped_get_device_error. */
+moe_status moe_fp8_get_device_error(const moe_fp8_t* plan, void* scratch, void* stream, int* code);
+void moe_destroy_fp8(moe_fp8_t* plan);
+
+/* ------------------------------------------------------------------------------------------
+ * Dense gated feed-forward block in 16 bits (a shared expert: its output is moe_block_norm's `shared`),
+ * with its backward pass (conventions of the 16-bit block):
+ *   [up; gate] = W13 x (halves in the order of `layout`),  h = g' sigmoid(alpha g') (u' + beta),  y = W2 h,
+ *   g' = min(gate, limit),  u' = clamp(up, -limit, limit).
+ * Both projections, the activation and its product are one kernel; sums are fp32.  h is rounded to the
+ * operand type between the two products.
+ * Limits: 1 <= H, I <= 2^20, max_rows <= 2^24.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (type). */
+typedef struct moe_ff_s moe_ff_t;
+moe_status moe_ff_plan(int H, int I, int dtype, int layout, float limit, float alpha, float beta,
+                       int max_rows, moe_ff_t** out);
+/* Bytes of the scratch buffer of both passes (256-byte aligned, caller-owned). */
+moe_status moe_ff_scratch_bytes(const moe_ff_t* plan, size_t* bytes);
+/* y [M, H] of x [M, H], w13 [2 I, H], w2 [H, I] (row strides ld*).
+ *   scratch  as for moe_grouped_run: its first 4096 bytes zero before the first use, calls that share it
+ *            stream-ordered, moe_ff_get_device_error after a device error.
+ *   pre, h   NULL, or [M, 2 I] and [M, I] (contiguous), which get up and gate in w13's order and h: what
+ *            moe_ff_backward needs.  pre is rounded to the operand type, on the side of the limit where
+ *            the fp32 value was, so that the backward pass clamps what the forward pass clamped.
+ * y, pre and h must not overlap an input or one another.
+ * Products whose operands and strides are 16-byte aligned run on the tensor cores; others (for instance
+ * H % 8 != 0) on the CUDA cores, slower.
+ * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (M > max_rows), MOE_ERR_CUDA. */
+moe_status moe_ff_forward(const moe_ff_t* plan, void* scratch, size_t scratch_bytes, const void* x,
+                          long long ldx, const void* w13, long long ldw13, const void* w2, long long ldw2,
+                          void* pre, void* h, void* y, long long ldy, int M, void* stream);
+/* Gradients of y at dy [M, H]: dx [M, H], dw13 [2 I, H], dw2 [H, I], each NULL where it is not wanted (and
+ * what only it needs may be NULL then: x for dw13, w13 for dx, h for dw2, w2 and pre for dx and dw13).
+ *   dh = dy W2,  du = dh g' s [|up| <= limit],  dg = dh (u' + beta) (s + alpha g' s (1 - s)) [gate <= limit],
+ *   s = sigmoid(alpha g');  dx = [du, dg] W13,  dw13 = [du, dg]^T x,  dw2 = dy^T h.
+ * dh stays in fp32; du and dg are rounded to the operand type before the two products over them.
+ * Gradients are written, not added to; with M == 0 dw13 and dw2 are zeros.  The outputs must not overlap
+ * an input or one another.  Errors as moe_ff_forward. */
+moe_status moe_ff_backward(const moe_ff_t* plan, void* scratch, size_t scratch_bytes, const void* dy,
+                           long long lddy, const void* x, long long ldx, const void* w13, long long ldw13,
+                           const void* w2, long long ldw2, const void* pre, const void* h, void* dx,
+                           long long lddx, void* dw13, long long lddw13, void* dw2, long long lddw2, int M,
+                           void* stream);
+/* As moe_grouped_get_device_error. */
+moe_status moe_ff_get_device_error(const moe_ff_t* plan, void* scratch, void* stream, int* code);
+void moe_destroy_ff(moe_ff_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

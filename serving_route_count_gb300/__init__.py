@@ -2,7 +2,8 @@
 
 The compute path lives in ``libmoe_gb300.so`` (hand-written CUDA, C ABI in
 ``include/moe_gb300.h``); ``moe`` is its Python binding (argument marshalling only), ``block``
-that of the 16-bit block around the experts (router, grouping, grouped products, norms).
+that of the 16-bit block around the experts (router, grouping, grouped products, norms), ``fp8`` that
+of the 8-bit products with block scales, ``feed_forward`` that of the dense gated feed-forward block.
 """
 from .moe import (  # noqa: F401
     MoEError, MoELayer, moe_plan_weights, moe_prepared_bytes, moe_prepare_weights, moe_unprepare_weights, moe_plan,
@@ -20,4 +21,11 @@ from .block import (  # noqa: F401
     moe_block_norm_set_wait_probe, moe_block_norm_get_device_error,
     MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID,
     MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_NORM_RMS, MOE_NORM_LAYER,
+)
+from .fp8 import (  # noqa: F401
+    MoEFp8, moe_fp8_quant, moe_fp8_plan, moe_fp8_scratch_bytes, moe_fp8_get_device_error, moe_destroy_fp8,
+    MOE_FP8_ROWS, MOE_FP8_TILES,
+)
+from .feed_forward import (  # noqa: F401
+    MoEFeedForward, moe_ff_plan, moe_ff_scratch_bytes, moe_ff_get_device_error, moe_destroy_ff,
 )

@@ -93,6 +93,27 @@ SIGNATURES = {
     "moe_block_norm_set_wait_probe": (c_int, [ctypes.c_ulonglong]),
     "moe_block_norm_get_device_error": (c_int, [c_void_p, c_int_p]),
     "moe_block_norm": (c_int, [c_void_p, c_void_p]),
+    "moe_fp8_quant": (c_int, [c_void_p, c_int, c_longlong, c_int, c_int, c_int, c_int, c_void_p,
+                              c_longlong, c_void_p, c_longlong, c_void_p]),
+    "moe_fp8_plan": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_float, c_float, c_int,
+                             ctypes.POINTER(c_void_p)]),
+    "moe_fp8_scratch_bytes": (c_int, [c_void_p, c_size_t_p]),
+    "moe_fp8_run": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_int, c_void_p,
+                            c_longlong, c_void_p, c_longlong, c_void_p, c_void_p, c_void_p, c_int,
+                            c_void_p, c_longlong, c_int, c_void_p]),
+    "moe_fp8_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
+    "moe_destroy_fp8": (None, [c_void_p]),
+    "moe_ff_plan": (c_int, [c_int, c_int, c_int, c_int, c_float, c_float, c_float, c_int,
+                            ctypes.POINTER(c_void_p)]),
+    "moe_ff_scratch_bytes": (c_int, [c_void_p, c_size_t_p]),
+    "moe_ff_forward": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_void_p, c_longlong,
+                               c_void_p, c_longlong, c_void_p, c_void_p, c_void_p, c_longlong, c_int,
+                               c_void_p]),
+    "moe_ff_backward": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_void_p, c_longlong,
+                                c_void_p, c_longlong, c_void_p, c_longlong, c_void_p, c_void_p, c_void_p,
+                                c_longlong, c_void_p, c_longlong, c_void_p, c_longlong, c_int, c_void_p]),
+    "moe_ff_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
+    "moe_destroy_ff": (None, [c_void_p]),
 }
 
 _LIB = None
