@@ -11,6 +11,11 @@ namespace moe {
 int report_cuda(cudaError_t e);
 // gemm_ff_simt.cu
 cudaError_t launch_ff_simt(const FfDims& d, const FfGemm& g, int epilogue, cudaStream_t st);
+// gemm_ff_tc.cu
+size_t ff_tc_part_bytes();
+bool ff_tc_addressable(const FfGemm& g);
+cudaError_t launch_ff_tc(const FfDims& d, const FfGemm& g, int epilogue, float* part, int32_t* tickets,
+                         cudaStream_t st);
 }  // namespace moe
 
 using namespace moe;
@@ -25,7 +30,10 @@ namespace {
 moe_status status(cudaError_t e) { return static_cast<moe_status>(report_cuda(e)); }
 
 cudaError_t product(const moe_ff_s& f, const FfGemm& g, int epilogue, cudaStream_t st) {
-  return launch_ff_simt(f.d, g, epilogue, st);
+  if (!ff_tc_addressable(g)) return launch_ff_simt(f.d, g, epilogue, st);
+  uint8_t* base = reinterpret_cast<uint8_t*>(g.err);      // the scratch buffer begins with the error word
+  return launch_ff_tc(f.d, g, epilogue, reinterpret_cast<float*>(base + kGtPartAt),
+                      reinterpret_cast<int32_t*>(base + kGtTicketsAt), st);
 }
 
 bool scratch_ok(const moe_ff_s& f, const void* scratch, size_t bytes) {
@@ -49,7 +57,7 @@ moe_status moe_ff_plan(int H, int I, int dtype, int layout, float limit, float a
   moe_ff_s* f = new (std::nothrow) moe_ff_s();
   if (f == nullptr) return MOE_ERR_ARG;
   f->d = FfDims{H, I, dtype, layout, max_rows, limit, alpha, beta, 0};
-  f->rows_at = kGtPartAt;
+  f->rows_at = kGtPartAt + ff_tc_part_bytes();
   // h [M, I] of a forward pass, d(up, gate) [M, 2 I] of a backward one
   f->bytes = f->rows_at + align_up((size_t)max_rows * 2 * I * 2, 256);
   *out = f;
