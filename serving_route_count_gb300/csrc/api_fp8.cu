@@ -14,6 +14,11 @@ cudaError_t launch_fp8_quant(const void* x, int dtype, long long ldx, int E, int
                              uint8_t* q, long long ldq, float* scale, long long lds, cudaStream_t st);
 // gemm_fp8_simt.cu
 cudaError_t launch_fp8_simt(const GroupedDims& d, const Fp8Call& f, cudaStream_t st);
+// gemm_fp8_tc.cu
+size_t fp8_tc_part_bytes(int S, int E);
+bool fp8_tc_addressable(const GroupedDims& d, const Fp8Call& f);
+cudaError_t launch_fp8_tc(const GroupedDims& d, const Fp8Call& f, float* part, int32_t* tickets,
+                          cudaStream_t st);
 }  // namespace moe
 
 using namespace moe;
@@ -62,7 +67,7 @@ moe_status moe_fp8_plan(int E, int N, int K, int dtype, int act, int layout, flo
   moe_fp8_s* g = new (std::nothrow) moe_fp8_s();
   if (g == nullptr) return MOE_ERR_ARG;
   g->d = GroupedDims{E, N, K, dtype, act, layout, max_rows, limit, alpha, beta, 0};
-  g->bytes = kGtPartAt;
+  g->bytes = kGtPartAt + fp8_tc_part_bytes(max_rows, E);
   *out = g;
   return MOE_OK;
 }
@@ -94,7 +99,10 @@ moe_status moe_fp8_run(const moe_fp8_t* plan, void* scratch, size_t scratch_byte
   const Fp8Call f{{x, ldx, x_rows, w, ldw, offsets, perm, topk, out, ldo, S, static_cast<int32_t*>(scratch)},
                   x_scale, ldxs, w_scale};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return status(launch_fp8_simt(d, f, st));
+  if (!fp8_tc_addressable(d, f)) return status(launch_fp8_simt(d, f, st));
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  return status(launch_fp8_tc(d, f, reinterpret_cast<float*>(base + kGtPartAt),
+                              reinterpret_cast<int32_t*>(base + kGtTicketsAt), st));
 }
 
 moe_status moe_fp8_get_device_error(const moe_fp8_t* plan, void* scratch, void* stream, int* code) {

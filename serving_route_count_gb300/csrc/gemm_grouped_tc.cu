@@ -128,51 +128,13 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   pdl_wait_prev();
   pdl_launch_next();
 
-  // the experts' tiles: thread t owns experts 4 t .. 4 t + 3.  Offsets that are out of order or range
-  // make the call empty (every CTA sees the same ones), so that no tile is ever out of its bounds.
-  int cnt[4], bad = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = 4 * tid + i;
-    cnt[i] = 0;
-    if (e < E) {
-      const int a = p.c.offsets[e], b = p.c.offsets[e + 1];
-      if (a < 0 || b < a || b > p.c.S)
-        bad = 1;
-      else
-        cnt[i] = b - a;
-      s_off[e] = a;
-      s_cnt[e] = cnt[i];
-      if (Cfg::kSorts) s_expert[e] = e;
-    }
-    if (e >= E && e < 1024) s_tile[e] = 0x7FFFFFFF;
+  // the experts' tiles
+  int cnt[4];
+  const int bad = gt_counts(p.c.offsets, E, p.c.S, cnt, s_off, s_cnt, s_tile);
+  if constexpr (Cfg::kSorts) {
+    for (int e = tid; e < E; e += kGtThreads) s_expert[e] = e;
   }
-  bad = __syncthreads_or(bad);
-  // numbers the tiles in the tables' order; their total
-  const auto number = [&]() {
-    int tiles = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tiles += cdiv(cnt[i], BN);
-    int incl = tiles;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    int before = incl - tiles, total = 0;
-#pragma unroll
-    for (int w = 0; w < kGtThreads / 32; ++w) {
-      if (w < warp) before += s_warp[w];
-      total += s_warp[w];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * tid + i < E) s_tile[4 * tid + i] = before;
-      before += cdiv(cnt[i], BN);
-    }
-    return total;
-  };
+  const auto number = [&]() { return gt_number<BN, kGtThreads>(cnt, E, s_tile, s_warp); };
   int total = number();
   bool sorted = false;
   if constexpr (Cfg::kSorts) {
@@ -241,7 +203,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
   if (warp == 0) {
     const uint32_t bar0 = map_rank(&full[0], 0);
     while (ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, Cfg::kSorts ? s_expert : nullptr, lane);
       const int accs = accs_of(rb);
       const int rows = p.c.perm != nullptr ? un.nhalf : cdiv(un.nhalf, Cfg::kChunk) * Cfg::kChunk;
       const uint32_t bytes = 2u * (accs * Cfg::kBytesW + rows * 128);
@@ -288,7 +250,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     if (p.d.probe_ns != 0 && blockIdx.x == 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tfull[0], 0, err, p.d.probe_ns));
     while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, Cfg::kSorts ? s_expert : nullptr, lane);
       const int accs = accs_of(rb);
       const int b0 = Cfg::kAcc == 2 ? 0 : seg & 1;
       for (int c = 0; ok && c < accs; ++c)
@@ -335,7 +297,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     int f[4] = {0, 0, 0, 0};
     GtTile un = {};
     const auto look_up = [&](int tile) {
-      un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
+      un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, Cfg::kSorts ? s_expert : nullptr, lane);
       if (p.c.perm != nullptr) {
         const int first = un.p0 + (int)rank * un.nhalf + 4 * tl;
 #pragma unroll
@@ -394,7 +356,7 @@ grouped_tc_kernel(const __grid_constant__ GtParams p) {
     const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
     for (int seg = 0; ok && work.next(u, tile, rb, k0, len); ++seg) {
       if (Cfg::kAcc == 2 ? g >= accs_of(rb) : (seg & 1) != g) continue;
-      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, s_expert, lane);
+      const GtTile un = gt_tile<BN>(tile, s_tile, s_off, s_cnt, Cfg::kSorts ? s_expert : nullptr, lane);
       const int acc = Cfg::kAcc == 2 ? g : 0;
       const int col0 = unit_col(rb) + acc * 2 * kRows + (int)rank * kRows;
       ok = mbar_wait_warp(&tfull[g], uses & 1, err);

@@ -100,9 +100,61 @@ template <int BN>
 __device__ __forceinline__ int gt_size(int cnt, int tiles) {
   return tiles > 1 ? 16 * cdiv(cdiv(cnt, tiles), 16) : BN;
 }
+// Rows of the experts, by all threads of a CTA: thread t owns experts 4 t .. 4 t + 3 (cnt), the tables
+// s_off and s_cnt get all of them, s_tile what lies past E.  Offsets that are out of order or range make
+// the call empty (every CTA sees the same ones; the result is true), so that no tile is ever out of
+// its bounds.  offsets NULL: one expert, all S rows.
+__device__ __forceinline__ int gt_counts(const int32_t* offsets, int E, int S, int (&cnt)[4], int* s_off,
+                                         int* s_cnt, int* s_tile) {
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * (int)threadIdx.x + i;
+    cnt[i] = 0;
+    if (e < E) {
+      const int a = offsets != nullptr ? offsets[e] : 0, b = offsets != nullptr ? offsets[e + 1] : S;
+      if (a < 0 || b < a || b > S)
+        bad = 1;
+      else
+        cnt[i] = b - a;
+      s_off[e] = a;
+      s_cnt[e] = cnt[i];
+    }
+    if (e >= E && e < 1024) s_tile[e] = 0x7FFFFFFF;
+  }
+  return __syncthreads_or(bad);
+}
+// Numbers the experts' tiles in the tables' order (s_tile); their total.  s_warp: an int for each warp.
+template <int BN, int THREADS>
+__device__ __forceinline__ int gt_number(const int (&cnt)[4], int E, int* s_tile, int* s_warp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int tiles = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tiles += cdiv(cnt[i], BN);
+  int incl = tiles;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int before = incl - tiles, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (4 * tid + i < E) s_tile[4 * tid + i] = before;
+    before += cdiv(cnt[i], BN);
+  }
+  return total;
+}
+
 // A tile's expert and token range (by a whole warp).  s_tile[i]: tiles before the
 // tables' expert i, 1024 entries; the tile's is the last one with s_tile[i] <= tile, found by two
-// 32-way comparisons.  s_expert: the experts' numbers (BN = 256; else the tables are in their order).
+// 32-way comparisons.  s_expert: the experts' numbers, NULL where the tables are in their order.
 template <int BN>
 __device__ __forceinline__ GtTile gt_tile(int tile, const int* s_tile, const int* s_off,
                                           const int* s_cnt, const int* s_expert, int lane) {
@@ -110,7 +162,7 @@ __device__ __forceinline__ GtTile gt_tile(int tile, const int* s_tile, const int
   const int lo = __popc(__ballot_sync(0xffffffffu, s_tile[32 * hi + lane] <= tile)) - 1;
   GtTile r;
   const int i = 32 * hi + lo;
-  r.e = BN == 256 ? s_expert[i] : i;
+  r.e = s_expert != nullptr ? s_expert[i] : i;
   const int t = tile - s_tile[i], cnt = s_cnt[i], size = gt_size<BN>(cnt, cdiv(cnt, BN));
   r.p0 = s_off[i] + t * size;
   r.n = min(size, cnt - t * size);
