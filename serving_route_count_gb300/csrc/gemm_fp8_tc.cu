@@ -10,15 +10,16 @@
 // Two forms, by the tile's tokens:
 //   up to 128: weight rows are the MMA's M operand and tokens its N operand, so one token still streams its
 //     weights through full-size MMAs.  A lane holds one weight row; the tokens' scales (times the
-//     row's) pass through shared memory, four steps at a time.
+//     row's) pass through shared memory, four steps at a time, from two warps of their own.
 //   256: tokens are M and weight rows N.  A lane holds one token and 128 weight rows, all of one scale (two for
 //     a SwiGLU), so a step costs it one factor and 64 packed FMAs; with the scales read from shared
 //     memory, as above, those reads and the MMA's operands would share its bandwidth at par.
 //     The 128 sums of a thread and what is in flight need 208 registers: the other warps give theirs
 //     up (setmaxnreg).
 //
-// Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-7 token copies (tiles, or gathers of
-// four rows by index; warp 3 also allocates the tensor memory), warps 8-15 epilogue.
+// Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-5 or 2-7 token copies (tiles, or
+// gathers of four rows by index; warp 3 also allocates the tensor memory, warp 2 asks for the next
+// unit's weight scales), warps 6 and 7 scales up to 128 tokens, warps 8-15 epilogue.
 #include <type_traits>
 
 #include "block_ops.cuh"
@@ -32,7 +33,6 @@ namespace moe {
 using namespace tc;
 
 constexpr int kF8Threads = 512;
-constexpr int kF8TokenWarps = 6;         // warps 2-7
 constexpr int kF8K = kFp8Block;          // K step: one block of scales, one 128-byte swizzled row
 constexpr int kF8RegsLaunch = 128;       // of a thread, as ptxas reports and the host checks
 
@@ -41,7 +41,7 @@ struct F8Cfg {
   static constexpr bool kTokenRows = BN == 256;              // tokens are the MMA's M operand
   // registers shared out anew by role: a thread's of the epilogue warps and of the others
   static constexpr bool kSplit = BN >= 128;
-  static constexpr int kRegsMore = BN == 256 ? 208 : 152, kRegsLess = 256 - kRegsMore;
+  static constexpr int kRegsMore = BN == 256 ? 208 : 184, kRegsLess = 256 - kRegsMore;
   static_assert(256 * (kRegsMore + kRegsLess) <= kF8Threads * kF8RegsLaunch, "register split");
   static constexpr int kHalf = BN / 2;                       // tokens a CTA loads
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;     // tokens per tile copy
@@ -51,9 +51,11 @@ struct F8Cfg {
   static constexpr int kGroups = BN == 32 ? 1 : 2;           // groups of four epilogue warps
   static constexpr int kWide = BN == 32 ? 32 : BN / 2;       // accumulator columns of a group
   static constexpr int kSets = ACT ? 2 : 1;                  // scales of a lane's column: up and gate
-  static constexpr int kPad = kWide + 4;                     // both sets' words in other banks
-  // scales of four steps, double-buffered, of each group
-  static constexpr int kScales = kTokenRows ? 0 : kGroups * 2 * 4 * kSets * kPad * 4;
+  static constexpr int kTokenWarps = kTokenRows ? 6 : 4;     // from warp 2 on
+  // ring of the tokens' scales: slots of four steps, each [4][sets][kPad]
+  static constexpr int kPad = BN + 4;                        // both sets' words in other banks
+  static constexpr int kSlots = 3, kSlot = 4 * kSets * kPad;
+  static constexpr int kScales = kTokenRows ? 0 : kSlots * kSlot * 4;
   static constexpr int kTables = 3 * 1028 * 4 + 512 + kScales;
   static constexpr int kStages = (227 * 1024 - 1024 - kTables) / kStage > 12
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
@@ -75,6 +77,13 @@ struct F8Params {
   int packed, vec;      // output rows on 4 bytes, on 16
   int whole16;          // SwiGLU weights by whole 16-row groups: one 5-d copy per K step
 };
+
+// Asks for the scales of the next unit's weight rows (up to four rows of KT) in L2: from DRAM under load
+// they would take longer than the steps that a fetch is ahead.
+__device__ __forceinline__ void f8_prefetch(const float* row, int n, int line) {
+  const char* at = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)127) + 128 * line;
+  if (at < reinterpret_cast<const char*>(row + n)) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
 
 // One verdict for the 128 threads of a group, at its named barrier.
 __device__ __forceinline__ bool f8_group_all(int group, bool ok) {
@@ -139,14 +148,16 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
   uint64_t* empty = full + S;          // [S]
   uint64_t* tfull = empty + S;         // [NB] a step's product is ready
   uint64_t* tempty = tfull + NB;       // [NB] and has been read (leader's are used)
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + NB);
+  uint64_t* sfull = tempty + NB;       // [slots] scales of four steps are there
+  uint64_t* sempty = sfull + Cfg::kSlots;   // [slots] and have been read
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sempty + Cfg::kSlots);
   int* s_flag = reinterpret_cast<int*>(s_tmem + 1);   // [2]
   int* s_warp = s_flag + 2;            // [warps]
   int* s_fills = s_warp + kF8Threads / 32;   // fills whose stage the weight warp has found empty
   int* s_off = reinterpret_cast<int*>(st + S * Cfg::kStage + 512);
   int* s_cnt = s_off + 1028;
   int* s_tile = s_cnt + 1028;
-  float* s_scale = reinterpret_cast<float*>(s_tile + 1028);   // [groups][2][4 steps][sets][kPad]
+  float* s_scale = reinterpret_cast<float*>(s_tile + 1028);   // [slots][4 steps][sets][kPad]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, G = gridDim.x >> 1;
@@ -165,6 +176,10 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     for (int b = 0; b < NB; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 8 * Cfg::kGroups);        // the epilogue warps of both CTAs
+    }
+    for (int b = 0; b < Cfg::kSlots; ++b) {
+      mbar_init(&sfull[b], 2);
+      mbar_init(&sempty[b], 4 * Cfg::kGroups);
     }
     fence_barrier_init();
     *s_fills = 0;
@@ -209,7 +224,18 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     }
   };
   const auto tile_at = [&](int tile) { return gt_tile<BN>(tile, s_tile, s_off, s_cnt, nullptr, lane); };
-  if (warp < 2 + kF8TokenWarps) {
+  // row of x at position pos; a bad entry sets the error word where its row is copied
+  const auto row_of = [&](int pos) {
+    if (p.c.perm == nullptr) return pos;
+    const int f = p.c.perm[pos], r = f < 0 ? 0 : f / p.c.topk;
+    return r < p.c.x_rows ? r : 0;
+  };
+  // scales of set h of weight rows r .. of one tile row (a row past the matrix takes its last tile's)
+  const auto scales_of = [&](int e, int h, int r) {
+    const int half = p.tall / Cfg::kSets;
+    return p.ws + ((size_t)e * p.tall + h * half + min(r / kFp8Block, half - 1)) * p.KT;
+  };
+  if (warp < 8) {
   if constexpr (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsLess));
   if (warp == 0) {
     const uint32_t bar0 = map_rank(&full[0], 0);
@@ -277,8 +303,8 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         advance();
       }
     }
-  } else {
-    const int tl = lane * kF8TokenWarps + (warp - 2);
+  } else if (warp < 2 + Cfg::kTokenWarps) {
+    const int tl = lane * Cfg::kTokenWarps + (warp - 2);
     const uint32_t bar0 = map_rank(&full[0], 0);
     // rows 4 tl .. 4 tl + 3 of this CTA's tokens by permutation (past the tile its last row again);
     // a unit's entries are loaded under the copies of the one before it
@@ -290,6 +316,11 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         const int first = un.p0 + (int)rank * un.nhalf + 4 * tl;
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = p.c.perm[min(first + i, un.p0 + un.n - 1)];
+      }
+      if (warp == 2) {
+        const int h = (lane >> 3) & 1, of = lane >> 4;   // set, and the CTA whose weight rows (tokens as M: both)
+        if (h < Cfg::kSets && (Cfg::kTokenRows || of == (int)rank))
+          f8_prefetch(scales_of(un.e, h, (2 * rb + of) * kRows) + k0, len, lane & 7);
       }
     };
     // A warp may have no copy in a unit, and then nothing waits for it: it goes by the weight warp's
@@ -335,29 +366,84 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
       }
       fill += steps;
     }
+  } else if constexpr (!Cfg::kTokenRows) {
+    // Scales of the tokens' columns: warp 6 columns 0 .. 31 and 64 .. 95, warp 7 the others.  Those of the next
+    // four steps, of the next unit too, are on their way while these wait for their slot.
+    constexpr int M = (BN + 63) / 64, SETS = Cfg::kSets;
+    const int c0 = (warp - 6) * 32 + lane;
+    float nx[M][4], nw[SETS][4];
+    const float* xs[M];
+    const float* w[SETS];
+    int i0 = 0, n = 0, slot = 0;
+    uint32_t turn = 0;
+    len = 0;
+    const auto fetch = [&]() {         // steps of the block that it asks for, 0 at the end
+      i0 += n;
+      if (i0 >= len) {
+        if (!work.next(u, tile, rb, k0, len)) return 0;
+        const GtTile un = tile_at(tile);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          xs[m] = p.xs + row_of(un.p0 + min(c0 + 64 * m, un.n - 1)) * p.ldxs + k0;
+#pragma unroll
+        for (int h = 0; h < SETS; ++h) w[h] = scales_of(un.e, h, (2 * rb + (int)rank) * kRows) + k0;
+        i0 = 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = min(i0 + j, len - 1);
+#pragma unroll
+        for (int m = 0; m < M; ++m) nx[m][j] = xs[m][i];
+#pragma unroll
+        for (int h = 0; h < SETS; ++h) nw[h][j] = w[h][i];
+      }
+      return min(4, len - i0);
+    };
+    n = fetch();
+    while (ok && n > 0) {
+      float now[M][SETS][4];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int h = 0; h < SETS; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) now[m][h][j] = nx[m][j] * nw[h][j];
+      n = fetch();
+      ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
+      if (!ok) break;
+      float* to = s_scale + slot * Cfg::kSlot + c0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < SETS; ++h)
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+            if (c0 + 64 * m < BN) to[(j * SETS + h) * Cfg::kPad + 64 * m] = now[m][h][j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull[slot]);
+      if (++slot == Cfg::kSlots) {
+        slot = 0;
+        ++turn;
+      }
+    }
   }
   } else {
     if constexpr (Cfg::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsMore));
-    const int g = (warp - 2 - kF8TokenWarps) >> 2;
     // groups of four warps share the columns of every step
     constexpr int CW = Cfg::kWide, SETS = Cfg::kSets;
-    const int q = warp & 3, t = q * 32 + lane;
+    const int q = warp & 3, g = (warp - 8) >> 2, t = q * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + g * CW;
     const uint32_t bempty = map_rank(&tempty[0], 0);
     const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
-    uint32_t step = 0, blocks = 0;
+    // a step's buffer has been read
+    const auto release = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_read(bempty + 8 * b);
+    };
+    uint32_t step = 0, turn = 0;
+    int slot = 0;
     uint64_t acc[CW / 2];
-    // row of x at position pos of the tile; a bad entry has set the error word already
-    const auto row_of = [&](int pos) {
-      if (p.c.perm == nullptr) return pos;
-      const int f = p.c.perm[pos], r = f < 0 ? 0 : f / p.c.topk;
-      return r < p.c.x_rows ? r : 0;
-    };
-    // scales of set h of weight rows r .. of one tile row (a row past the matrix takes its last tile's)
-    const auto scales_of = [&](int e, int h, int r) {
-      const int half = p.tall / SETS;
-      return p.ws + ((size_t)e * p.tall + h * half + min(r / kFp8Block, half - 1)) * p.KT;
-    };
     // this group's sums, or those of all pieces of a cut unit, to the output
     const auto store = [&](const GtTile& un) {
       if constexpr (Cfg::kTokenRows) {
@@ -379,13 +465,16 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         }
       }
     };
-    // Where a group meets at barriers in every unit, a warp whose wait gave up goes on to the next one,
-    // and there all four end.
-    bool over = g >= Cfg::kGroups;
-    while (!over && work.next(u, tile, rb, k0, len)) {
+    while (ok && g < Cfg::kGroups && work.next(u, tile, rb, k0, len)) {
       const GtTile un = tile_at(tile);
 #pragma unroll
       for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
+      uint32_t v[2][32];
+      const auto add = [&](int j, const uint64_t (&f)[SETS]) {     // 32 columns, one factor (two: by 16)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          fma_pair_f32(acc[16 * j + i], pair_f32(v[j & 1][2 * i], v[j & 1][2 * i + 1]), f[ACT ? i / 8 : 0]);
+      };
       if constexpr (Cfg::kTokenRows) {
         const float* xs = p.xs + row_of(un.p0 + min((int)rank * un.nhalf + t, un.n - 1)) * p.ldxs + k0;
         const float* w[SETS];
@@ -413,89 +502,65 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
           ok = mbar_wait_warp(&tfull[b], (step / NB) & 1, err);
           if (!ok) break;
           tc_fence_after();
-          uint32_t v[2][16];
-          tmem_ld16_start(at, v[0]);
-#pragma unroll
-          for (int j = 0; j < CW / 16; ++j) {
-            tmem_ld16_wait(v[j & 1]);
-            if (j + 1 < CW / 16) {
-              tmem_ld16_start(at + 16 * (j + 1), v[(j + 1) & 1]);
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(bempty + 8 * b);
-            }
-#pragma unroll
-            for (int i2 = 0; i2 < 8; ++i2)
-              fma_pair_f32(acc[8 * j + i2], pair_f32(v[j & 1][2 * i2], v[j & 1][2 * i2 + 1]), f[ACT ? j & 1 : 0]);
-          }
+          // 64 columns at a time in flight: a wait takes all loads that have been started
+          tmem_ld32_start(at, v[0]);
+          tmem_ld32_start(at + 32, v[1]);
+          tmem_ld_wait(v[0]);
+          tmem_after_wait(v[1]);
+          add(0, f);
+          tmem_ld32_start(at + 64, v[0]);
+          add(1, f);
+          tmem_ld32_start(at + 96, v[1]);
+          tmem_ld_wait(v[0]);
+          tmem_after_wait(v[1]);
+          release(b);
+          add(2, f);
+          add(3, f);
         }
       } else {
-        const int c = g * CW + t;
-        const bool mine = t < CW && c < un.n;            // this thread's column has a token
-        const float* xs = p.xs;
-        const float* w[SETS];
-        if (mine) xs += row_of(un.p0 + c) * p.ldxs + k0;
-#pragma unroll
-        for (int h = 0; h < SETS; ++h) w[h] = scales_of(un.e, h, (2 * rb + (int)rank) * kRows) + k0;
-        float* sc = s_scale + g * (2 * 4 * SETS * Cfg::kPad);
-        float nx[4], nw[SETS][4];
-        const auto fetch = [&](int i0) {
-          if (mine)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int i = min(i0 + j, len - 1);
-              nx[j] = xs[i];
-#pragma unroll
-              for (int h = 0; h < SETS; ++h) nw[h][j] = w[h][i];
-            }
-        };
-        fetch(0);
-        for (int i0 = 0; i0 < len; i0 += 4, ++blocks) {
-          // scales of four steps; the buffer's last readers are past the barrier of the block before
-          float* now = sc + (blocks & 1) * (4 * SETS * Cfg::kPad);
-          if (t < CW)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int h = 0; h < SETS; ++h) now[(j * SETS + h) * Cfg::kPad + t] = mine ? nx[j] * nw[h][j] : 0.f;
-          if (i0 + 4 < len) fetch(i0 + 4);
-          ok = f8_group_all(g, ok);
-          if (!ok) {
-            over = true;
-            break;
-          }
-          const float* mine4 = now + (ACT && lane >= 16 ? Cfg::kPad : 0);
+        for (int i0 = 0; ok && i0 < len; i0 += 4) {
+          ok = mbar_wait_warp(&sfull[slot], turn & 1, err);
+          const float* now = s_scale + slot * Cfg::kSlot + g * CW + (ACT && lane >= 16 ? Cfg::kPad : 0);
 #pragma unroll 1
-          for (int j = 0; j < 4 && i0 + j < len; ++j, ++step) {
-            const uint32_t b = step % NB, at = trow + b * BN;
-            if (ok) ok = mbar_wait_warp(&tfull[b], (step / NB) & 1, err);
-            if (!ok) continue;                           // up to the next barrier, where the group learns of it
-            tc_fence_after();
-            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(mine4 + j * SETS * Cfg::kPad);
+          for (int j = 0; ok && j < 4 && i0 + j < len; ++j, ++step) {
+            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(now + j * SETS * Cfg::kPad);
+            ulonglong2 s4[8];
 #pragma unroll
-            for (int c0 = 0; c0 < CW; c0 += 32) {
-              if (g * CW + c0 < un.n) {
-                float v[32];
-                tmem_ld32(at + c0, v);
+            for (int i = 0; i < 8; ++i) s4[i] = f[i];
+            const uint32_t b = step % NB, at = trow + b * BN;
+            ok = mbar_wait_warp(&tfull[b], (step / NB) & 1, err);
+            if (!ok) break;
+            tc_fence_after();
+            if (g * CW < un.n) {
+              tmem_ld32_start(at, v[0]);
+              if (CW == 64) tmem_ld32_start(at + 32, v[1]);
+              tmem_ld_wait(v[0]);
+              if (CW == 64) tmem_after_wait(v[1]);
+            }
+            release(b);
+            if (g * CW < un.n) {
+#pragma unroll
+              for (int h = 0; h < CW / 32; ++h) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const ulonglong2 s4 = f[c0 / 4 + i];
-                  fma_pair_f32(acc[c0 / 2 + 2 * i], pair_f32(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1])), s4.x);
-                  fma_pair_f32(acc[c0 / 2 + 2 * i + 1], pair_f32(__float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])), s4.y);
+                  fma_pair_f32(acc[16 * h + 2 * i], pair_f32(v[h][4 * i], v[h][4 * i + 1]), s4[i].x);
+                  fma_pair_f32(acc[16 * h + 2 * i + 1], pair_f32(v[h][4 * i + 2], v[h][4 * i + 3]), s4[i].y);
+                  if (h + 1 < CW / 32) s4[i] = f[8 + i];
                 }
               }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(bempty + 8 * b);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+          if (++slot == Cfg::kSlots) {
+            slot = 0;
+            ++turn;
           }
         }
       }
       if (len == p.KT) {
-        if (ok) store(un);
-        if (Cfg::kTokenRows) over = !ok;                 // no barrier from here on: pieces come first
-      } else if (!over) {
+        if (ok) store(un);             // no named barrier from here on: pieces come first
+      } else {
         // one verdict for the four warps: all of them reach the named barriers below, or none
         ok = f8_group_all(g, ok);
         if (!ok) break;
