@@ -356,6 +356,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
     const uint32_t stepr = p.r_mn ? 2048 >> 4 : 32 >> 4, stepc = p.c_mn ? 2048 >> 4 : 32 >> 4;
     uint32_t uses[2] = {0, 0};       // units that each accumulator buffer has held
     int seg = 0;
+    bool ready = false;              // the next step's operands are known to be there
     // nothing commits to this phase before the first unit's MMAs
     if (p.d.probe_ns != 0 && blockIdx.x == 0)
       ok = __all_sync(0xffffffffu, mbar_wait(&tfull[0], 0, err, p.d.probe_ns));
@@ -371,12 +372,14 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
       const uint32_t idesc = idesc_pair16(p.bf16, 2 * nhalf) | (p.r_mn ? 1u << 15 : 0u) | (p.c_mn ? 1u << 16 : 0u);
       uint32_t accumulate = 0;
       for (int i = 0; i < len; ++i) {
-        if (!mbar_wait_warp(&full[s], phase, err)) {
+        if (!ready && !mbar_wait_warp(&full[s], phase, err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
+        const uint32_t s1 = s + 1 == S ? 0 : s + 1;
+        const bool next = mbar_test(&full[s1], phase ^ (s1 == 0));     // of this unit or another
+        if (elect_one()) {
           const uint32_t at = s * (Cfg::kStage >> 4);
 #pragma unroll
           for (int c = 0; c < Cfg::kAcc; ++c) {
@@ -393,9 +396,10 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         }
         accumulate = 1;
         advance();
+        ready = __all_sync(0xffffffffu, next);
       }
       for (int c = 0; c < accs; ++c) {
-        if (lane == 0) tc2_commit(&tfull[b0 + c]);
+        if (elect_one()) tc2_commit(&tfull[b0 + c]);
         ++uses[b0 + c];
       }
       ++seg;

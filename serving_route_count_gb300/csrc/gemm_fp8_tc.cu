@@ -17,9 +17,9 @@
 //     The 128 sums of a thread and what is in flight need 208 registers: the other warps give theirs
 //     up (setmaxnreg).
 //
-// Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-5 or 2-7 token copies (tiles, or
+// Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-5 or 2-6 token copies (tiles, or
 // gathers of four rows by index; warp 3 also allocates the tensor memory, warp 2 asks for the next
-// unit's weight scales), warps 6 and 7 scales up to 128 tokens, warps 8-15 epilogue.
+// unit's weight scales), the others up to warp 7 scales, warps 8-15 epilogue.
 #include <type_traits>
 
 #include "block_ops.cuh"
@@ -36,11 +36,16 @@ constexpr int kF8Threads = 512;
 constexpr int kF8K = kFp8Block;          // K step: one block of scales, one 128-byte swizzled row
 constexpr int kF8RegsLaunch = 128;       // of a thread, as ptxas reports and the host checks
 
+// What a slot of scales says of its steps: how many (0: the work is over), whether the unit ends with them,
+// and the unit: first position, positions, positions of a CTA, weight row block, number, whether it is a piece,
+// expert, first step.
+enum { kF8Steps, kF8Last, kF8P0, kF8N, kF8Half, kF8Rb, kF8Unit, kF8Piece, kF8Expert, kF8K0, kF8Head };
+
 template <int BN, bool ACT>
 struct F8Cfg {
   static constexpr bool kTokenRows = BN == 256;              // tokens are the MMA's M operand
   // registers shared out anew by role: a thread's of the epilogue warps and of the others
-  static constexpr bool kSplit = BN >= 128;
+  static constexpr bool kSplit = true;
   static constexpr int kRegsMore = BN == 256 ? 208 : 184, kRegsLess = 256 - kRegsMore;
   static_assert(256 * (kRegsMore + kRegsLess) <= kF8Threads * kF8RegsLaunch, "register split");
   static constexpr int kHalf = BN / 2;                       // tokens a CTA loads
@@ -51,11 +56,12 @@ struct F8Cfg {
   static constexpr int kGroups = BN == 32 ? 1 : 2;           // groups of four epilogue warps
   static constexpr int kWide = BN == 32 ? 32 : BN / 2;       // accumulator columns of a group
   static constexpr int kSets = ACT ? 2 : 1;                  // scales of a lane's column: up and gate
-  static constexpr int kTokenWarps = kTokenRows ? 6 : 4;     // from warp 2 on
-  // ring of the tokens' scales: slots of four steps, each [4][sets][kPad]
-  static constexpr int kPad = BN + 4;                        // both sets' words in other banks
-  static constexpr int kSlots = 3, kSlot = 4 * kSets * kPad;
-  static constexpr int kScales = kTokenRows ? 0 : kSlots * kSlot * 4;
+  static constexpr int kTokenWarps = kTokenRows ? 5 : 4;     // from warp 2 on
+  static constexpr int kScaleWarps = 6 - kTokenWarps;        // the ones after them
+  // ring of scales: slots of four steps, each [sets][kPad] of the tokens' columns (times the rows'; both
+  // sets' words in other banks), and what they belong to; tokens as M: that alone, a slot for each unit
+  static constexpr int kPad = BN + 4, kStep = kTokenRows ? 0 : kSets * kPad;
+  static constexpr int kSlots = 3, kSlot = 4 * kStep, kScales = kSlots * (kSlot + kF8Head) * 4;
   static constexpr int kTables = 3 * 1028 * 4 + 512 + kScales;
   static constexpr int kStages = (227 * 1024 - 1024 - kTables) / kStage > 12
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
@@ -85,54 +91,34 @@ __device__ __forceinline__ void f8_prefetch(const float* row, int n, int line) {
   if (at < reinterpret_cast<const char*>(row + n)) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
-// One verdict for the 128 threads of a group, at its named barrier.
-__device__ __forceinline__ bool f8_group_all(int group, bool ok) {
-  int all;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %2, 0;\n"
-      " barrier.cta.red.and.pred q, %1, 128, p;\n selp.b32 %0, 1, 0, q;\n}"
-      : "=r"(all)
-      : "r"(1 + group), "r"((int)ok)
-      : "memory");
-  return all != 0;
-}
-
-// Stores a lane's outputs of 128 accumulator columns, tokens in lanes: columns col0 .. of row `row`.
+// Stores a lane's outputs of 32 accumulator columns, tokens in lanes: columns col0 .. of row `row`.
 template <typename T, bool ACT>
-__device__ __forceinline__ void f8_store_row(const F8Params& p, const uint64_t (&acc)[64], long long row, int col0) {
+__device__ __forceinline__ void f8_store_row(const F8Params& p, const float (&x)[32], long long row, int col0) {
   T* o = static_cast<T*>(p.c.out) + row * p.c.ldo + col0;
   const bool up_first = p.d.layout == MOE_W13_UP_GATE;
-  constexpr int kOut = ACT ? 64 : 128;
 #pragma unroll
-  for (int c = 0; c < kOut; c += 8) {
-    float v[8];
+  for (int c = 0; c < (ACT ? 16 : 32); c += 8) {
+    T v[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      if constexpr (ACT) {
-        // outputs 16 b .. 16 b + 15: half 0 in columns 32 b .., half 1 in 32 b + 16 ..
-        const int at = (c / 16) * 32 + c % 16 + j;
-        const float2 a = unpair_f32(acc[at / 2]), b = unpair_f32(acc[at / 2 + 8]);
-        v[j] = swiglu_f32(up_first ? a.x : b.x, up_first ? b.x : a.x, p.d.limit, p.d.alpha, p.d.beta);
-        v[j + 1] = swiglu_f32(up_first ? a.y : b.y, up_first ? b.y : a.y, p.d.limit, p.d.alpha, p.d.beta);
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (ACT) {             // half 0 in the first 16 columns, half 1 in the others
+        const float a = x[c + j], b = x[16 + c + j];
+        v[j] = from_f32<T>(swiglu_f32(up_first ? a : b, up_first ? b : a, p.d.limit, p.d.alpha, p.d.beta));
       } else {
-        const float2 a = unpair_f32(acc[(c + j) / 2]);
-        v[j] = a.x;
-        v[j + 1] = a.y;
+        v[j] = from_f32<T>(x[c + j]);
       }
     }
-    const T t[8] = {from_f32<T>(v[0]), from_f32<T>(v[1]), from_f32<T>(v[2]), from_f32<T>(v[3]),
-                    from_f32<T>(v[4]), from_f32<T>(v[5]), from_f32<T>(v[6]), from_f32<T>(v[7])};
     const int left = p.cols - col0 - c;
     if (p.vec) {
       if (left > 0) {
         uint4 w;
-        memcpy(&w, t, 16);
+        memcpy(&w, v, 16);
         *reinterpret_cast<uint4*>(o + c) = w;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < left) o[c + j] = t[j];
+        if (j < left) o[c + j] = v[j];
     }
   }
 }
@@ -142,22 +128,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 fp8_tc_kernel(const __grid_constant__ F8Params p) {
   using Cfg = F8Cfg<BN, ACT>;
   constexpr int S = Cfg::kStages, NB = Cfg::kBuffers;
+  static_assert(S > NB, "phases");
   extern __shared__ uint8_t raw[];
   uint8_t* st = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(st + S * Cfg::kStage);   // [S] (leader's are used)
-  uint64_t* empty = full + S;          // [S]
-  uint64_t* tfull = empty + S;         // [NB] a step's product is ready
-  uint64_t* tempty = tfull + NB;       // [NB] and has been read (leader's are used)
+  // [S] a step has been multiplied: its stage may be filled again, and its product is ready.  The MMAs are at
+  // most NB < S steps ahead of the epilogue, so no phase passes that it has not waited for.
+  uint64_t* done = full + S;
+  uint64_t* tempty = done + S;         // [NB] a step's product has been read (leader's are used)
   uint64_t* sfull = tempty + NB;       // [slots] scales of four steps are there
   uint64_t* sempty = sfull + Cfg::kSlots;   // [slots] and have been read
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sempty + Cfg::kSlots);
+  uint64_t* gbar = sempty + Cfg::kSlots;    // [2] the four warps of an epilogue group
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(gbar + 2);
   int* s_flag = reinterpret_cast<int*>(s_tmem + 1);   // [2]
-  int* s_warp = s_flag + 2;            // [warps]
+  int* s_total = s_flag + 2;           // tiles of the call
+  int* s_warp = s_total + 1;           // [warps]
   int* s_fills = s_warp + kF8Threads / 32;   // fills whose stage the weight warp has found empty
   int* s_off = reinterpret_cast<int*>(st + S * Cfg::kStage + 512);
   int* s_cnt = s_off + 1028;
   int* s_tile = s_cnt + 1028;
-  float* s_scale = reinterpret_cast<float*>(s_tile + 1028);   // [slots][4 steps][sets][kPad]
+  float* s_scale = reinterpret_cast<float*>(s_tile + 1028);   // [slots][4][kStep]
+  int* s_head = reinterpret_cast<int*>(s_scale + Cfg::kSlots * Cfg::kSlot);   // [slots][kF8Head]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, G = gridDim.x >> 1;
@@ -171,16 +162,16 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&done[s], 1);
     }
     for (int b = 0; b < NB; ++b) {
-      mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 8 * Cfg::kGroups);        // the epilogue warps of both CTAs
     }
     for (int b = 0; b < Cfg::kSlots; ++b) {
-      mbar_init(&sfull[b], 2);
+      mbar_init(&sfull[b], Cfg::kScaleWarps);
       mbar_init(&sempty[b], 4 * Cfg::kGroups);
     }
+    for (int g = 0; g < 2; ++g) mbar_init(&gbar[g], 4);
     fence_barrier_init();
     *s_fills = 0;
   }
@@ -200,6 +191,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     total = 0;
     if (tid == 0) set_error(err, kErrRouteBounds);
   }
+  if (tid == 0) *s_total = total;
   // rows past the last group
   if (p.c.offsets != nullptr) {
     const int end = max(0, min(p.c.S, p.c.offsets[E]));
@@ -235,6 +227,30 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     const int half = p.tall / Cfg::kSets;
     return p.ws + ((size_t)e * p.tall + h * half + min(r / kFp8Block, half - 1)) * p.KT;
   };
+  // the ring of scales, by the warps that fill it
+  int slot = 0;
+  uint32_t turn = 0;
+  const auto head = [&](const GtTile& un, int steps, bool last) {
+    int* h = s_head + slot * kF8Head;
+    h[kF8Steps] = steps;
+    h[kF8Last] = last;
+    h[kF8P0] = un.p0;
+    h[kF8N] = un.n;
+    h[kF8Half] = un.nhalf;
+    h[kF8Rb] = rb;
+    h[kF8Unit] = u;
+    h[kF8Piece] = len != p.KT;
+    h[kF8Expert] = un.e;
+    h[kF8K0] = k0;
+  };
+  const auto publish = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sfull[slot]);
+    if (++slot == Cfg::kSlots) {
+      slot = 0;
+      ++turn;
+    }
+  };
   if (warp < 8) {
   if constexpr (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsLess));
   if (warp == 0) {
@@ -245,7 +261,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
       const uint32_t bytes = 2u * (Cfg::kBytesW + rows * 128);
       const int r = (2 * rb + (int)rank) * kRows;
       for (int x = k0 * kF8K; x < (k0 + len) * kF8K; x += kF8K, ++issued) {
-        if (!mbar_wait_warp(&empty[s], phase ^ 1, err)) {
+        if (!mbar_wait_warp(&done[s], phase ^ 1, err)) {
           ok = false;
           break;
         }
@@ -270,7 +286,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     if (lane == 0) {
       // the last fills have been multiplied: nothing arrives at this CTA's barriers any more
       for (int j = max(0, issued - S); ok && j < issued; ++j)
-        ok = mbar_wait(&empty[j % S], (j / S) & 1, err);
+        ok = mbar_wait(&done[j % S], (j / S) & 1, err);
       if (!ok && rank == 0) drain_stage_loads<S>(full, issued, err);
     }
   } else if (warp == 1) {
@@ -278,18 +294,22 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     const uint64_t desc0 = desc_sw128(st);
     const uint32_t hi = (uint32_t)(desc0 >> 32), lo0 = (uint32_t)desc0;
     uint32_t step = 0;               // steps that have gone to tensor memory
+    bool ready = false;              // the next step's operands and buffer are known to be
     // nothing commits to this phase before the first step's MMAs
     if (p.d.probe_ns != 0 && blockIdx.x == 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(&tfull[0], 0, err, p.d.probe_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait(&done[0], 0, err, p.d.probe_ns));
     while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
       const GtTile un = tile_at(tile);
       const uint32_t idesc = idesc_pair8(Cfg::kTokenRows ? 256 : 2 * un.nhalf);
       for (int i = 0; i < len; ++i, ++step) {
         const uint32_t b = step % NB;
-        ok = mbar_wait_warp(&tempty[b], ((step / NB) & 1) ^ 1, err) && mbar_wait_warp(&full[s], phase, err);
+        if (!ready) ok = mbar_wait2_warp(&tempty[b], ((step / NB) & 1) ^ 1, &full[s], phase, err);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        // the next step, of this unit or another
+        const uint32_t s1 = s + 1 == S ? 0 : s + 1, b1 = (step + 1) % NB;
+        const bool next = mbar_test(&tempty[b1], (((step + 1) / NB) & 1) ^ 1) && mbar_test(&full[s1], phase ^ (s1 == 0));
+        if (elect_one()) {
           const uint32_t lo = lo0 + s * (Cfg::kStage >> 4);
 #pragma unroll
           for (int kb = 0; kb < 4; ++kb) {
@@ -297,10 +317,10 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
             const uint64_t dx = ((uint64_t)hi << 32) | (lo + (Cfg::kBytesW >> 4) + 2 * kb);
             mma2_f8(tmem + b * BN, Cfg::kTokenRows ? dx : dw, Cfg::kTokenRows ? dw : dx, idesc, kb != 0);
           }
-          tc2_commit(&empty[s]);
-          tc2_commit(&tfull[b]);
+          tc2_commit(&done[s]);
         }
         advance();
+        ready = __all_sync(0xffffffffu, next);
       }
     }
   } else if (warp < 2 + Cfg::kTokenWarps) {
@@ -366,7 +386,20 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
       }
       fill += steps;
     }
-  } else if constexpr (!Cfg::kTokenRows) {
+  } else if constexpr (Cfg::kTokenRows) {
+    // tokens as M: units alone, the epilogue warps fetch their few scales themselves
+    while (ok && work.next(u, tile, rb, k0, len)) {
+      const GtTile un = tile_at(tile);
+      ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
+      if (!ok) break;
+      if (lane == 0) head(un, len, true);
+      publish();
+    }
+    if (ok && mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err)) {
+      if (lane == 0) s_head[slot * kF8Head + kF8Steps] = 0;
+      publish();
+    }
+  } else {
     // Scales of the tokens' columns: warp 6 columns 0 .. 31 and 64 .. 95, warp 7 the others.  Those of the next
     // four steps, of the next unit too, are on their way while these wait for their slot.
     constexpr int M = (BN + 63) / 64, SETS = Cfg::kSets;
@@ -374,14 +407,14 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     float nx[M][4], nw[SETS][4];
     const float* xs[M];
     const float* w[SETS];
-    int i0 = 0, n = 0, slot = 0;
-    uint32_t turn = 0;
+    GtTile un = {};
+    int i0 = 0, n = 0;
     len = 0;
     const auto fetch = [&]() {         // steps of the block that it asks for, 0 at the end
       i0 += n;
       if (i0 >= len) {
         if (!work.next(u, tile, rb, k0, len)) return 0;
-        const GtTile un = tile_at(tile);
+        un = tile_at(tile);
 #pragma unroll
         for (int m = 0; m < M; ++m)
           xs[m] = p.xs + row_of(un.p0 + min(c0 + 64 * m, un.n - 1)) * p.ldxs + k0;
@@ -400,7 +433,14 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
       return min(4, len - i0);
     };
     n = fetch();
-    while (ok && n > 0) {
+    while (ok) {
+      ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
+      if (!ok) break;
+      if (warp == 6 && lane == 0) head(un, n, i0 + 4 >= len);
+      if (n == 0) {
+        publish();
+        break;
+      }
       float now[M][SETS][4];
 #pragma unroll
       for (int m = 0; m < M; ++m)
@@ -409,8 +449,6 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) now[m][h][j] = nx[m][j] * nw[h][j];
       n = fetch();
-      ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
-      if (!ok) break;
       float* to = s_scale + slot * Cfg::kSlot + c0;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -418,191 +456,234 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         for (int h = 0; h < SETS; ++h)
 #pragma unroll
           for (int m = 0; m < M; ++m)
-            if (c0 + 64 * m < BN) to[(j * SETS + h) * Cfg::kPad + 64 * m] = now[m][h][j];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sfull[slot]);
-      if (++slot == Cfg::kSlots) {
-        slot = 0;
-        ++turn;
-      }
+            if (c0 + 64 * m < BN) to[j * Cfg::kStep + h * Cfg::kPad + 64 * m] = now[m][h][j];
+      publish();
     }
   }
   } else {
     if constexpr (Cfg::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsMore));
-    // groups of four warps share the columns of every step
+    // Groups of four warps share the columns of every step.  They follow the slots of scales, which say where
+    // units end; nothing of the schedule is kept in their registers.
     constexpr int CW = Cfg::kWide, SETS = Cfg::kSets;
     const int q = warp & 3, g = (warp - 8) >> 2, t = q * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + g * CW;
     const uint32_t bempty = map_rank(&tempty[0], 0);
-    const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
-    // a step's buffer has been read
-    const auto release = [&](uint32_t b) {
+    uint32_t step = 0, at = 0, syncs = 0;
+    int j = 0, steps = 0;              // in the slot
+    uint64_t acc[CW / 2];
+    uint32_t v[2][32];
+    const auto clear = [&]() {
+#pragma unroll
+      for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
+    };
+    // the group's four warps, with a bound like every wait
+    const auto sync_group = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&gbar[g]);
+      return mbar_wait_warp(&gbar[g], syncs++ & 1, err);
+    };
+    // the next slot of scales; false at the end of the work
+    const auto open = [&]() {
+      if (!mbar_wait_warp(&sfull[slot], turn & 1, err)) return false;
+      steps = s_head[slot * kF8Head + kF8Steps];
+      j = 0;
+      return steps > 0;
+    };
+    // the slot's scales have been read
+    const auto leave = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sempty[slot]);
+      if (++slot == Cfg::kSlots) {
+        slot = 0;
+        ++turn;
+      }
+    };
+    // the next step's product
+    const auto begin = [&]() {
+      if (!mbar_wait_warp(&done[s], phase, err)) return false;
+      advance();
+      tc_fence_after();
+      at = trow + (step % NB) * BN;
+      return true;
+    };
+    // the step's buffer has been read
+    const auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_read(bempty + 8 * b);
+      if (lane == 0) mbar_arrive_cluster_read(bempty + 8 * (step % NB));
+      ++step;
     };
-    uint32_t step = 0, turn = 0;
-    int slot = 0;
-    uint64_t acc[CW / 2];
-    // this group's sums, or those of all pieces of a cut unit, to the output
-    const auto store = [&](const GtTile& un) {
+    // 32 of the group's columns to the output
+    const auto store = [&](const int* h, int b, float (&x)[32]) {
+      const int n = h[kF8N];
       if constexpr (Cfg::kTokenRows) {
-        const int i = (int)rank * un.nhalf + t;
-        if (t < un.nhalf && i < un.n) f8_store_row<T, ACT>(p, acc, un.p0 + i, (2 * rb + g) * kRows);
-      } else {
-        const int col0 = (2 * rb + (int)rank) * kRows;
-#pragma unroll
-        for (int j = 0; j < CW / 32; ++j) {
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 f = unpair_f32(acc[16 * j + i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-          }
-          const int c0 = g * CW + 32 * j;
-          if (c0 < un.n) gt_store<T, ACT>(p, v, un, col0, c0, q, lane);
-        }
+        const int i = (int)rank * h[kF8Half] + t;
+        if (t < h[kF8Half] && i < n)
+          f8_store_row<T, ACT>(p, x, h[kF8P0] + i, (2 * h[kF8Rb] + g) * kRows + b * (ACT ? 16 : 32));
+      } else if (g * CW + 32 * b < n) {
+        const GtTile un{0, h[kF8P0], n, h[kF8Half]};
+        gt_store<T, ACT>(p, x, un, (2 * h[kF8Rb] + (int)rank) * kRows, g * CW + 32 * b, q, lane);
       }
     };
-    while (ok && g < Cfg::kGroups && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = tile_at(tile);
+    // The unit's sums to the output; those of a piece to the scratch buffer, and the piece that arrives last
+    // adds them all in K order.
+    const auto finish = [&]() {
+      const int* h = s_head + slot * kF8Head;
+      const int n = h[kF8N];
+      if (h[kF8Piece]) {
+        GtWork w;
+        w.init(*s_total, p.KT, p.RB, 0, gridDim.x >> 1, blockIdx.x >> 1, Cfg::kFixSteps, false);
+        const int unit = h[kF8Unit];
+        const size_t stride = (size_t)2 * BN * 128;      // floats of one slot of the scratch buffer
+        const size_t mine = ((size_t)rank * BN + g * CW) * 128 + t;
+        float* out = p.part + (size_t)w.slot_of(blockIdx.x >> 1, unit) * stride + mine;
+        const int m = Cfg::kTokenRows ? CW : n - g * CW;
 #pragma unroll
-      for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
-      uint32_t v[2][32];
-      const auto add = [&](int j, const uint64_t (&f)[SETS]) {     // 32 columns, one factor (two: by 16)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          fma_pair_f32(acc[16 * j + i], pair_f32(v[j & 1][2 * i], v[j & 1][2 * i + 1]), f[ACT ? i / 8 : 0]);
-      };
-      if constexpr (Cfg::kTokenRows) {
-        const float* xs = p.xs + row_of(un.p0 + min((int)rank * un.nhalf + t, un.n - 1)) * p.ldxs + k0;
-        const float* w[SETS];
-#pragma unroll
-        for (int h = 0; h < SETS; ++h) w[h] = scales_of(un.e, h, (2 * rb + g) * kRows) + k0;
-        // scales of the next two steps are on their way
-        float x1 = xs[0], x2 = xs[min(1, len - 1)], w1[SETS], w2[SETS];
-#pragma unroll
-        for (int h = 0; h < SETS; ++h) {
-          w1[h] = w[h][0];
-          w2[h] = w[h][min(1, len - 1)];
+        for (int c = 0; c < CW / 2; ++c) {
+          const float2 f = unpair_f32(acc[c]);
+          if (2 * c < m) __stcg(out + (size_t)(2 * c) * 128, f.x);
+          if (2 * c + 1 < m) __stcg(out + (size_t)(2 * c + 1) * 128, f.y);
         }
-        for (int i = 0; i < len; ++i, ++step) {
-          uint64_t f[SETS];
-#pragma unroll
-          for (int h = 0; h < SETS; ++h) {
-            const uint32_t b = __float_as_uint(x1 * w1[h]);
-            f[h] = pair_f32(b, b);
-            w1[h] = w2[h];
-            w2[h] = w[h][min(i + 2, len - 1)];
-          }
-          x1 = x2;
-          x2 = xs[min(i + 2, len - 1)];
-          const uint32_t b = step % NB, at = trow + b * BN;
-          ok = mbar_wait_warp(&tfull[b], (step / NB) & 1, err);
-          if (!ok) break;
-          tc_fence_after();
-          // 64 columns at a time in flight: a wait takes all loads that have been started
-          tmem_ld32_start(at, v[0]);
-          tmem_ld32_start(at + 32, v[1]);
-          tmem_ld_wait(v[0]);
-          tmem_after_wait(v[1]);
-          add(0, f);
-          tmem_ld32_start(at + 64, v[0]);
-          add(1, f);
-          tmem_ld32_start(at + 96, v[1]);
-          tmem_ld_wait(v[0]);
-          tmem_after_wait(v[1]);
-          release(b);
-          add(2, f);
-          add(3, f);
-        }
-      } else {
-        for (int i0 = 0; ok && i0 < len; i0 += 4) {
-          ok = mbar_wait_warp(&sfull[slot], turn & 1, err);
-          const float* now = s_scale + slot * Cfg::kSlot + g * CW + (ACT && lane >= 16 ? Cfg::kPad : 0);
-#pragma unroll 1
-          for (int j = 0; ok && j < 4 && i0 + j < len; ++j, ++step) {
-            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(now + j * SETS * Cfg::kPad);
-            ulonglong2 s4[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s4[i] = f[i];
-            const uint32_t b = step % NB, at = trow + b * BN;
-            ok = mbar_wait_warp(&tfull[b], (step / NB) & 1, err);
-            if (!ok) break;
-            tc_fence_after();
-            if (g * CW < un.n) {
-              tmem_ld32_start(at, v[0]);
-              if (CW == 64) tmem_ld32_start(at + 32, v[1]);
-              tmem_ld_wait(v[0]);
-              if (CW == 64) tmem_after_wait(v[1]);
-            }
-            release(b);
-            if (g * CW < un.n) {
-#pragma unroll
-              for (int h = 0; h < CW / 32; ++h) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  fma_pair_f32(acc[16 * h + 2 * i], pair_f32(v[h][4 * i], v[h][4 * i + 1]), s4[i].x);
-                  fma_pair_f32(acc[16 * h + 2 * i + 1], pair_f32(v[h][4 * i + 2], v[h][4 * i + 3]), s4[i].y);
-                  if (h + 1 < CW / 32) s4[i] = f[8 + i];
-                }
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[slot]);
-          if (++slot == Cfg::kSlots) {
-            slot = 0;
-            ++turn;
-          }
-        }
-      }
-      if (len == p.KT) {
-        if (ok) store(un);             // no named barrier from here on: pieces come first
-      } else {
-        // one verdict for the four warps: all of them reach the named barriers below, or none
-        ok = f8_group_all(g, ok);
-        if (!ok) break;
-        const size_t stride = (size_t)2 * BN * 128;      // floats of one slot
-        const size_t at = ((size_t)rank * BN + g * CW) * 128 + t;
-        float* out = p.part + (size_t)work.slot_of(pair, u) * stride + at;
-        const int n = Cfg::kTokenRows ? CW : un.n - g * CW;
-#pragma unroll
-        for (int j = 0; j < CW / 2; ++j) {
-          const float2 f = unpair_f32(acc[j]);
-          if (2 * j < n) __stcg(out + (size_t)(2 * j) * 128, f.x);
-          if (2 * j + 1 < n) __stcg(out + (size_t)(2 * j + 1) * 128, f.y);
-        }
-        sync_group();
+        if (!sync_group()) return false;
         int c_lo, c_hi;
-        work.owners(u, c_lo, c_hi);
+        w.owners(unit, c_lo, c_hi);
         if (t == 0) {
           __threadfence();                               // the group's sums, ordered by its barrier
-          int32_t* ticket = p.tickets + 4 * (u - work.first) + 2 * rank + g;
+          int32_t* ticket = p.tickets + 4 * (unit - w.first) + 2 * rank + g;
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                         // ready for the next call
           __threadfence();
           s_flag[g] = last;
         }
-        sync_group();
-        if (s_flag[g]) {
+        if (!sync_group()) return false;
+        const bool last = s_flag[g];
+        if (!sync_group()) return false;                 // read by all
+        if (!last) return true;
+#pragma unroll 1
+        for (int b = 0; b < CW / 32; ++b) {
+          float x[32];
 #pragma unroll
-          for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
-          for (int c = c_lo; c <= c_hi; ++c) {
-            const float* src = p.part + (size_t)work.slot_of(c, u) * stride + at;
+          for (int c = 0; c < 32; ++c) x[c] = 0.f;
+          for (int o = c_lo; o <= c_hi; ++o) {
+            const float* src = p.part + (size_t)w.slot_of(o, unit) * stride + mine + (size_t)(32 * b) * 128;
 #pragma unroll
-            for (int j = 0; j < CW / 2; ++j) {
-              if (2 * j < n) {
-                const float lo = __ldcg(src + (size_t)(2 * j) * 128), hi = 2 * j + 1 < n ? __ldcg(src + (size_t)(2 * j + 1) * 128) : 0.f;
-                const float2 f = unpair_f32(acc[j]);
-                acc[j] = pair_f32(__float_as_uint(f.x + lo), __float_as_uint(f.y + hi));
-              }
-            }
+            for (int c = 0; c < 32; ++c)
+              if (32 * b + c < m) x[c] += __ldcg(src + (size_t)c * 128);
           }
-          store(un);
+          store(h, b, x);
         }
-        sync_group();                                    // s_flag read by all
+        return true;
+      }
+#pragma unroll
+      for (int b = 0; b < CW / 32; ++b) {
+        float x[32];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 f = unpair_f32(acc[16 * b + c]);
+          x[2 * c] = f.x;
+          x[2 * c + 1] = f.y;
+        }
+        store(h, b, x);
+      }
+      return true;
+    };
+    clear();
+    // A step's columns come 64 at a time: what is in flight at a wait, which takes all of it.
+    if constexpr (Cfg::kTokenRows) {
+      while (ok && g < Cfg::kGroups && open()) {
+        const int* h = s_head + slot * kF8Head;
+        const int n = steps;
+        const int pos = h[kF8P0] + min((int)rank * h[kF8Half] + t, h[kF8N] - 1);
+        const float* xs = p.xs + row_of(pos) * p.ldxs + h[kF8K0];
+        const float* w[SETS];
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) w[k] = scales_of(h[kF8Expert], k, (2 * h[kF8Rb] + g) * kRows) + h[kF8K0];
+        // scales of the next two steps are on their way
+        float x1 = xs[0], x2 = xs[min(1, n - 1)], w1[SETS], w2[SETS];
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) {
+          w1[k] = w[k][0];
+          w2[k] = w[k][min(1, n - 1)];
+        }
+        for (int i = 0; i < n; ++i) {
+          uint64_t f[SETS];
+          const int i2 = min(i + 2, n - 1);
+#pragma unroll
+          for (int k = 0; k < SETS; ++k) {
+            const uint32_t b = __float_as_uint(x1 * w1[k]);
+            f[k] = pair_f32(b, b);
+            w1[k] = w2[k];
+            w2[k] = w[k][i2];
+          }
+          x1 = x2;
+          x2 = xs[i2];
+          const auto add = [&](int c) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              fma_pair_f32(acc[16 * c + k], pair_f32(v[c & 1][2 * k], v[c & 1][2 * k + 1]), f[ACT ? k / 8 : 0]);
+          };
+          ok = begin();
+          if (!ok) break;
+          tmem_ld32_start(at, v[0]);
+          tmem_ld32_start(at + 32, v[1]);
+          tmem_ld_wait(v[0]);
+          tmem_after_wait(v[1]);
+          add(0);
+          tmem_ld32_start(at + 64, v[0]);
+          add(1);
+          tmem_ld32_start(at + 96, v[1]);
+          tmem_ld_wait(v[0]);
+          tmem_after_wait(v[1]);
+          release();
+          add(2);
+          add(3);
+        }
+        ok = ok && finish();
+        clear();
+        leave();
+      }
+    } else {
+      ok = g < Cfg::kGroups && open() && begin();
+      if (ok) {
+        tmem_ld32_start(at, v[0]);
+        if (CW > 32) tmem_ld32_start(at + 32, v[1]);
+      }
+      while (ok) {
+        const float* sc = s_scale + slot * Cfg::kSlot + j * Cfg::kStep;
+        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sc + g * CW + (ACT && lane >= 16 ? Cfg::kPad : 0));
+        const bool last = j + 1 == steps && s_head[slot * kF8Head + kF8Last];
+        ulonglong2 s4[8];
+        const auto add = [&](int c) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            fma_pair_f32(acc[16 * c + 2 * k], pair_f32(v[c][4 * k], v[c][4 * k + 1]), s4[k].x);
+            fma_pair_f32(acc[16 * c + 2 * k + 1], pair_f32(v[c][4 * k + 2], v[c][4 * k + 3]), s4[k].y);
+          }
+        };
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s4[k] = f[k];
+        tmem_ld_wait(v[0]);
+        if (CW == 64) tmem_after_wait(v[1]);
+        release();
+        add(0);
+        if constexpr (CW == 64) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s4[k] = f[8 + k];
+        }
+        if (CW == 64) add(CW / 64);
+        if (last) {
+          ok = finish();
+          clear();
+        }
+        if (++j == steps) {
+          leave();
+          ok = ok && open();
+        }
+        ok = ok && begin();
+        if (ok) {
+          tmem_ld32_start(at, v[0]);
+          if (CW > 32) tmem_ld32_start(at + 32, v[1]);
+        }
       }
     }
   }

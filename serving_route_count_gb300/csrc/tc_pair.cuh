@@ -35,6 +35,33 @@ TC_DEV void mbar_arrive_cluster(uint32_t bar) {
 TC_DEV void mbar_arrive_cluster_read(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// True in one lane of a whole warp, always the same one.  The compiler keeps what only that lane
+// issues (MMAs and their descriptors) in uniform registers, which it does not under lane == 0.
+TC_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait_warp on two barriers; both are asked before either is waited for.
+TC_DEV bool mbar_wait2_warp(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, int32_t* err) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  bool ok = ra && rb;
+  if (!__all_sync(0xffffffffu, ok))
+    ok = __all_sync(0xffffffffu, mbar_wait(a, pa, err) && mbar_wait(b, pb, err));
+  return ok;
+}
+// Whether phase `parity` of b has completed, without waiting: asked for the next step before this one's
+// MMAs are issued, so that the answer is there after them.
+TC_DEV bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // A count in shared memory that one thread raises and others wait for.
 TC_DEV void publish_count(int* c, int v) {
   asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(c)), "r"(v) : "memory");
