@@ -1,11 +1,15 @@
 // fp8_quant.cu - quantisation to e4m3 with fp32 scales (moe_fp8_quant): a scale for each 128 values of
 // a row (activations), or for each 128 x 128 tile (weights).
 //   scale = max(max |x| / 448, 2^-126),  code = e4m3(x / scale)
-// Both quotients are IEEE divisions: x / scale meets the middle of two codes for about one element in
+// Both quotients are correctly rounded: x / scale meets the middle of two codes for about one element in
 // 250 (448 = 7 * 64, so elements of 3/4 of the largest one's mantissa do), where a product by a
 // reciprocal, an ulp off, would go to the other side.  The largest may not be skipped by a NaN or be
 // one: fmaxf takes the other value, so a NaN spoils its own code alone and an infinity its whole block
 // (scale inf, codes 0 and NaN), and any product over either is NaN.
+//
+// Bound by HBM: x is read once and codes and scales written once.  Rows on 16 bytes go 16 values to a
+// thread, whole vectors in and out, eight threads to a block of a row; a tile stays in its CTA's
+// registers between the maximum and the codes.
 #include <cuda_fp8.h>
 
 #include "block_ops.cuh"
@@ -31,7 +35,135 @@ __device__ __forceinline__ uint8_t quant_code(float v, float scale) {
   return (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(v, scale), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Rows: a warp per block of 128 values.
+// 16 consecutive values.
+template <typename T>
+struct Quant16 {
+  static constexpr int kWords = 16 * sizeof(T) / 16;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const T* x) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(x) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float top() const {
+    T v[16];
+    memcpy(v, w, sizeof(v));
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(to_f32(v[i])));
+    return m;
+  }
+  // Codes by one reciprocal, with Markstein's correction: for r = 1 / s rounded to nearest and q within an
+  // ulp of x / s, q + r (x - q s) with two fused operations is x / s rounded to nearest.  The residual has
+  // to be exact: scales of 2^-60 and more keep it above the least subnormal wherever the quotient does not
+  // round to a zero code; smaller scales and infinite ones take the division.
+  __device__ __forceinline__ uint4 codes(float scale) const {
+    T v[16];
+    memcpy(v, w, sizeof(v));
+    uint16_t c[8];
+    if (scale >= 8.67361738e-19f && scale <= 3.40282347e38f) {
+      const float r = __frcp_rn(scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 q;
+        const float a = to_f32(v[2 * i]), b = to_f32(v[2 * i + 1]);
+        q.x = a * r;
+        q.y = b * r;
+        q.x = copysignf(fmaf(fmaf(-q.x, scale, a), r, q.x), a);      // the sum of zeros loses the sign
+        q.y = copysignf(fmaf(fmaf(-q.y, scale, b), r, q.y), b);
+        c[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(to_f32(v[2 * i]), scale), __fdiv_rn(to_f32(v[2 * i + 1]), scale)),
+                                        __NV_SATFINITE, __NV_E4M3);
+    }
+    uint4 o;
+    memcpy(&o, c, 16);
+    return o;
+  }
+};
+
+// Rows on 16 bytes: eight threads per block of 128 values, kQuantAhead blocks of each in flight.
+constexpr int kQuantAhead = 2;
+template <typename T>
+__global__ void __launch_bounds__(256) quant_rows16_kernel(const QuantParams p) {
+  const int sub = threadIdx.x & 7;
+  pdl_wait_prev();
+  pdl_launch_next();
+  const long long n = (long long)p.rows * p.KB, step = (long long)gridDim.x * 32;
+  for (long long i0 = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i0 < n; i0 += kQuantAhead * step) {
+    Quant16<T> v[kQuantAhead];
+    long long row[kQuantAhead];
+    int k[kQuantAhead];
+#pragma unroll
+    for (int u = 0; u < kQuantAhead; ++u) {
+      const long long i = i0 + u * step;
+      row[u] = i < n ? i / p.KB : -1;
+      k[u] = row[u] < 0 ? p.K : (int)(i - row[u] * p.KB) * kFp8Block + 16 * sub;
+      if (k[u] < p.K)
+        v[u].load(static_cast<const T*>(p.x) + row[u] * p.ldx + k[u]);
+      else
+        v[u].zero();
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantAhead; ++u) {
+      float top = v[u].top();
+#pragma unroll
+      for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float scale = quant_scale(top);
+      if (row[u] < 0) continue;
+      if (sub == 0) p.scale[row[u] * p.lds + k[u] / kFp8Block] = scale;
+      if (k[u] < p.K) *reinterpret_cast<uint4*>(p.q + row[u] * p.ldq + k[u]) = v[u].codes(scale);
+    }
+  }
+}
+
+// Tiles on 16 bytes: a CTA per tile, 16 values of four rows to a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) quant_tiles16_kernel(const QuantParams p, int tiles) {
+  __shared__ float s_top[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tall = fp8_blocks(p.rows);       // of one matrix
+  pdl_wait_prev();
+  pdl_launch_next();
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int b = t % p.KB, rb = t / p.KB;   // rb: tile row over all matrices
+    const int e = rb / tall, r0 = (rb - e * tall) * kFp8Block, k = b * kFp8Block + 16 * (threadIdx.x & 7);
+    const long long first = (long long)e * p.rows + r0;
+    Quant16<T> v[4];
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 32 * j + (threadIdx.x >> 3);
+      if (k < p.K && r0 + r < p.rows)
+        v[j].load(static_cast<const T*>(p.x) + (first + r) * p.ldx + k);
+      else
+        v[j].zero();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, v[j].top());
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_top[w]);
+    const float scale = quant_scale(top);
+    if (threadIdx.x == 0) p.scale[(long long)rb * p.lds + b] = scale;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 32 * j + (threadIdx.x >> 3);
+      if (k < p.K && r0 + r < p.rows) *reinterpret_cast<uint4*>(p.q + (first + r) * p.ldq + k) = v[j].codes(scale);
+    }
+    __syncthreads();                         // s_top read by all
+  }
+}
+
+// Rows of any alignment: a warp per block of 128 values.
 template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantParams p) {
   const int lane = threadIdx.x & 31;
@@ -60,7 +192,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantParams p) {
   }
 }
 
-// Tiles: a CTA per tile of 128 rows x 128 values.
+// Tiles of any alignment: a CTA per tile, which is read twice.
 template <typename T>
 __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantParams p, int tiles) {
   __shared__ float s_top[8];
@@ -92,12 +224,18 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantParams p, i
 
 template <typename T>
 static cudaError_t launch_quant(const QuantParams& p, int E, bool tiles, cudaStream_t st) {
+  // whole vectors of 16 values: K and row strides of them, bases on 16 bytes
+  const bool vec = p.K % 16 == 0 && p.ldq % 16 == 0 && p.ldx * (long long)sizeof(T) % 16 == 0 &&
+                   (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.q) & 15) == 0;
   if (tiles) {
     const long long n = (long long)E * fp8_blocks(p.rows) * p.KB;
-    return launch_kernel(quant_tiles_kernel<T>, dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)), dim3(256), 0, st, true, p, (int)n);
+    return launch_kernel(vec ? quant_tiles16_kernel<T> : quant_tiles_kernel<T>, dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)),
+                         dim3(256), 0, st, true, p, (int)n);
   }
-  const long long n = ((long long)p.rows * p.KB + 7) / 8;
-  return launch_kernel(quant_rows_kernel<T>, dim3((unsigned)(n < 152 * 64 ? n : 152 * 64)), dim3(256), 0, st, true, p);
+  const long long blocks = (long long)p.rows * p.KB;
+  const long long n = vec ? (blocks + 32 * kQuantAhead - 1) / (32 * kQuantAhead) : (blocks + 7) / 8;
+  return launch_kernel(vec ? quant_rows16_kernel<T> : quant_rows_kernel<T>, dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)), dim3(256),
+                       0, st, true, p);
 }
 
 cudaError_t launch_fp8_quant(const void* x, int dtype, long long ldx, int E, int rows, int K, bool tiles,
