@@ -33,29 +33,26 @@ struct FfGemm {
   int32_t* err;                        // device error word
 };
 
-// v in T, on the same side of `bound` as v itself: what clamps is told by the saved value as by the
-// sum that it was rounded from.
+// The 16 bits of v in T, on the same side of `bound` >= 0 as v itself, for v >= 0 or any v where
+// bound > 0: what clamps is told by the saved value as by the sum that it was rounded from.  Next to each
+// other, values of one sign differ by one in their bits.
+__device__ __forceinline__ uint32_t bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+__device__ __forceinline__ uint32_t bits16(__half v) { return __half_as_ushort(v); }
 template <typename T>
-__device__ __forceinline__ T round_same_side(float v, float bound) {
-  T t = from_f32<T>(v);
+__device__ __forceinline__ uint32_t round_same_side(float v, float bound) {
+  const T t = from_f32<T>(v);
   const float f = to_f32(t);
-  // the neighbour away from zero or towards it: one up or down in the bits
-  unsigned short b;
-  memcpy(&b, &t, 2);
-  if (v > bound && f <= bound)
-    b = f == 0.f ? 0x0001 : (f > 0.f ? b + 1 : b - 1);
-  else if (v <= bound && f > bound)
-    b = f == 0.f ? 0x8001 : (f > 0.f ? b - 1 : b + 1);
-  memcpy(&t, &b, 2);
-  return t;
+  uint32_t b = bits16(t);
+  b += v > bound && f <= bound;        // v > bound > 0: f is 0 or positive
+  b -= v <= bound && f > bound;        // f > bound > 0
+  return b;
 }
 // The saved forms of gate and up.
 template <typename T>
-__device__ __forceinline__ T save_gate(float g, float limit) { return round_same_side<T>(g, limit); }
+__device__ __forceinline__ uint32_t save_gate(float g, float limit) { return round_same_side<T>(g, limit); }
 template <typename T>
-__device__ __forceinline__ T save_up(float u, float limit) {
-  const float a = to_f32(round_same_side<T>(fabsf(u), limit));
-  return from_f32<T>(copysignf(a, u));
+__device__ __forceinline__ uint32_t save_up(float u, float limit) {
+  return round_same_side<T>(fabsf(u), limit) | (__float_as_uint(u) >> 16 & 0x8000u);
 }
 
 // Gradients of swiglu_f32 by up and gate, times dh.  A clamp passes the gradient within its bounds, the

@@ -78,8 +78,8 @@ ff_simt_kernel(const FfsParams p) {
           const float u = acc[up_first ? 0 : kSets - 1][i][j], gt = acc[up_first ? kSets - 1 : 0][i][j];
           *o = from_f32<T>(swiglu_f32(u, gt, p.d.limit, p.d.alpha, p.d.beta));
           if (pre != nullptr) {
-            s[up_first ? 0 : g.nr] = save_up<T>(u, p.d.limit);
-            s[up_first ? g.nr : 0] = save_gate<T>(gt, p.d.limit);
+            reinterpret_cast<uint16_t*>(s)[up_first ? 0 : g.nr] = (uint16_t)save_up<T>(u, p.d.limit);
+            reinterpret_cast<uint16_t*>(s)[up_first ? g.nr : 0] = (uint16_t)save_gate<T>(gt, p.d.limit);
           }
         } else {
           float du, dg;

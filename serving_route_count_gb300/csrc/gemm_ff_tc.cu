@@ -47,38 +47,27 @@ struct FtParams {
   int32_t* tickets;     // [pairs][2 CTAs][2 accumulators]
   int KT, RB, half;     // RB: row blocks with all accumulators; half: one more with one
   int tiles, size;      // tiles of C, rows of a tile (the last may have fewer)
+  int fix_steps;        // K steps that cutting the leftover units has to save (GtWork)
   int r_mn, c_mn;       // operand stored with its rows along the contiguous dimension
   int bf16, packed, whole16;
 };
 
 __device__ __forceinline__ uint32_t ft_pack(bool bf16, float a, float b) {
-  uint32_t w;
   if (bf16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    memcpy(&w, &v, 4);
-  } else {
-    const __half2 v = __floats2half2_rn(a, b);
-    memcpy(&w, &v, 4);
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return reinterpret_cast<uint32_t&>(v);
   }
-  return w;
+  __half2 v = __floats2half2_rn(a, b);
+  return reinterpret_cast<uint32_t&>(v);
 }
 __device__ __forceinline__ float2 ft_unpack(bool bf16, uint32_t w) {
   if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  __half2 v;
-  memcpy(&v, &w, 4);
-  return __half22float2(v);
+  return __half22float2(reinterpret_cast<__half2&>(w));
 }
-// The saved forms of up (abs) and gate, as 16 bits.
+// The saved forms of up and gate, as 16 bits.
 __device__ __forceinline__ uint32_t ft_save(bool bf16, bool up, float v, float limit) {
-  unsigned short b;
-  if (bf16) {
-    const __nv_bfloat16 t = up ? save_up<__nv_bfloat16>(v, limit) : save_gate<__nv_bfloat16>(v, limit);
-    memcpy(&b, &t, 2);
-  } else {
-    const __half t = up ? save_up<__half>(v, limit) : save_gate<__half>(v, limit);
-    memcpy(&b, &t, 2);
-  }
-  return b;
+  if (bf16) return up ? save_up<__nv_bfloat16>(v, limit) : save_gate<__nv_bfloat16>(v, limit);
+  return up ? save_up<__half>(v, limit) : save_gate<__half>(v, limit);
 }
 __device__ __forceinline__ uint32_t ft_pair(uint32_t lo, uint32_t hi) { return lo | (hi << 16); }
 
@@ -276,7 +265,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
   // Every loop below is taken by whole warps; one lane issues.
   constexpr int kRows = EPI == kFfGlu ? 64 : 128;    // output columns of one CTA and accumulator
   GtWork work;
-  work.init(p.tiles, p.KT, p.RB, p.half, G, pair, Cfg::kFixSteps, false);
+  work.init(p.tiles, p.KT, p.RB, p.half, G, pair, p.fix_steps, false);
   int u, tile, rb, k0, len;
   int s = 0, issued = 0;             // ring stage, stages filled
   uint32_t phase = 0;
@@ -583,6 +572,7 @@ static cudaError_t launch_ft(FtParams& p, cudaStream_t st) {
   p.half = blocks % Cfg::kAcc;
   p.tiles = cdiv(g.nc, BN);
   p.size = p.tiles > 1 ? 16 * cdiv(cdiv(g.nc, p.tiles), 16) : BN;
+  p.fix_steps = Cfg::kFixSteps;
   // no more pairs than K steps can keep busy
   const long long units = (long long)p.tiles * (p.RB + p.half);
   const long long useful = units * (p.KT < kGtMinSteps ? 1 : cdiv(p.KT, kGtMinSteps));
