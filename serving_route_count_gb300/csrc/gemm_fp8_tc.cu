@@ -52,6 +52,8 @@ struct F8Cfg {
   static constexpr int kChunk = kHalf < 32 ? kHalf : 32;     // tokens per tile copy
   static constexpr int kBytesW = 128 * 128, kBytesB = kHalf * 128, kStage = kBytesW + kBytesB;
   static constexpr int kBuffers = BN == 256 ? 2 : 4;         // tensor-memory buffers of a step
+  static constexpr int kTurn = kTokenRows ? 1 : 2;           // steps that change hands together
+  static constexpr int kTurns = kBuffers / kTurn;
   static constexpr int kCols = kBuffers * BN;                // tensor-memory columns
   static constexpr int kGroups = BN == 32 ? 1 : 2;           // groups of four epilogue warps
   static constexpr int kWide = BN == 32 ? 32 : BN / 2;       // accumulator columns of a group
@@ -127,16 +129,16 @@ template <typename T, bool ACT, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 fp8_tc_kernel(const __grid_constant__ F8Params p) {
   using Cfg = F8Cfg<BN, ACT>;
-  constexpr int S = Cfg::kStages, NB = Cfg::kBuffers;
-  static_assert(S > NB, "phases");
+  constexpr int S = Cfg::kStages, TURNS = Cfg::kTurns;
+  static_assert(S > Cfg::kBuffers, "phases");
   extern __shared__ uint8_t raw[];
   uint8_t* st = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(st + S * Cfg::kStage);   // [S] (leader's are used)
   // [S] a step has been multiplied: its stage may be filled again, and its product is ready.  The MMAs are at
-  // most NB < S steps ahead of the epilogue, so no phase passes that it has not waited for.
+  // most kBuffers < S steps ahead of the epilogue, so no phase passes that it has not waited for.
   uint64_t* done = full + S;
-  uint64_t* tempty = done + S;         // [NB] a step's product has been read (leader's are used)
-  uint64_t* sfull = tempty + NB;       // [slots] scales of four steps are there
+  uint64_t* tempty = done + S;         // [TURNS] a turn's products have been read (leader's are used)
+  uint64_t* sfull = tempty + TURNS;       // [slots] scales of four steps are there
   uint64_t* sempty = sfull + Cfg::kSlots;   // [slots] and have been read
   uint64_t* gbar = sempty + Cfg::kSlots;    // [2] the four warps of an epilogue group
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(gbar + 2);
@@ -164,7 +166,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
       mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
     }
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < TURNS; ++b) {
       mbar_init(&tempty[b], 8 * Cfg::kGroups);        // the epilogue warps of both CTAs
     }
     for (int b = 0; b < Cfg::kSlots; ++b) {
@@ -293,7 +295,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     // operand descriptors: only the address changes from stage to stage and from K block to K block
     const uint64_t desc0 = desc_sw128(st);
     const uint32_t hi = (uint32_t)(desc0 >> 32), lo0 = (uint32_t)desc0;
-    uint32_t step = 0;               // steps that have gone to tensor memory
+    uint32_t hand = 0;               // turns that have gone to tensor memory
     bool ready = false;              // the next step's operands and buffer are known to be
     // nothing commits to this phase before the first step's MMAs
     if (p.d.probe_ns != 0 && blockIdx.x == 0)
@@ -301,25 +303,33 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
       const GtTile un = tile_at(tile);
       const uint32_t idesc = idesc_pair8(Cfg::kTokenRows ? 256 : 2 * un.nhalf);
-      for (int i = 0; i < len; ++i, ++step) {
-        const uint32_t b = step % NB;
-        if (!ready) ok = mbar_wait2_warp(&tempty[b], ((step / NB) & 1) ^ 1, &full[s], phase, err);
+      for (int i = 0; i < len; ++i) {
+        const uint32_t b = hand % TURNS;
+        if (!ready) {
+          if (i % Cfg::kTurn == 0)
+            ok = mbar_wait2_warp(&tempty[b], ((hand / TURNS) & 1) ^ 1, &full[s], phase, err);
+          else
+            ok = mbar_wait_warp(&full[s], phase, err);
+        }
         if (!ok) break;
         tc_fence_after();
         // the next step, of this unit or another
-        const uint32_t s1 = s + 1 == S ? 0 : s + 1, b1 = (step + 1) % NB;
-        const bool next = mbar_test(&tempty[b1], (((step + 1) / NB) & 1) ^ 1) && mbar_test(&full[s1], phase ^ (s1 == 0));
+        const bool end = i % Cfg::kTurn == Cfg::kTurn - 1 || i + 1 == len;     // of the turn
+        const uint32_t s1 = s + 1 == S ? 0 : s + 1, h1 = hand + 1;
+        const bool next = mbar_test(&full[s1], phase ^ (s1 == 0)) &&
+                          (!end || mbar_test(&tempty[h1 % TURNS], ((h1 / TURNS) & 1) ^ 1));
         if (elect_one()) {
           const uint32_t lo = lo0 + s * (Cfg::kStage >> 4);
 #pragma unroll
           for (int kb = 0; kb < 4; ++kb) {
             const uint64_t dw = ((uint64_t)hi << 32) | (lo + 2 * kb);
             const uint64_t dx = ((uint64_t)hi << 32) | (lo + (Cfg::kBytesW >> 4) + 2 * kb);
-            mma2_f8(tmem + b * BN, Cfg::kTokenRows ? dx : dw, Cfg::kTokenRows ? dw : dx, idesc, kb != 0);
+            mma2_f8(tmem + (b * Cfg::kTurn + i % Cfg::kTurn) * BN, Cfg::kTokenRows ? dx : dw, Cfg::kTokenRows ? dw : dx, idesc, kb != 0);
           }
           tc2_commit(&done[s]);
         }
         advance();
+        hand += end;
         ready = __all_sync(0xffffffffu, next);
       }
     }
@@ -468,7 +478,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     const int q = warp & 3, g = (warp - 8) >> 2, t = q * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + g * CW;
     const uint32_t bempty = map_rank(&tempty[0], 0);
-    uint32_t step = 0, at = 0, syncs = 0;
+    uint32_t hand = 0, at = 0, syncs = 0;
     int j = 0, steps = 0;              // in the slot
     uint64_t acc[CW / 2];
     uint32_t v[2][32];
@@ -498,20 +508,21 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         ++turn;
       }
     };
-    // the next step's product
-    const auto begin = [&]() {
+    // the products of the next turn, of one step or two
+    const auto begin = [&](int n) {
+      if (n == 2) advance();
       if (!mbar_wait_warp(&done[s], phase, err)) return false;
       advance();
       tc_fence_after();
-      at = trow + (step % NB) * BN;
+      at = trow + (hand % TURNS) * (Cfg::kTurn * BN);
       return true;
     };
-    // the step's buffer has been read
+    // the turn's buffers have been read
     const auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_read(bempty + 8 * (step % NB));
-      ++step;
+      if (lane == 0) mbar_arrive_cluster_read(bempty + 8 * (hand % TURNS));
+      ++hand;
     };
     // 32 of the group's columns to the output
     const auto store = [&](const int* h, int b, float (&x)[32]) {
@@ -622,7 +633,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
             for (int k = 0; k < 16; ++k)
               fma_pair_f32(acc[16 * c + k], pair_f32(v[c & 1][2 * k], v[c & 1][2 * k + 1]), f[ACT ? k / 8 : 0]);
           };
-          ok = begin();
+          ok = begin(1);
           if (!ok) break;
           tmem_ld32_start(at, v[0]);
           tmem_ld32_start(at + 32, v[1]);
@@ -643,46 +654,66 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         leave();
       }
     } else {
-      ok = g < Cfg::kGroups && open() && begin();
-      if (ok) {
-        tmem_ld32_start(at, v[0]);
-        if (CW > 32) tmem_ld32_start(at + 32, v[1]);
-      }
+      ok = g < Cfg::kGroups && open();
       while (ok) {
-        const float* sc = s_scale + slot * Cfg::kSlot + j * Cfg::kStep;
-        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sc + g * CW + (ACT && lane >= 16 ? Cfg::kPad : 0));
-        const bool last = j + 1 == steps && s_head[slot * kF8Head + kF8Last];
+        const int two = min(2, steps - j);               // steps of this turn
+        const float* sc = s_scale + slot * Cfg::kSlot + j * Cfg::kStep + g * CW + (ACT && lane >= 16 ? Cfg::kPad : 0);
         ulonglong2 s4[8];
-        const auto add = [&](int c) {
+        const auto scales = [&](int step, int c) {       // of 32 columns
+          const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sc + step * Cfg::kStep + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s4[k] = f[k];
+        };
+        const auto add = [&](int c, const uint32_t (&x)[32]) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            fma_pair_f32(acc[16 * c + 2 * k], pair_f32(v[c][4 * k], v[c][4 * k + 1]), s4[k].x);
-            fma_pair_f32(acc[16 * c + 2 * k + 1], pair_f32(v[c][4 * k + 2], v[c][4 * k + 3]), s4[k].y);
+            fma_pair_f32(acc[16 * c + 2 * k], pair_f32(x[4 * k], x[4 * k + 1]), s4[k].x);
+            fma_pair_f32(acc[16 * c + 2 * k + 1], pair_f32(x[4 * k + 2], x[4 * k + 3]), s4[k].y);
           }
         };
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s4[k] = f[k];
-        tmem_ld_wait(v[0]);
-        if (CW == 64) tmem_after_wait(v[1]);
-        release();
-        add(0);
-        if constexpr (CW == 64) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) s4[k] = f[8 + k];
+        scales(0, 0);
+        ok = begin(two);
+        if (!ok) break;
+        if constexpr (CW == 32) {
+          tmem_ld32_start(at, v[0]);
+          if (two == 2) tmem_ld32_start(at + BN, v[1]);
+          tmem_ld_wait(v[0]);
+          tmem_after_wait(v[1]);
+          release();
+          add(0, v[0]);
+          if (two == 2) {
+            scales(1, 0);
+            add(0, v[1]);
+          }
+        } else {
+          tmem_ld32_start(at, v[0]);
+          tmem_ld32_start(at + 32, v[1]);
+          tmem_ld_wait(v[0]);
+          tmem_after_wait(v[1]);
+          if (two == 1) release();
+          add(0, v[0]);
+          if (two == 2) tmem_ld32_start(at + BN, v[0]);
+          scales(0, 1);
+          add(1, v[1]);
+          if (two == 2) {
+            tmem_ld32_start(at + BN + 32, v[1]);
+            scales(1, 0);
+            tmem_ld_wait(v[0]);
+            tmem_after_wait(v[1]);
+            release();
+            add(0, v[0]);
+            scales(1, 1);
+            add(1, v[1]);
+          }
         }
-        if (CW == 64) add(CW / 64);
-        if (last) {
-          ok = finish();
-          clear();
-        }
-        if (++j == steps) {
+        j += two;
+        if (j == steps) {
+          if (s_head[slot * kF8Head + kF8Last]) {
+            ok = finish();
+            clear();
+          }
           leave();
           ok = ok && open();
-        }
-        ok = ok && begin();
-        if (ok) {
-          tmem_ld32_start(at, v[0]);
-          if (CW > 32) tmem_ld32_start(at + 32, v[1]);
         }
       }
     }
