@@ -11,6 +11,9 @@ namespace moe {
 int report_cuda(cudaError_t e);
 // gemm_ff_simt.cu
 cudaError_t launch_ff_simt(const FfDims& d, const FfGemm& g, int epilogue, cudaStream_t st);
+// gemv_ff.cu
+bool ff_gemv_takes(const FfGemm& g, int epilogue);
+cudaError_t launch_ff_gemv(const FfDims& d, const FfGemm& g, int epilogue, cudaStream_t st);
 // gemm_ff_tc.cu
 size_t ff_tc_part_bytes();
 bool ff_tc_addressable(const FfGemm& g);
@@ -31,6 +34,7 @@ moe_status status(cudaError_t e) { return static_cast<moe_status>(report_cuda(e)
 
 cudaError_t product(const moe_ff_s& f, const FfGemm& g, int epilogue, cudaStream_t st) {
   if (!ff_tc_addressable(g)) return launch_ff_simt(f.d, g, epilogue, st);
+  if (ff_gemv_takes(g, epilogue)) return launch_ff_gemv(f.d, g, epilogue, st);
   uint8_t* base = reinterpret_cast<uint8_t*>(g.err);      // the scratch buffer begins with the error word
   return launch_ff_tc(f.d, g, epilogue, reinterpret_cast<float*>(base + kGtPartAt),
                       reinterpret_cast<int32_t*>(base + kGtTicketsAt), st);

@@ -27,6 +27,19 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
   return __float2bfloat16_rn(v);
 }
 
+// 16 bytes that are read once, zeros where `in` is false.  Volatile, so that several of them are under way
+// before the first is used (the compiler otherwise saves their registers).
+__device__ __forceinline__ uint4 load_once16(const void* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
+      " mov.u32 %3, 0;\n @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)in)
+      : "memory");
+  return v;
+}
+
 // Clamped SwiGLU in fp32: g' * sigmoid(alpha g') * (u' + beta), g' = min(g, limit),
 // u' = clamp(u, -limit, limit).  sigmoid(a) = 1 / (1 + e) or e / (1 + e), e = exp(-|a|): the divisor
 // stays within [1, 2], where __fdividef is within 2 ulp (above 2^126 it returns 0, which lost every

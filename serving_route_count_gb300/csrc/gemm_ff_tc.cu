@@ -35,19 +35,17 @@ struct FtCfg {
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
   static constexpr int kSmem = 1024 + kStages * kStage + kTables;
   static constexpr int kCols = 2 * BN;                       // tensor-memory columns: two buffers
-  // K steps that joining the pieces of a unit costs (as for the grouped products)
-  static constexpr int kFixSteps = BN <= 32 ? 8 : (BN <= 64 ? 12 : (BN <= 128 ? 24 : 40));
 };
 
 struct FtParams {
   CUtensorMap tm_r, tm_c;
   FfDims d;
   FfGemm g;
-  float* part;          // [pairs][2][2 CTAs][accumulators][BN][128]
+  float* part;          // [pairs][2][2 CTAs][accumulators][BN / 4][128][4]
   int32_t* tickets;     // [pairs][2 CTAs][2 accumulators]
   int KT, RB, half;     // RB: row blocks with all accumulators; half: one more with one
   int tiles, size;      // tiles of C, rows of a tile (the last may have fewer)
-  int fix_steps;        // K steps that cutting the leftover units has to save (GtWork)
+  int cut;              // whether the units left over are cut along K
   int r_mn, c_mn;       // operand stored with its rows along the contiguous dimension
   int bf16, packed, whole16;
 };
@@ -265,7 +263,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
   // Every loop below is taken by whole warps; one lane issues.
   constexpr int kRows = EPI == kFfGlu ? 64 : 128;    // output columns of one CTA and accumulator
   GtWork work;
-  work.init(p.tiles, p.KT, p.RB, p.half, G, pair, p.fix_steps, false);
+  work.init(p.tiles, p.KT, p.RB, p.half, G, pair, p.cut ? 0 : 0x7FFFFFFF, false);
   int u, tile, rb, k0, len;
   int s = 0, issued = 0;             // ring stage, stages filled
   uint32_t phase = 0;
@@ -428,14 +426,16 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         if (!ok) break;
         tc_fence_after();
         const size_t stride = (size_t)2 * Cfg::kAcc * BN * 128;     // floats of one slot
-        const size_t at = (size_t)(rank * Cfg::kAcc + acc) * BN * 128 + q * 32 + lane;
+        // four columns of a lane are adjacent: 16-byte accesses
+        const size_t at = (size_t)(rank * Cfg::kAcc + acc) * BN * 128 + (q * 32 + lane) * 4;
         float* mine = p.part + (size_t)work.slot_of(pair, u) * stride + at;
 #pragma unroll 1
         for (int c0 = 0; c0 < n; c0 += 32) {
           tmem_ld32(trow + c0, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + j < n) __stcg(mine + (size_t)(c0 + j) * 128, v[j]);
+          for (int j = 0; j < 32; j += 4)
+            if (c0 + j < n)
+              __stcg(reinterpret_cast<float4*>(mine + (size_t)(c0 + j) * 128), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
         }
         tc_fence_before();
         __syncwarp();
@@ -453,22 +453,29 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         }
         sync_group();
         if (s_flag[g]) {
+          // K order; few rows: the sums of four pieces in flight at a time, else of two
+          const auto piece = [&](int c) {
+            return reinterpret_cast<const float4*>(p.part + (size_t)work.slot_of(min(c, c_hi), u) * stride + at);
+          };
+          const auto add = [&](float* x, const float4& y, bool there) {
+            x[0] += there ? y.x : 0.f;
+            x[1] += there ? y.y : 0.f;
+            x[2] += there ? y.z : 0.f;
+            x[3] += there ? y.w : 0.f;
+          };
           if (n <= 8) {
-            // few rows: the sums of four pieces in flight at a time
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
             for (int c = c_lo; c <= c_hi; c += 4) {
-              float t[4][8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float* src = p.part + (size_t)work.slot_of(min(c + i, c_hi), u) * stride + at;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) t[i][j] = __ldcg(src + (size_t)min(j, n - 1) * 128);
-              }
+              float4 x[4][2];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += c + i <= c_hi ? t[i][j] : 0.f;
+                for (int j = 0; j < 2; ++j) x[i][j] = __ldcg(piece(c + i) + (4 * j < n ? j : 0) * 128);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) add(&v[4 * j], x[i][j], c + i <= c_hi);
             }
             ft_store<EPI>(p, v, p0, n, col0, 0, q, lane);
           } else {
@@ -476,11 +483,16 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
             for (int c0 = 0; c0 < n; c0 += 32) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.f;
-#pragma unroll 2
-              for (int c = c_lo; c <= c_hi; ++c) {
-                const float* src = p.part + (size_t)work.slot_of(c, u) * stride + at;
+              for (int c = c_lo; c <= c_hi; c += 2) {
+                float4 x[2][8];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + (size_t)(c0 + j) * 128);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) x[i][j] = __ldcg(piece(c + i) + (c0 / 4 + j) * 128);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) add(&v[4 * j], x[i][j], c + i <= c_hi);
               }
               ft_store<EPI>(p, v, p0, n, col0, c0, q, lane);
             }
@@ -499,13 +511,42 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
 
 // ---------------------------------------------------------------------------------- host side
 
-// Tile width: the rows of C in one tile up to 256.  Sums over tokens have both operands the other way
-// round, whose boxes are 64 wide for each CTA: 128 at least.
-static int ff_tc_bn(const FfGemm& g) {
-  const bool mn = g.ck != 1;
-  if (g.nc <= 32 && !mn) return 32;
-  if (g.nc <= 64 && !mn) return 64;
-  return g.nc <= 128 ? 128 : 256;
+// Tile width, and whether the units that whole waves leave over are cut along K: the least of the estimated
+// times.  A K step of a unit takes what its MMAs or its loads take, whichever is more; joining the pieces of a
+// unit takes time by its rows of C and its pieces, one group of warps adding them.  Estimates from
+// us of the up projection, forward, at widths 32 / 64 / 128 / 256, c cut, w whole: H = 6144, I = 512, M = 48
+// 24c / 31w / 34w / 33w, M = 777 - / 40w / 41w / 40w (cut 41 / 43 / 55); H = I = 4096, M = 200 78c / 54w / 45w /
+// 47w, M = 2048 - / 315c / 187c / 129w.
+// Sums over tokens have both operands the other way round, whose boxes are 64 wide for each CTA: 128 at
+// least.
+struct FtPlan {
+  int bn, cut;
+};
+static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
+  FtPlan best{256, 0};
+  double least = 1e300;
+  for (int bn = g.ck != 1 ? 128 : 32; bn <= 256; bn *= 2) {
+    const int KT = cdiv(g.K, kFtK), tiles = cdiv(g.nc, bn);
+    const double step = bn == 32 ? 235 : (bn == 64 ? 240 : (bn == 128 ? 267 : 334));     // ns
+    const long long units = (long long)tiles * cdiv(g.nr, epilogue == kFfGlu ? 128 : 256);
+    const long long waves = units / pairs, left = units % pairs;
+    const double base = (double)waves * KT * step;
+    double whole = base + (left ? KT * step : 0), cut = 1e300;
+    if (left) {
+      const double pieces = (double)pairs / left + 1, rows = cdiv(g.nc, tiles);
+      cut = base + (double)left * KT / pairs * step + 1000 + rows * (150 + 8.6 * pieces);
+    }
+    if (whole <= least) {
+      least = whole;
+      best = {bn, 0};
+    }
+    if (cut < least) {
+      least = cut;
+      best = {bn, 1};
+    }
+    if (bn >= g.nc) break;             // one tile holds them all
+  }
+  return best;
 }
 
 // Scratch of cut units: [pairs][2][2 CTAs][accumulators][BN][128] fp32 of the widest tile.
@@ -572,7 +613,6 @@ static cudaError_t launch_ft(FtParams& p, cudaStream_t st) {
   p.half = blocks % Cfg::kAcc;
   p.tiles = cdiv(g.nc, BN);
   p.size = p.tiles > 1 ? 16 * cdiv(cdiv(g.nc, p.tiles), 16) : BN;
-  p.fix_steps = Cfg::kFixSteps;
   // no more pairs than K steps can keep busy
   const long long units = (long long)p.tiles * (p.RB + p.half);
   const long long useful = units * (p.KT < kGtMinSteps ? 1 : cdiv(p.KT, kGtMinSteps));
@@ -582,7 +622,19 @@ static cudaError_t launch_ft(FtParams& p, cudaStream_t st) {
 
 template <int EPI>
 static cudaError_t launch_ft_bn(FtParams& p, cudaStream_t st) {
-  switch (ff_tc_bn(p.g)) {
+  static PerDevice<int> per;           // CTA pairs of the device
+  int pairs = 0;
+  const cudaError_t e = on_device(per, &pairs, [](int* v) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    *v = std::max(1, sms / 2);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
+  const FtPlan plan = ff_tc_plan(p.g, EPI, pairs);
+  p.cut = plan.cut;
+  switch (plan.bn) {
     case 32: return launch_ft<EPI, 32>(p, st);
     case 64: return launch_ft<EPI, 64>(p, st);
     case 128: return launch_ft<EPI, 128>(p, st);

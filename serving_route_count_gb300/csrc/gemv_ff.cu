@@ -1,0 +1,125 @@
+// gemv_ff.cu - products of the gated feed-forward block's forward pass for a few tokens (up to four):
+// out[c][r] = act(sum_k R(r, k) C(c, k)), both operands along K.
+//
+// Bound by reading the weights once.  One to eight warps to an output row (GLU: to a pair of rows, up and
+// gate), as many as fill the GPU; a lane takes 16 bytes of every row at a time, four of them in flight, and
+// multiplies in fp32 on the CUDA cores, which at so few tokens keep up with HBM.  Sums go lane by lane, then
+// over the lanes, then over the warps: one order.  Units on the tensor cores are too large for this: one
+// token of 7168 -> 1152 -> 7168 took 24 us there, pieces of units and their joining among it.
+#include "feed_forward.cuh"
+#include "../../include/moe_gb300.h"
+
+namespace moe {
+
+constexpr int kFvThreads = 256, kFvWarps = kFvThreads / 32, kFvAhead = 4;
+
+struct FvParams {
+  FfDims d;
+  FfGemm g;
+  int warps;            // of an output
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+  T t[8];
+  memcpy(t, &w, 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = to_f32(t[i]);
+}
+
+template <typename T, int EPI, int NC>
+__global__ void __launch_bounds__(kFvThreads) ff_gemv_kernel(const FvParams p) {
+  constexpr int kSets = EPI == kFfGlu ? 2 : 1;
+  __shared__ float s_sum[kFvWarps][kSets * NC];
+  const FfGemm& g = p.g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % p.warps;
+  const int r = blockIdx.x * (kFvWarps / p.warps) + warp / p.warps;
+  const int stride = p.warps * 256;
+  const T* R = static_cast<const T*>(g.r) + min(r, g.nr - 1) * g.rs;
+  const T* C = static_cast<const T*>(g.c);
+  pdl_wait_prev();
+  pdl_launch_next();
+  float acc[kSets][NC] = {};
+  for (int k0 = (part * 32 + lane) * 8; k0 < g.K; k0 += kFvAhead * stride) {
+    uint4 w[kFvAhead][kSets], x[kFvAhead][NC];
+#pragma unroll
+    for (int i = 0; i < kFvAhead; ++i) {
+      const int k = k0 + i * stride;
+#pragma unroll
+      for (int h = 0; h < kSets; ++h)
+        w[i][h] = load_once16(R + h * g.half + k, k < g.K);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        x[i][c] = k < g.K ? *reinterpret_cast<const uint4*>(C + min(c, g.nc - 1) * g.cs + k) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kFvAhead; ++i) {
+      float a[kSets][8];
+#pragma unroll
+      for (int h = 0; h < kSets; ++h) unpack8<T>(w[i][h], a[h]);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float b[8];
+        unpack8<T>(x[i][c], b);
+#pragma unroll
+        for (int h = 0; h < kSets; ++h)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[h][c] = fmaf(a[h][j], b[j], acc[h][c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kSets; ++h)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) acc[h][c] += __shfl_xor_sync(0xffffffffu, acc[h][c], o);
+      if (lane == 0) s_sum[warp][h * NC + c] = acc[h][c];
+    }
+  __syncthreads();
+  if (part != 0 || r >= g.nr || lane >= min(NC, g.nc)) return;
+  float v[kSets];
+#pragma unroll
+  for (int h = 0; h < kSets; ++h) {
+    v[h] = 0.f;
+    for (int i = 0; i < p.warps; ++i) v[h] += s_sum[warp + i][h * NC + lane];
+  }
+  T* o = static_cast<T*>(g.out) + lane * g.ldo + r;
+  if constexpr (EPI == kFfStore) {
+    *o = from_f32<T>(v[0]);
+  } else {
+    const bool up_first = p.d.layout == MOE_W13_UP_GATE;
+    const float u = v[up_first ? 0 : 1], gt = v[up_first ? 1 : 0];
+    *o = from_f32<T>(swiglu_f32(u, gt, p.d.limit, p.d.alpha, p.d.beta));
+    if (g.pre != nullptr) {
+      uint16_t* s = static_cast<uint16_t*>(g.pre) + (long long)lane * 2 * g.nr + r;
+      s[up_first ? 0 : g.nr] = (uint16_t)save_up<T>(u, p.d.limit);
+      s[up_first ? g.nr : 0] = (uint16_t)save_gate<T>(gt, p.d.limit);
+    }
+  }
+}
+
+// A few tokens, both operands along K in whole vectors (their alignment as for the tensor cores).
+bool ff_gemv_takes(const FfGemm& g, int epilogue) {
+  return g.nc <= 4 && g.rk == 1 && g.ck == 1 && g.K % 8 == 0 && epilogue != kFfGrad;
+}
+
+template <typename T, int EPI>
+static cudaError_t launch_fv(FvParams& p, cudaStream_t st) {
+  // warps enough for every SM to have 16, as far as each still has a vector of every lane
+  p.warps = 1;
+  while (p.warps < kFvWarps && p.g.nr * p.warps < 152 * 16 && p.g.K > p.warps * 256) p.warps *= 2;
+  const dim3 grid(cdiv(p.g.nr, kFvWarps / p.warps));
+  const auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kFvThreads), 0, st, true, p); };
+  if (p.g.nc == 1) return go(ff_gemv_kernel<T, EPI, 1>);
+  return p.g.nc == 2 ? go(ff_gemv_kernel<T, EPI, 2>) : go(ff_gemv_kernel<T, EPI, 4>);
+}
+
+cudaError_t launch_ff_gemv(const FfDims& d, const FfGemm& g, int epilogue, cudaStream_t st) {
+  FvParams p{d, g, 1};
+  if (d.dtype == MOE_DTYPE_F16)
+    return epilogue == kFfGlu ? launch_fv<__half, kFfGlu>(p, st) : launch_fv<__half, kFfStore>(p, st);
+  return epilogue == kFfGlu ? launch_fv<__nv_bfloat16, kFfGlu>(p, st) : launch_fv<__nv_bfloat16, kFfStore>(p, st);
+}
+
+}  // namespace moe
