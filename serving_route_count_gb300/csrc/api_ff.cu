@@ -13,7 +13,7 @@ int report_cuda(cudaError_t e);
 cudaError_t launch_ff_simt(const FfDims& d, const FfGemm& g, int epilogue, cudaStream_t st);
 // gemv_ff.cu
 bool ff_gemv_takes(const FfGemm& g, int epilogue);
-cudaError_t launch_ff_gemv(const FfDims& d, const FfGemm& g, int epilogue, cudaStream_t st);
+cudaError_t launch_ff_gemv(const FfDims& d, const FfGemm& g, int epilogue, bool early, cudaStream_t st);
 // gemm_ff_tc.cu
 size_t ff_tc_part_bytes();
 bool ff_tc_addressable(const FfGemm& g);
@@ -32,9 +32,10 @@ namespace {
 
 moe_status status(cudaError_t e) { return static_cast<moe_status>(report_cuda(e)); }
 
-cudaError_t product(const moe_ff_s& f, const FfGemm& g, int epilogue, cudaStream_t st) {
+// after: the launch before this one is this call's, and writes C alone of this product's operands
+cudaError_t product(const moe_ff_s& f, const FfGemm& g, int epilogue, cudaStream_t st, bool after = false) {
   if (!ff_tc_addressable(g)) return launch_ff_simt(f.d, g, epilogue, st);
-  if (ff_gemv_takes(g, epilogue)) return launch_ff_gemv(f.d, g, epilogue, st);
+  if (ff_gemv_takes(g, epilogue)) return launch_ff_gemv(f.d, g, epilogue, after, st);
   uint8_t* base = reinterpret_cast<uint8_t*>(g.err);      // the scratch buffer begins with the error word
   return launch_ff_tc(f.d, g, epilogue, reinterpret_cast<float*>(base + kGtPartAt),
                       reinterpret_cast<int32_t*>(base + kGtTicketsAt), st);
@@ -93,7 +94,7 @@ moe_status moe_ff_forward(const moe_ff_t* plan, void* scratch, size_t scratch_by
   cudaError_t e = product(*plan, FfGemm{w13, ldw13, 1, ldw13 * d.I, x, ldx, 1, d.I, M, d.H, h, d.I, pre, err},
                           kFfGlu, st);
   if (e == cudaSuccess)
-    e = product(*plan, FfGemm{w2, ldw2, 1, 0, h, d.I, 1, d.H, M, d.I, y, ldy, nullptr, err}, kFfStore, st);
+    e = product(*plan, FfGemm{w2, ldw2, 1, 0, h, d.I, 1, d.H, M, d.I, y, ldy, nullptr, err}, kFfStore, st, true);
   return status(e);
 }
 

@@ -27,17 +27,27 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
   return __float2bfloat16_rn(v);
 }
 
-// 16 bytes that are read once, zeros where `in` is false.  Volatile, so that several of them are under way
-// before the first is used (the compiler otherwise saves their registers).
-__device__ __forceinline__ uint4 load_once16(const void* p, bool in) {
-  uint4 v;
+// Four times 16 bytes that are read once, `step` bytes apart, the first n of them; zeros for the others.  One
+// statement, so that all four are under way before the first is used (apart, the compiler uses each in turn
+// and saves the registers).
+__device__ __forceinline__ void load_once16x4(uint4 (&v)[4], const void* p, long long step, int n) {
+  const char* q = static_cast<const char*>(p);
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
-      " mov.u32 %3, 0;\n @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((uint32_t)in)
+      "{\n .reg .pred p0, p1, p2, p3;\n"
+      " setp.gt.s32 p0, %20, 0;\n setp.gt.s32 p1, %20, 1;\n setp.gt.s32 p2, %20, 2;\n setp.gt.s32 p3, %20, 3;\n"
+      " mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+      " mov.u32 %4, 0;\n mov.u32 %5, 0;\n mov.u32 %6, 0;\n mov.u32 %7, 0;\n"
+      " mov.u32 %8, 0;\n mov.u32 %9, 0;\n mov.u32 %10, 0;\n mov.u32 %11, 0;\n"
+      " mov.u32 %12, 0;\n mov.u32 %13, 0;\n mov.u32 %14, 0;\n mov.u32 %15, 0;\n"
+      " @p0 ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%16];\n"
+      " @p1 ld.global.L1::no_allocate.v4.u32 {%4, %5, %6, %7}, [%17];\n"
+      " @p2 ld.global.L1::no_allocate.v4.u32 {%8, %9, %10, %11}, [%18];\n"
+      " @p3 ld.global.L1::no_allocate.v4.u32 {%12, %13, %14, %15}, [%19];\n}"
+      : "=&r"(v[0].x), "=&r"(v[0].y), "=&r"(v[0].z), "=&r"(v[0].w), "=&r"(v[1].x), "=&r"(v[1].y),
+        "=&r"(v[1].z), "=&r"(v[1].w), "=&r"(v[2].x), "=&r"(v[2].y), "=&r"(v[2].z), "=&r"(v[2].w),
+        "=&r"(v[3].x), "=&r"(v[3].y), "=&r"(v[3].z), "=&r"(v[3].w)
+      : "l"(q), "l"(q + step), "l"(q + 2 * step), "l"(q + 3 * step), "r"(n)
       : "memory");
-  return v;
 }
 
 // Clamped SwiGLU in fp32: g' * sigmoid(alpha g') * (u' + beta), g' = min(g, limit),

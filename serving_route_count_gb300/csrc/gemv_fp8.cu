@@ -36,7 +36,7 @@ __device__ __forceinline__ void e4m3_unpack16(const uint4& w, float (&f)[16]) {
 
 template <typename T, bool ACT, int NC>
 __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p) {
-  constexpr int kSets = ACT ? 2 : 1, kF8vAhead = NC == 4 ? 2 : 4;
+  constexpr int kSets = ACT ? 2 : 1, kF8vAhead = 4;
   __shared__ float s_sum[kF8vWarps][kSets * NC];
   const GroupedCall& c = p.f.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % p.warps;
@@ -89,38 +89,30 @@ __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p
   }
   float acc[kSets][NC] = {};
   for (int k0 = (part * 32 + lane) * 16; k0 < K; k0 += kF8vAhead * stride) {
-    uint4 a[kF8vAhead][kSets], b[kF8vAhead][NC];
-    float sa[kF8vAhead][kSets], sb[kF8vAhead][NC];
+    uint4 a[kSets][kF8vAhead];
+#pragma unroll
+    for (int h = 0; h < kSets; ++h) load_once16x4(a[h], w[h] + k0, stride, cdiv(K - k0, stride));
 #pragma unroll
     for (int i = 0; i < kF8vAhead; ++i) {
       const int k = k0 + i * stride;
       const bool in = k < K;
+      float wf[kSets][16], sa[kSets];
 #pragma unroll
       for (int h = 0; h < kSets; ++h) {
-        a[i][h] = load_once16(w[h] + k, in);
-        sa[i][h] = in ? ws[h][k / kFp8Block] : 0.f;
+        sa[h] = in ? ws[h][k / kFp8Block] : 0.f;
+        e4m3_unpack16(a[h][i], wf[h]);
       }
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        b[i][j] = in ? *reinterpret_cast<const uint4*>(x + row[j] * c.ldx + k) : make_uint4(0, 0, 0, 0);
-        sb[i][j] = in ? p.f.xs[row[j] * p.f.ldxs + k / kFp8Block] : 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kF8vAhead; ++i) {
-      float wf[kSets][16];
-#pragma unroll
-      for (int h = 0; h < kSets; ++h) e4m3_unpack16(a[i][h], wf[h]);
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
+        const float sb = in ? p.f.xs[row[j] * p.f.ldxs + k / kFp8Block] : 0.f;
         float xf[16];
-        e4m3_unpack16(b[i][j], xf);
+        e4m3_unpack16(in ? *reinterpret_cast<const uint4*>(x + row[j] * c.ldx + k) : make_uint4(0, 0, 0, 0), xf);
 #pragma unroll
         for (int h = 0; h < kSets; ++h) {
           float s = 0.f;
 #pragma unroll
           for (int t = 0; t < 16; ++t) s = fmaf(wf[h][t], xf[t], s);
-          acc[h][j] = fmaf(s, sa[i][h] * sb[i][j], acc[h][j]);
+          acc[h][j] = fmaf(s, sa[h] * sb, acc[h][j]);
         }
       }
     }

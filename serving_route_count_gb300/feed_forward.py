@@ -77,13 +77,14 @@ class MoEFeedForward:
     def forward(self, x, w13, w2, out=None, saved=None, stream=None):
         """(y, saved): saved = (up and gate [M, 2 I] in w13's order, h [M, I]) is what backward needs, in new
         tensors or the given ones."""
+        made = None
         if saved is None:
-            M = x.shape[0]
-            saved = (torch.empty((M, 2 * self.I), dtype=self.dtype, device=x.device),
-                     torch.empty((M, self.I), dtype=self.dtype, device=x.device))
-        return self._forward(x, w13, w2, out, saved, stream), saved
+            on, M = x.device, x.shape[0]
+            saved = made = (torch.empty((M, 2 * self.I), dtype=self.dtype, device=on),
+                            torch.empty((M, self.I), dtype=self.dtype, device=on))
+        return self._forward(x, w13, w2, out, saved, stream, made is None), saved
 
-    def _forward(self, x, w13, w2, out, saved, stream):
+    def _forward(self, x, w13, w2, out, saved, stream, given=True):
         dev = self._here(x, "x")
         H, I, dtype = self.H, self.I, self.dtype
         xp, ldx = _rows(x, "x", dev, None, H, dtype)
@@ -93,12 +94,17 @@ class MoEFeedForward:
         pre_p = h_p = None
         if saved is not None:
             pre, h = saved
-            pre_p, h_p = _whole(pre, "saved[0]", dev, dtype, M * 2 * I), _whole(h, "saved[1]", dev, dtype, M * I)
+            if given:                  # tensors made here need no checks
+                _whole(pre, "saved[0]", dev, dtype, M * 2 * I)
+                _whole(h, "saved[1]", dev, dtype, M * I)
+            pre_p, h_p = pre.data_ptr(), h.data_ptr()
+        ldo = H
         if out is None:
             out = torch.empty((M, H), dtype=dtype, device=x.device)
-        op, ldo = _rows(out, "out", dev, M, H, dtype)
-        st = _lib.load().moe_ff_forward(*self._fixed, xp, ldx, w13p, ldw13, w2p, ldw2, pre_p, h_p, op, ldo, M,
-                                        _stream(stream, dev))
+        else:
+            ldo = _rows(out, "out", dev, M, H, dtype)[1]
+        st = _lib.load().moe_ff_forward(*self._fixed, xp, ldx, w13p, ldw13, w2p, ldw2, pre_p, h_p,
+                                        out.data_ptr(), ldo, M, _stream(stream, dev))
         if st:
             _check(st, "moe_ff_forward")
         return out
@@ -116,7 +122,7 @@ class MoEFeedForward:
         w2p, ldw2 = _rows(w2, "w2", dev, H, I, dtype)
         pre, h = saved
         pre_p, h_p = _whole(pre, "saved[0]", dev, dtype, M * 2 * I), _whole(h, "saved[1]", dev, dtype, M * I)
-        wanted = []
+        wanted, on = [], dy.device
         for needed, t, name, rows, cols in zip(need, (dx, dw13, dw2), ("dx", "dw13", "dw2"), (M, 2 * I, H), (H, H, I)):
             if not needed:
                 if t is not None:
@@ -124,8 +130,10 @@ class MoEFeedForward:
                 wanted.append((None, None, cols))
                 continue
             if t is None:
-                t = torch.empty((rows, cols), dtype=dtype, device=dy.device)
-            wanted.append((t, *_rows(t, name, dev, rows, cols, dtype)))
+                t = torch.empty((rows, cols), dtype=dtype, device=on)
+                wanted.append((t, t.data_ptr(), cols))
+            else:
+                wanted.append((t, *_rows(t, name, dev, rows, cols, dtype)))
         (dx, dxp, lddx), (dw13, dw13p, lddw13), (dw2, dw2p, lddw2) = wanted
         st = _lib.load().moe_ff_backward(*self._fixed, dyp, lddy, xp, ldx, w13p, ldw13, w2p, ldw2, pre_p, h_p,
                                          dxp, lddx, dw13p, lddw13, dw2p, lddw2, M, _stream(stream, dev))

@@ -48,35 +48,46 @@ def moe_fp8_quant(x, form=MOE_FP8_ROWS, q=None, scale=None, stream=None):
     if dtype is None:
         _code(x, "x")
     on = x.device
+    # outputs made here need no checks
     if form == MOE_FP8_ROWS:
         if x.dim() != 2:
             raise ValueError(f"x must be [rows, K], not {list(x.shape)}")
         E, (rows, K) = 1, x.shape
         KB = _blocks(K)
-        xp, ldx = _rows(x, "x", dev, rows, K)
+        ldx, unit = x.stride()
+        if unit != 1 or ldx < K:
+            ldx = _rows(x, "x", dev, rows, K)[1]
+        ldq, lds = K, KB
         if q is None:
             q = torch.empty((rows, K), dtype=_E4M3, device=on)
-        qp, ldq = _rows(q, "q", dev, rows, K, _E4M3)
+        else:
+            ldq = _rows(q, "q", dev, rows, K, _E4M3)[1]
         if scale is None:
             scale = torch.empty((rows, KB), dtype=torch.float32, device=on)
-        sp, lds = _rows(scale, "scale", dev, rows, KB, torch.float32)
+        else:
+            lds = _rows(scale, "scale", dev, rows, KB, torch.float32)[1]
     elif form == MOE_FP8_TILES:
         if x.dim() not in (2, 3):
             raise ValueError(f"x must be [rows, K] or [E, rows, K], not {list(x.shape)}")
         E, rows, K = (1, *x.shape) if x.dim() == 2 else x.shape
         KB, lead = _blocks(K), x.shape[:-2]
-        xp, ldx = x.data_ptr(), _stack(x if lead else x.unsqueeze(0), "x", E, rows, K)
+        ldx = _stack(x if lead else x.unsqueeze(0), "x", E, rows, K)
+        ldq, lds = K, KB
         if q is None:
             q = torch.empty(x.shape, dtype=_E4M3, device=on)
-        elif q.shape != x.shape:
-            raise ValueError(f"q must be {list(x.shape)}, not {list(q.shape)}")
-        qp, ldq = _dev(q, "q", dev, _E4M3), _stack(q if lead else q.unsqueeze(0), "q", E, rows, K)
+        else:
+            if q.shape != x.shape:
+                raise ValueError(f"q must be {list(x.shape)}, not {list(q.shape)}")
+            _dev(q, "q", dev, _E4M3)
+            ldq = _stack(q if lead else q.unsqueeze(0), "q", E, rows, K)
         if scale is None:
             scale = torch.empty((*lead, _blocks(rows), KB), dtype=torch.float32, device=on)
-        sp, lds = _whole(scale, "scale", dev, torch.float32, E * _blocks(rows) * KB), KB
+        else:
+            _whole(scale, "scale", dev, torch.float32, E * _blocks(rows) * KB)
     else:
         raise ValueError(f"form {form} is neither MOE_FP8_ROWS nor MOE_FP8_TILES")
-    st = _lib.load().moe_fp8_quant(xp, dtype, ldx, E, rows, K, form, qp, ldq, sp, lds, _stream(stream, dev))
+    st = _lib.load().moe_fp8_quant(x.data_ptr(), dtype, ldx, E, rows, K, form, q.data_ptr(), ldq, scale.data_ptr(), lds,
+                                   _stream(stream, dev))
     if st:
         _check(st, "moe_fp8_quant")
     return q, scale
@@ -145,20 +156,25 @@ class MoEFp8:
         rows = x.shape[0]
         xsp, ldxs = _rows(x_scale, "x_scale", dev, rows, self.blocks, torch.float32)
         S = rows if perm is None else perm.numel()
-        ldw = _stack(w.unsqueeze(0) if self.E == 1 and w.dim() == 2 else w, "w", self.E, self.N, self.K)
+        if self.E == 1 and w.dim() == 2:
+            wp, ldw = _rows(w, "w", dev, self.N, self.K, _E4M3)
+        else:
+            wp, ldw = _dev(w, "w", dev, _E4M3), _stack(w, "w", self.E, self.N, self.K)
         if offsets is None:
             if self.E != 1:
                 raise ValueError("products of several experts need offsets")
             offsets_p = None
         else:
             offsets_p = _whole(offsets, "offsets", dev, torch.int32, self.E + 1)
+        ldo = self.cols
         if out is None:
-            out = torch.empty((S, self.cols), dtype=self.dtype, device=x.device)
-        op, ldo = _rows(out, "out", dev, S, self.cols, self.dtype)
+            out = torch.empty((S, ldo), dtype=self.dtype, device=x.device)
+        else:
+            ldo = _rows(out, "out", dev, S, ldo, self.dtype)[1]
         st = _lib.load().moe_fp8_run(
-            *self._fixed, xp, ldx, rows, xsp, ldxs, _dev(w, "w", dev, _E4M3), ldw,
+            *self._fixed, xp, ldx, rows, xsp, ldxs, wp, ldw,
             _whole(w_scale, "w_scale", dev, torch.float32, self.E * self.tall * self.blocks), offsets_p,
-            None if perm is None else _whole(perm, "perm", dev, torch.int32, S), topk, op, ldo, S,
+            None if perm is None else _whole(perm, "perm", dev, torch.int32, S), topk, out.data_ptr(), ldo, S,
             _stream(stream, dev))
         if st:
             _check(st, "moe_fp8_run")
