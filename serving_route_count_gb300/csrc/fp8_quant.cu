@@ -12,6 +12,8 @@
 // registers between the maximum and the codes.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "block_ops.cuh"
 #include "fp8.cuh"
 #include "../../include/moe_gb300.h"
@@ -48,13 +50,23 @@ struct Quant16 {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
+  // 16-bit values two at a time; either maximum leaves NaN out
   __device__ __forceinline__ float top() const {
-    T v[16];
-    memcpy(v, w, sizeof(v));
-    float m = 0.f;
+    if constexpr (sizeof(T) == 2) {
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      T2 v[8];
+      memcpy(v, w, sizeof(v));
+      T2 m = __habs2(v[0]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(to_f32(v[i])));
-    return m;
+      for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(v[i]));
+      return fmaxf(fmaxf(to_f32(m.x), to_f32(m.y)), 0.f);
+    } else {
+      float v[16], m = 0.f;
+      memcpy(v, w, sizeof(v));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+      return m;
+    }
   }
   // Codes by one reciprocal, with Markstein's correction: for r = 1 / s rounded to nearest and q within an
   // ulp of x / s, q + r (x - q s) with two fused operations is x / s rounded to nearest.  The residual has
@@ -95,16 +107,16 @@ __global__ void __launch_bounds__(256) quant_rows16_kernel(const QuantParams p) 
   const int sub = threadIdx.x & 7;
   pdl_wait_prev();
   pdl_launch_next();
-  const long long n = (long long)p.rows * p.KB, step = (long long)gridDim.x * 32;
-  for (long long i0 = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i0 < n; i0 += kQuantAhead * step) {
+  // blocks are counted in 32 bits: a division in 64 costs a quarter of the call
+  const unsigned n = (unsigned)p.rows * (unsigned)p.KB, step = gridDim.x * 32;
+  for (unsigned i0 = blockIdx.x * 32 + (threadIdx.x >> 3); i0 < n; i0 += kQuantAhead * step) {
     Quant16<T> v[kQuantAhead];
-    long long row[kQuantAhead];
-    int k[kQuantAhead];
+    int row[kQuantAhead], k[kQuantAhead];
 #pragma unroll
     for (int u = 0; u < kQuantAhead; ++u) {
-      const long long i = i0 + u * step;
-      row[u] = i < n ? i / p.KB : -1;
-      k[u] = row[u] < 0 ? p.K : (int)(i - row[u] * p.KB) * kFp8Block + 16 * sub;
+      const unsigned i = i0 + u * step, r = i / p.KB;
+      row[u] = i < n ? (int)r : -1;
+      k[u] = row[u] < 0 ? p.K : (int)(i - r * p.KB) * kFp8Block + 16 * sub;
       if (k[u] < p.K)
         v[u].load(static_cast<const T*>(p.x) + row[u] * p.ldx + k[u]);
       else
@@ -125,7 +137,7 @@ __global__ void __launch_bounds__(256) quant_rows16_kernel(const QuantParams p) 
 
 // Tiles on 16 bytes: a CTA per tile, 16 values of four rows to a thread.
 template <typename T>
-__global__ void __launch_bounds__(256) quant_tiles16_kernel(const QuantParams p, int tiles) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quant_tiles16_kernel(const QuantParams p, int tiles) {
   __shared__ float s_top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tall = fp8_blocks(p.rows);       // of one matrix
@@ -225,7 +237,7 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantParams p, i
 template <typename T>
 static cudaError_t launch_quant(const QuantParams& p, int E, bool tiles, cudaStream_t st) {
   // whole vectors of 16 values: K and row strides of them, bases on 16 bytes
-  const bool vec = p.K % 16 == 0 && p.ldq % 16 == 0 && p.ldx * (long long)sizeof(T) % 16 == 0 &&
+  bool vec = p.K % 16 == 0 && p.ldq % 16 == 0 && p.ldx * (long long)sizeof(T) % 16 == 0 &&
                    (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.q) & 15) == 0;
   if (tiles) {
     const long long n = (long long)E * fp8_blocks(p.rows) * p.KB;
@@ -233,6 +245,7 @@ static cudaError_t launch_quant(const QuantParams& p, int E, bool tiles, cudaStr
                          dim3(256), 0, st, true, p, (int)n);
   }
   const long long blocks = (long long)p.rows * p.KB;
+  vec = vec && blocks < (1LL << 31);         // counted in 32 bits, a grid's step past the end too
   const long long n = vec ? (blocks + 32 * kQuantAhead - 1) / (32 * kQuantAhead) : (blocks + 7) / 8;
   return launch_kernel(vec ? quant_rows16_kernel<T> : quant_rows_kernel<T>, dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)), dim3(256),
                        0, st, true, p);
