@@ -727,20 +727,18 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
 
 // ---------------------------------------------------------------------------------- host side
 
-// Token-tile width by the mean positions per expert, as for the 16-bit products; of one matrix without
-// offsets, whose rows are known, the narrowest that holds them.
-static int fp8_tc_bn(int S, int E, bool dense) {
-  const long long many = dense ? 1 : 4;
-  if ((long long)S * many <= 32LL * E) return 32;
+// Token-tile width by the mean positions per expert, as for the 16-bit products; of one matrix, whose rows
+// are known, the narrowest that holds them.
+static int fp8_tc_bn(int S, int E) {
+  const bool dense = E == 1;
+  if ((long long)S * (dense ? 1 : 4) <= 32LL * E) return 32;
   if (dense ? S <= 64 : (long long)S <= 24LL * E) return 64;
   if (dense ? S <= 128 : (long long)S <= 64LL * E) return 128;
   return 256;
 }
 
 size_t fp8_tc_part_bytes(int S, int E) {
-  // a call may have fewer rows than the plan, and offsets or none: the widest tile of any of them
-  const int bn = std::max(fp8_tc_bn(S, E, false), fp8_tc_bn(S, E, E == 1));
-  return (size_t)kGtMaxPairs * 2 * 2 * bn * 128 * sizeof(float);
+  return (size_t)kGtMaxPairs * 2 * 2 * fp8_tc_bn(S, E) * 128 * sizeof(float);
 }
 
 static bool f8_tmap(CUtensorMap* tm, int rank, const void* base, const cuuint64_t* dims,
@@ -817,7 +815,7 @@ static cudaError_t launch_f8(F8Params& p, cudaStream_t st) {
 
 template <typename T, bool ACT>
 static cudaError_t launch_f8_bn(F8Params& p, cudaStream_t st) {
-  switch (fp8_tc_bn(p.c.S, p.d.E, p.c.offsets == nullptr)) {
+  switch (fp8_tc_bn(p.c.S, p.d.E)) {
     case 32: return launch_f8<T, ACT, 32>(p, st);
     case 64: return launch_f8<T, ACT, 64>(p, st);
     case 128: return launch_f8<T, ACT, 128>(p, st);

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p
 
 // A few positions in whole vectors (their alignment as for the tensor cores).
 bool fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f) {
-  return f.c.S <= (f.c.offsets == nullptr ? 4 : 8) && d.K % 16 == 0;
+  return f.c.S <= (d.E == 1 ? 4 : 8) && d.K % 16 == 0;
 }
 
 template <typename T, bool ACT>
