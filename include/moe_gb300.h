@@ -572,16 +572,16 @@ moe_status moe_ff_scratch_bytes(const moe_ff_t* plan, size_t* bytes);
 /* y [M, H] of x [M, H], w13 [2 I, H], w2 [H, I] (row strides ld*).
  *   scratch  as for moe_grouped_run: its first 4096 bytes zero before the first use, calls that share it
  *            stream-ordered, moe_ff_get_device_error after a device error.
- *   pre, h   NULL, or [M, 2 I] and [M, I] (contiguous), which get up and gate in w13's order and h: what
- *            moe_ff_backward needs.  pre is rounded to the operand type, on the side of the limit where
- *            the fp32 value was, so that the backward pass clamps what the forward pass clamped.
+ *   pre, h   NULL, or [M, 2 I] fp32 and [M, I] of the operand type (contiguous), which get up and gate in
+ *            w13's order and h: what moe_ff_backward needs.  pre is not rounded: the backward pass clamps
+ *            what the forward pass clamped, and du and dg are rounded once.
  * y, pre and h must not overlap an input or one another.
  * Products whose operands and strides are 16-byte aligned run on the tensor cores; others (for instance
  * H % 8 != 0) on the CUDA cores, slower.
  * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (M > max_rows), MOE_ERR_CUDA. */
 moe_status moe_ff_forward(const moe_ff_t* plan, void* scratch, size_t scratch_bytes, const void* x,
                           long long ldx, const void* w13, long long ldw13, const void* w2, long long ldw2,
-                          void* pre, void* h, void* y, long long ldy, int M, void* stream);
+                          float* pre, void* h, void* y, long long ldy, int M, void* stream);
 /* Gradients of y at dy [M, H]: dx [M, H], dw13 [2 I, H], dw2 [H, I], each NULL where it is not wanted (and
  * what only it needs may be NULL then: x for dw13, w13 for dx, h for dw2, w2 and pre for dx and dw13).
  *   dh = dy W2,  du = dh g' s [|up| <= limit],  dg = dh (u' + beta) (s + alpha g' s (1 - s)) [gate <= limit],
@@ -591,7 +591,7 @@ moe_status moe_ff_forward(const moe_ff_t* plan, void* scratch, size_t scratch_by
  * an input or one another.  Errors as moe_ff_forward. */
 moe_status moe_ff_backward(const moe_ff_t* plan, void* scratch, size_t scratch_bytes, const void* dy,
                            long long lddy, const void* x, long long ldx, const void* w13, long long ldw13,
-                           const void* w2, long long ldw2, const void* pre, const void* h, void* dx,
+                           const void* w2, long long ldw2, const float* pre, const void* h, void* dx,
                            long long lddx, void* dw13, long long lddw13, void* dw2, long long lddw2, int M,
                            void* stream);
 /* As moe_grouped_get_device_error. */

@@ -79,7 +79,7 @@ moe_status moe_ff_scratch_bytes(const moe_ff_t* plan, size_t* bytes) {
 
 moe_status moe_ff_forward(const moe_ff_t* plan, void* scratch, size_t scratch_bytes, const void* x,
                           long long ldx, const void* w13, long long ldw13, const void* w2, long long ldw2,
-                          void* pre, void* h, void* y, long long ldy, int M, void* stream) {
+                          float* pre, void* h, void* y, long long ldy, int M, void* stream) {
   if (plan == nullptr || M < 0) return MOE_ERR_ARG;
   const FfDims& d = plan->d;
   if (M > d.max_rows) return MOE_ERR_CAPACITY;
@@ -100,7 +100,7 @@ moe_status moe_ff_forward(const moe_ff_t* plan, void* scratch, size_t scratch_by
 
 moe_status moe_ff_backward(const moe_ff_t* plan, void* scratch, size_t scratch_bytes, const void* dy,
                            long long lddy, const void* x, long long ldx, const void* w13, long long ldw13,
-                           const void* w2, long long ldw2, const void* pre, const void* h, void* dx,
+                           const void* w2, long long ldw2, const float* pre, const void* h, void* dx,
                            long long lddx, void* dw13, long long lddw13, void* dw2, long long lddw2, int M,
                            void* stream) {
   if (plan == nullptr || M < 0) return MOE_ERR_ARG;
@@ -126,7 +126,7 @@ moe_status moe_ff_backward(const moe_ff_t* plan, void* scratch, size_t scratch_b
   const long long I2 = 2LL * d.I;
   cudaError_t e = cudaSuccess;
   if (inner)                              // dh = dy W2, then through the activation
-    e = product(*plan, FfGemm{w2, 1, ldw2, 0, dy, lddy, 1, d.I, M, d.H, dp, I2, const_cast<void*>(pre), err}, kFfGrad, st);
+    e = product(*plan, FfGemm{w2, 1, ldw2, 0, dy, lddy, 1, d.I, M, d.H, dp, I2, const_cast<float*>(pre), err}, kFfGrad, st);
   if (dx && e == cudaSuccess)             // dx = d(up, gate) W13
     e = product(*plan, FfGemm{w13, 1, ldw13, 0, dp, I2, 1, d.H, M, (int)I2, dx, lddx, nullptr, err}, kFfStore, st);
   if (dw13 && e == cudaSuccess)           // dW13 = d(up, gate)^T x

@@ -29,31 +29,9 @@ struct FfGemm {
   int nr, nc, K;
   void* out;
   long long ldo;
-  void* pre;                           // [nc, 2 nr]: written (kFfGlu, or NULL), read (kFfGrad)
+  float* pre;                          // [nc, 2 nr]: written (kFfGlu, or NULL), read (kFfGrad)
   int32_t* err;                        // device error word
 };
-
-// The 16 bits of v in T, on the same side of `bound` >= 0 as v itself, for v >= 0 or any v where
-// bound > 0: what clamps is told by the saved value as by the sum that it was rounded from.  Next to each
-// other, values of one sign differ by one in their bits.
-__device__ __forceinline__ uint32_t bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
-__device__ __forceinline__ uint32_t bits16(__half v) { return __half_as_ushort(v); }
-template <typename T>
-__device__ __forceinline__ uint32_t round_same_side(float v, float bound) {
-  const T t = from_f32<T>(v);
-  const float f = to_f32(t);
-  uint32_t b = bits16(t);
-  b += v > bound && f <= bound;        // v > bound > 0: f is 0 or positive
-  b -= v <= bound && f > bound;        // f > bound > 0
-  return b;
-}
-// The saved forms of gate and up.
-template <typename T>
-__device__ __forceinline__ uint32_t save_gate(float g, float limit) { return round_same_side<T>(g, limit); }
-template <typename T>
-__device__ __forceinline__ uint32_t save_up(float u, float limit) {
-  return round_same_side<T>(fabsf(u), limit) | (__float_as_uint(u) >> 16 & 0x8000u);
-}
 
 // Gradients of swiglu_f32 by up and gate, times dh.  A clamp passes the gradient within its bounds, the
 // bounds included.  With s = sigmoid(a), a = alpha g': d/dg' (g' s (u' + beta)) = (u' + beta) (s + a s (1 - s)),

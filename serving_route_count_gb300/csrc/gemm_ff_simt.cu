@@ -30,7 +30,6 @@ ff_simt_kernel(const FfsParams p) {
   const T* R = static_cast<const T*>(g.r);
   const T* C = static_cast<const T*>(g.c);
   T* out = static_cast<T*>(g.out);
-  T* pre = static_cast<T*>(g.pre);
   const int c0 = blockIdx.x * kGsTile;
   for (int r0 = blockIdx.y * kGsTile; r0 < g.nr; r0 += gridDim.y * kGsTile) {
     float acc[kSets][4][4] = {};
@@ -70,20 +69,20 @@ ff_simt_kernel(const FfsParams p) {
         const int c = c0 + 4 * tr + i, r = r0 + 4 * tc + j;
         if (c >= g.nc || r >= g.nr) continue;
         T* o = out + c * g.ldo + r;
-        T* s = EPI == kFfStore ? nullptr : pre + (long long)c * 2 * g.nr + r;
+        float* s = EPI == kFfStore ? nullptr : g.pre + (long long)c * 2 * g.nr + r;
         const bool up_first = p.d.layout == MOE_W13_UP_GATE;
         if constexpr (EPI == kFfStore) {
           *o = from_f32<T>(acc[0][i][j]);
         } else if constexpr (EPI == kFfGlu) {
           const float u = acc[up_first ? 0 : kSets - 1][i][j], gt = acc[up_first ? kSets - 1 : 0][i][j];
           *o = from_f32<T>(swiglu_f32(u, gt, p.d.limit, p.d.alpha, p.d.beta));
-          if (pre != nullptr) {
-            reinterpret_cast<uint16_t*>(s)[up_first ? 0 : g.nr] = (uint16_t)save_up<T>(u, p.d.limit);
-            reinterpret_cast<uint16_t*>(s)[up_first ? g.nr : 0] = (uint16_t)save_gate<T>(gt, p.d.limit);
+          if (g.pre != nullptr) {
+            s[up_first ? 0 : g.nr] = u;
+            s[up_first ? g.nr : 0] = gt;
           }
         } else {
           float du, dg;
-          swiglu_grad(to_f32(s[up_first ? 0 : g.nr]), to_f32(s[up_first ? g.nr : 0]), acc[0][i][j], p.d.limit,
+          swiglu_grad(s[up_first ? 0 : g.nr], s[up_first ? g.nr : 0], acc[0][i][j], p.d.limit,
                       p.d.alpha, p.d.beta, &du, &dg);
           o[up_first ? 0 : g.nr] = from_f32<T>(du);
           o[up_first ? g.nr : 0] = from_f32<T>(dg);

@@ -58,17 +58,6 @@ __device__ __forceinline__ uint32_t ft_pack(bool bf16, float a, float b) {
   __half2 v = __floats2half2_rn(a, b);
   return reinterpret_cast<uint32_t&>(v);
 }
-__device__ __forceinline__ float2 ft_unpack(bool bf16, uint32_t w) {
-  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(reinterpret_cast<__half2&>(w));
-}
-// The saved forms of up and gate, as 16 bits.
-__device__ __forceinline__ uint32_t ft_save(bool bf16, bool up, float v, float limit) {
-  if (bf16) return up ? save_up<__nv_bfloat16>(v, limit) : save_gate<__nv_bfloat16>(v, limit);
-  return up ? save_up<__half>(v, limit) : save_gate<__half>(v, limit);
-}
-__device__ __forceinline__ uint32_t ft_pair(uint32_t lo, uint32_t hi) { return lo | (hi << 16); }
-
 // Epilogue of 32 accumulator columns (rows c0 .. c0 + 31 of the unit's tile of n rows of C from p0) of
 // this lane's row of R; col0: output column of the CTA's first row.  A lane and its neighbour exchange
 // every other row of C, so that each access takes two adjacent columns; where rows do not start on 4 bytes
@@ -77,7 +66,7 @@ template <int EPI>
 __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int p0, int n, int col0, int c0,
                                          int q, int lane) {
   uint16_t* out = static_cast<uint16_t*>(p.g.out);
-  uint16_t* pre = static_cast<uint16_t*>(p.g.pre);
+  float* pre = p.g.pre;
   const int odd = lane & 1, nr = p.g.nr;
   const bool bf16 = p.bf16;
   const long long ldo = p.g.ldo;
@@ -117,26 +106,21 @@ __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int 
     const auto act = [&](int c) {
       return swiglu_f32(up_first ? a[c] : b[c], up_first ? b[c] : a[c], p.d.limit, p.d.alpha, p.d.beta);
     };
+    if (pre != nullptr) {
+      const int m = col < nr ? n - t0 : 0;
+      float* s = pre + (long long)(p0 + t0) * 2 * nr + col;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        if (c < m) {
+          s[0] = a[c];
+          s[nr] = b[c];
+        }
+        s += 2LL * nr;
+      }
+    }
     if (p.packed) {
       const int m = col < nr ? n - t0 - odd : 0;
       uint16_t* o = out + (long long)(p0 + t0 + odd) * ldo + (col & ~1);
-      if (pre != nullptr) {
-        uint16_t* s = pre + (long long)(p0 + t0 + odd) * 2 * nr + (col & ~1);
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          // this lane's values of both rows, then both columns of this lane's row
-          const uint32_t a0 = ft_pair(ft_save(bf16, up_first, a[c], p.d.limit), ft_save(bf16, up_first, a[c + 1], p.d.limit));
-          const uint32_t b0 = ft_pair(ft_save(bf16, !up_first, b[c], p.d.limit), ft_save(bf16, !up_first, b[c + 1], p.d.limit));
-          const uint32_t a1 = __shfl_xor_sync(0xffffffffu, a0, 1), b1 = __shfl_xor_sync(0xffffffffu, b0, 1);
-          const uint32_t wa = odd ? __byte_perm(a1, a0, 0x7632) : __byte_perm(a0, a1, 0x5410);
-          const uint32_t wb = odd ? __byte_perm(b1, b0, 0x7632) : __byte_perm(b0, b1, 0x5410);
-          if (c < m) {
-            *reinterpret_cast<uint32_t*>(s) = wa;
-            *reinterpret_cast<uint32_t*>(s + nr) = wb;
-          }
-          s += 4LL * nr;
-        }
-      }
 #pragma unroll
       for (int c = 0; c < 16; c += 2) {
         const float h0 = act(c), h1 = act(c + 1);
@@ -148,18 +132,10 @@ __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int 
     } else {
       const int m = col < nr ? n - t0 : 0;
       uint16_t* o = out + (long long)(p0 + t0) * ldo + col;
-      uint16_t* s = pre + (long long)(p0 + t0) * 2 * nr + col;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        if (c < m) {
-          *o = (uint16_t)ft_pack(bf16, act(c), 0.f);
-          if (pre != nullptr) {
-            s[0] = (uint16_t)ft_save(bf16, up_first, a[c], p.d.limit);
-            s[nr] = (uint16_t)ft_save(bf16, !up_first, b[c], p.d.limit);
-          }
-        }
+        if (c < m) *o = (uint16_t)ft_pack(bf16, act(c), 0.f);
         o += ldo;
-        s += 2LL * nr;
       }
     }
   } else {
@@ -173,15 +149,15 @@ __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int 
     };
     if (p.packed) {
       const int m = col < nr ? n - c0 - odd : 0;
-      const uint16_t* s = pre + (long long)(p0 + c0 + odd) * 2 * nr + (col & ~1);
+      const float* s = pre + (long long)(p0 + c0 + odd) * 2 * nr + (col & ~1);
       uint16_t* o = out + (long long)(p0 + c0 + odd) * ldo + (col & ~1);
-      uint32_t x0[16], x1[16];
+      float2 x0[16], x1[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        x0[c] = x1[c] = 0;
+        x0[c] = x1[c] = make_float2(0.f, 0.f);
         if (2 * c < m) {
-          x0[c] = __ldcg(reinterpret_cast<const uint32_t*>(s));
-          x1[c] = __ldcg(reinterpret_cast<const uint32_t*>(s + nr));
+          x0[c] = __ldcg(reinterpret_cast<const float2*>(s));
+          x1[c] = __ldcg(reinterpret_cast<const float2*>(s + nr));
         }
         s += 4LL * nr;
       }
@@ -189,7 +165,7 @@ __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int 
       for (int c = 0; c < 32; c += 2) {
         const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
         const float h0 = odd ? got : v[c], h1 = odd ? v[c + 1] : got;
-        const float2 f0 = ft_unpack(bf16, x0[c / 2]), f1 = ft_unpack(bf16, x1[c / 2]);
+        const float2 f0 = x0[c / 2], f1 = x1[c / 2];
         float d00, d01, d10, d11;
         grad(f0.x, f1.x, h0, &d00, &d01);
         grad(f0.y, f1.y, h1, &d10, &d11);
@@ -201,13 +177,13 @@ __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int 
       }
     } else {
       const int m = col < nr ? n - c0 : 0;
-      const uint16_t* s = pre + (long long)(p0 + c0) * 2 * nr + col;
+      const float* s = pre + (long long)(p0 + c0) * 2 * nr + col;
       uint16_t* o = out + (long long)(p0 + c0) * ldo + col;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         if (c < m) {
           float d0, d1;
-          grad(ft_unpack(bf16, s[0]).x, ft_unpack(bf16, s[nr]).x, v[c], &d0, &d1);
+          grad(s[0], s[nr], v[c], &d0, &d1);
           o[0] = (uint16_t)ft_pack(bf16, d0, 0.f);
           o[nr] = (uint16_t)ft_pack(bf16, d1, 0.f);
         }
@@ -662,7 +638,7 @@ cudaError_t launch_ff_tc(const FfDims& d, const FfGemm& g, int epilogue, float* 
   p.c_mn = g.ck != 1;
   p.bf16 = d.dtype == MOE_DTYPE_BF16;
   p.packed = g.nr % 2 == 0 && g.ldo % 2 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 3) == 0 &&
-             (reinterpret_cast<uintptr_t>(g.pre) & 3) == 0;
+             (reinterpret_cast<uintptr_t>(g.pre) & 7) == 0;
   if (epilogue == kFfGlu) return launch_ft_bn<kFfGlu>(p, st);
   if (epilogue == kFfGrad) return launch_ft_bn<kFfGrad>(p, st);
   return launch_ft_bn<kFfStore>(p, st);

@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(kFvThreads) ff_gemv_kernel(const FvParams p) {
     const float u = v[up_first ? 0 : 1], gt = v[up_first ? 1 : 0];
     *o = from_f32<T>(swiglu_f32(u, gt, p.d.limit, p.d.alpha, p.d.beta));
     if (g.pre != nullptr) {
-      uint16_t* s = static_cast<uint16_t*>(g.pre) + (long long)lane * 2 * g.nr + r;
-      s[up_first ? 0 : g.nr] = (uint16_t)save_up<T>(u, p.d.limit);
-      s[up_first ? g.nr : 0] = (uint16_t)save_gate<T>(gt, p.d.limit);
+      float* s = g.pre + (long long)lane * 2 * g.nr + r;
+      s[up_first ? 0 : g.nr] = u;
+      s[up_first ? g.nr : 0] = gt;
     }
   }
 }

@@ -75,12 +75,12 @@ class MoEFeedForward:
         return self._forward(x, w13, w2, out, None, stream)
 
     def forward(self, x, w13, w2, out=None, saved=None, stream=None):
-        """(y, saved): saved = (up and gate [M, 2 I] in w13's order, h [M, I]) is what backward needs, in new
+        """(y, saved): saved = (up and gate [M, 2 I] in w13's order, fp32, and h [M, I]) is what backward needs, in new
         tensors or the given ones."""
         made = None
         if saved is None:
             on, M = x.device, x.shape[0]
-            saved = made = (torch.empty((M, 2 * self.I), dtype=self.dtype, device=on),
+            saved = made = (torch.empty((M, 2 * self.I), dtype=torch.float32, device=on),
                             torch.empty((M, self.I), dtype=self.dtype, device=on))
         return self._forward(x, w13, w2, out, saved, stream, made is None), saved
 
@@ -95,7 +95,7 @@ class MoEFeedForward:
         if saved is not None:
             pre, h = saved
             if given:                  # tensors made here need no checks
-                _whole(pre, "saved[0]", dev, dtype, M * 2 * I)
+                _whole(pre, "saved[0]", dev, torch.float32, M * 2 * I)
                 _whole(h, "saved[1]", dev, dtype, M * I)
             pre_p, h_p = pre.data_ptr(), h.data_ptr()
         ldo = H
@@ -121,7 +121,7 @@ class MoEFeedForward:
         w13p, ldw13 = _rows(w13, "w13", dev, 2 * I, H, dtype)
         w2p, ldw2 = _rows(w2, "w2", dev, H, I, dtype)
         pre, h = saved
-        pre_p, h_p = _whole(pre, "saved[0]", dev, dtype, M * 2 * I), _whole(h, "saved[1]", dev, dtype, M * I)
+        pre_p, h_p = _whole(pre, "saved[0]", dev, torch.float32, M * 2 * I), _whole(h, "saved[1]", dev, dtype, M * I)
         wanted, on = [], dy.device
         for needed, t, name, rows, cols in zip(need, (dx, dw13, dw2), ("dx", "dw13", "dw2"), (M, 2 * I, H), (H, H, I)):
             if not needed:
