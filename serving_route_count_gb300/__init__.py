@@ -23,9 +23,10 @@ from .block import (  # noqa: F401
     MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_NORM_RMS, MOE_NORM_LAYER,
 )
 from .fp8 import (  # noqa: F401
-    MoEFp8, moe_fp8_quant, moe_fp8_plan, moe_fp8_scratch_bytes, moe_fp8_get_device_error, moe_destroy_fp8,
+    MoEFp8, moe_fp8_quant, moe_fp8_plan, moe_fp8_scratch_bytes, moe_fp8_set_wait_probe, moe_fp8_get_device_error,
+    moe_destroy_fp8,
     MOE_FP8_ROWS, MOE_FP8_TILES,
 )
 from .feed_forward import (  # noqa: F401
-    MoEFeedForward, moe_ff_plan, moe_ff_scratch_bytes, moe_ff_get_device_error, moe_destroy_ff,
+    MoEFeedForward, moe_ff_plan, moe_ff_scratch_bytes, moe_ff_set_wait_probe, moe_ff_get_device_error, moe_destroy_ff,
 )

@@ -101,6 +101,7 @@ SIGNATURES = {
     "moe_fp8_run": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_int, c_void_p,
                             c_longlong, c_void_p, c_longlong, c_void_p, c_void_p, c_void_p, c_int,
                             c_void_p, c_longlong, c_int, c_void_p]),
+    "moe_fp8_set_wait_probe": (c_int, [c_void_p, ctypes.c_ulonglong]),
     "moe_fp8_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
     "moe_destroy_fp8": (None, [c_void_p]),
     "moe_ff_plan": (c_int, [c_int, c_int, c_int, c_int, c_float, c_float, c_float, c_int,
@@ -112,6 +113,7 @@ SIGNATURES = {
     "moe_ff_backward": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p, c_longlong, c_void_p, c_longlong,
                                 c_void_p, c_longlong, c_void_p, c_longlong, c_void_p, c_void_p, c_void_p,
                                 c_longlong, c_void_p, c_longlong, c_void_p, c_longlong, c_int, c_void_p]),
+    "moe_ff_set_wait_probe": (c_int, [c_void_p, ctypes.c_ulonglong]),
     "moe_ff_get_device_error": (c_int, [c_void_p, c_void_p, c_void_p, c_int_p]),
     "moe_destroy_ff": (None, [c_void_p]),
 }

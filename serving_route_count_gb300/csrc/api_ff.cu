@@ -69,6 +69,12 @@ moe_status moe_ff_plan(int H, int I, int dtype, int layout, float limit, float a
   return MOE_OK;
 }
 
+moe_status moe_ff_set_wait_probe(moe_ff_t* plan, unsigned long long ns) {
+  if (plan == nullptr || ns > 1000000000ull) return MOE_ERR_ARG;
+  plan->d.probe_ns = ns;
+  return MOE_OK;
+}
+
 void moe_destroy_ff(moe_ff_t* plan) { delete plan; }
 
 moe_status moe_ff_scratch_bytes(const moe_ff_t* plan, size_t* bytes) {

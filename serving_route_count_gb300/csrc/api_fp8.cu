@@ -75,6 +75,12 @@ moe_status moe_fp8_plan(int E, int N, int K, int dtype, int act, int layout, flo
   return MOE_OK;
 }
 
+moe_status moe_fp8_set_wait_probe(moe_fp8_t* plan, unsigned long long ns) {
+  if (plan == nullptr || ns > 1000000000ull) return MOE_ERR_ARG;
+  plan->d.probe_ns = ns;
+  return MOE_OK;
+}
+
 void moe_destroy_fp8(moe_fp8_t* plan) { delete plan; }
 
 moe_status moe_fp8_scratch_bytes(const moe_fp8_t* plan, size_t* bytes) {

@@ -30,6 +30,10 @@ def moe_ff_scratch_bytes(plan) -> int:
     return n.value
 
 
+def moe_ff_set_wait_probe(plan, ns):
+    _check(_lib.load().moe_ff_set_wait_probe(plan, int(ns)), "moe_ff_set_wait_probe")
+
+
 def moe_ff_get_device_error(plan, scratch, stream=None):
     """(status, code) of the device error word in `scratch`, which is cleared."""
     code = ctypes.c_int()

@@ -106,6 +106,10 @@ def moe_fp8_scratch_bytes(plan) -> int:
     return n.value
 
 
+def moe_fp8_set_wait_probe(plan, ns):
+    _check(_lib.load().moe_fp8_set_wait_probe(plan, int(ns)), "moe_fp8_set_wait_probe")
+
+
 def moe_fp8_get_device_error(plan, scratch, stream=None):
     """(status, code) of the device error word in `scratch`, which is cleared."""
     code = ctypes.c_int()

@@ -89,6 +89,12 @@ def test_arguments():
     for bad in (dict(plan=None), dict(M=-1), dict(scratch=None), dict(scratch=8), dict(size=4095), dict(dy=None), dict(x=None), dict(w13=None), dict(w2=None),
                 dict(pre=None), dict(h=None), dict(lddy=63), dict(ldx=63), dict(ld13=63), dict(ld2=31), dict(lddx=63), dict(ldd13=63), dict(ldd2=31)):
         assert bwd(**bad) == 1, bad
+    m.moe_ff_set_wait_probe(p, 1_000_000_000)
+    m.moe_ff_set_wait_probe(p, 0)
+    for plan, ns in ((p, 1_000_000_001), (None, 0)):
+        with pytest.raises(m.MoEError) as e:
+            m.moe_ff_set_wait_probe(plan, ns)
+        assert e.value.status == 1
     m.moe_destroy_ff(p)
     for bad, status in (((0, 8, 0, 0, 1.0), 2), ((8, 0, 0, 0, 1.0), 2), ((8, 8, 2, 0, 1.0), 3), ((8, 8, 0, 2, 1.0), 1), ((8, 8, 0, 0, -1.0), 1),
                         ((8, 8, 0, 0, math.nan), 1), (((1 << 20) + 1, 8, 0, 0, 1.0), 2)):
@@ -245,6 +251,45 @@ def test_many_units(moe, M, H, I):
         y2, saved2 = op.forward(x, w13, w2)
         assert torch.equal(y2, y) and all(torch.equal(a, b) for a, b in zip(saved, saved2))
         assert all(torch.equal(a, b) for a, b in zip(grads, op.backward(dy, x, w13, w2, saved)))
+    assert op.device_error() == (0, 0)
+
+
+@gpu
+@pytest.mark.parametrize("M,H,I", [(2, 4096, 1152), (3, 520, 2056), (4, 264, 8), (4, 8, 264), (5, 520, 136), (1, 7176, 40)])
+def test_a_few_tokens(moe, M, H, I):
+    """Up to four tokens and one more; a forward pass that is captured, between calls that change its input."""
+    for layout in (0, 1):
+        op, (x, w13, w2, dy), y, saved, grads = check(moe, M, H, I, "bf16", seed=M, layout=layout, limit=1.0)
+    out = torch.empty_like(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op(x, w13, w2, out=out)
+    keep = x.clone()
+    for _ in range(3):
+        x.zero_()
+        graph.replay()
+        assert torch.count_nonzero(out) == 0
+        x.copy_(keep)
+        graph.replay()
+        assert torch.equal(out, y)
+    assert op.device_error() == (0, 0)
+
+
+@gpu
+@pytest.mark.parametrize("M,H,I", [(40, 4096, 256), (600, 1024, 4096)])
+def test_a_wait_that_runs_out(moe, M, H, I):
+    """The first CTA pair's MMA issuer gives up a wait of 2 ms in every product: both passes end with MOE_ERR_TIMEOUT in the error
+    word, and the next ones give the results of a plan that never saw it."""
+    op, (x, w13, w2, dy), y, saved, grads = check(moe, M, H, I, "bf16")
+    moe.moe_ff_set_wait_probe(op.plan, 2_000_000)
+    op(x, w13, w2)
+    assert op.device_error() == (7, 2)
+    op.backward(dy, x, w13, w2, saved)
+    assert op.device_error() == (7, 2)
+    moe.moe_ff_set_wait_probe(op.plan, 0)
+    for _ in range(3):
+        y2, s2 = op.forward(x, w13, w2)
+        assert torch.equal(y2, y) and all(torch.equal(a, b) for a, b in zip(grads, op.backward(dy, x, w13, w2, s2)))
     assert op.device_error() == (0, 0)
 
 

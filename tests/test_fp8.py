@@ -70,6 +70,12 @@ def test_arguments():
                 dict(ws=None), dict(out=None), dict(ldx=255), dict(ldxs=1), dict(ldw=255), dict(ldo=127), dict(rows=15), dict(off=None),
                 dict(perm=1, topk=0), dict(perm=1, rows=0)):
         assert run(**bad) == 1, bad
+    m.moe_fp8_set_wait_probe(p, 1_000_000_000)
+    m.moe_fp8_set_wait_probe(p, 0)
+    for plan, ns in ((p, 1_000_000_001), (None, 0)):
+        with pytest.raises(m.MoEError) as e:
+            m.moe_fp8_set_wait_probe(plan, ns)
+        assert e.value.status == 1
     m.moe_destroy_fp8(p)
     for bad, status in (((0, 8, 8, 0, 0), 2), ((1025, 8, 8, 0, 0), 2), ((1, 0, 8, 0, 0), 2), ((1, 8, 0, 0, 0), 2), ((1, 7, 8, 0, 1), 2),
                         ((1, 8, 8, 2, 0), 3), ((1, 8, 8, 0, 5), 3)):
@@ -409,6 +415,65 @@ def test_product_reports_bad_tables(moe, K):
         op(x, xs, w, ws, torch.tensor(o, dtype=torch.int32, device="cuda"), perm=perm, topk=2)
         assert op.device_error() == (8, 1)
     check(moe, x, xs, w, ws, off, perm, S, "bf16", 2, op=op)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,act", [("bf16", True), ("f16", False)])
+@pytest.mark.parametrize("counts,pad", [([1] * 8, 0), ([8] + [0] * 7, 0), ([0, 3, 0, 0, 2, 0, 0, 1], 2), ([0] * 7 + [1], 0), ([0] * 8, 4),
+                                        ([2, 0, 0, 0, 0, 0, 0, 3], 3), ([9] + [0] * 7, 0)])
+def test_product_of_a_few_positions(moe, counts, pad, dtype, act):
+    """One token's slots, several of one expert, dropped ones; K that a warp's vectors do not divide."""
+    for N, K in ((130, 1040), (2, 16), (2050, 144)):
+        for gather in (False, True):
+            topk = 4 if gather else 1
+            check(moe, *case(8, N, K, counts, gather, topk, act, seed=N, pad=pad), dtype, topk, act, limit=2.0)
+
+
+@gpu
+@pytest.mark.parametrize("S", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("K", [16, 128, 528, 7184])
+def test_dense_of_a_few_positions(moe, S, K):
+    for N, act in ((5, False), (640, False), (384, True)):
+        x, xs, w, ws, off, _, _ = case(1, N, K, [S], False, act=act, seed=S)
+        got = check(moe, x, xs, w, ws, None, None, S, act=act)
+        op = moe.MoEFp8(1, N, K, max_rows=8, act=moe.MOE_ACT_SWIGLU if act else moe.MOE_ACT_NONE)
+        perm = torch.tensor([2 * i for i in reversed(range(S))], dtype=torch.int32, device="cuda")
+        assert torch.equal(op(x, xs, w, ws, perm=perm, topk=2), got.flip(0))
+
+
+@gpu
+def test_few_positions_report_bad_tables(moe):
+    x, xs, w, ws, off, perm, S = case(3, 64, 64, [2, 2, 2], True, 2)
+    op = moe.MoEFp8(3, 64, 64, max_rows=S)
+    for bad in (10 ** 6, -7):
+        p = perm.clone()
+        p[5] = bad
+        op(x, xs, w, ws, off, perm=p, topk=2)
+        assert op.device_error() == (8, 1)
+    for o in ([0, 4, 2, 6], [0, 2, 4, 7], [-1, 2, 4, 6]):
+        op(x, xs, w, ws, torch.tensor(o, dtype=torch.int32, device="cuda"), perm=perm, topk=2)
+        assert op.device_error() == (8, 1)
+    check(moe, x, xs, w, ws, off, perm, S, "bf16", 2, op=op)
+
+
+@gpu
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,N,K,act", [([9, 0, 8], 512, 4096, True),             # units cut by K steps
+                                            ([40, 300, 7], 8192, 512, False),         # more units than CTA pairs, whole ones first
+                                            ([20, 400, 130], 1024, 8192, True)])      # tokens as M, cut units
+def test_a_wait_that_runs_out(moe, counts, N, K, act, gather):
+    """The first CTA pair's MMA issuer gives up a wait of 2 ms: the call ends with MOE_ERR_TIMEOUT in the error word, and the
+    next one gives the result of a plan that never saw it."""
+    x, xs, w, ws, off, perm, S = case(len(counts), N, K, counts, gather, 1, act, seed=K)
+    new = lambda: moe.MoEFp8(len(counts), N, K, max_rows=S, act=moe.MOE_ACT_SWIGLU if act else moe.MOE_ACT_NONE)  # noqa: E731
+    want, op = new()(x, xs, w, ws, off, perm=perm), new()
+    moe.moe_fp8_set_wait_probe(op.plan, 2_000_000)
+    op(x, xs, w, ws, off, perm=perm)
+    assert op.device_error() == (7, 2)
+    moe.moe_fp8_set_wait_probe(op.plan, 0)
+    for _ in range(3):
+        assert torch.equal(op(x, xs, w, ws, off, perm=perm), want)
+    assert op.device_error() == (0, 0)
 
 
 @gpu
