@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quant_tiles16_ker
   const int tall = fp8_blocks(p.rows);       // of one matrix
   pdl_wait_prev();
   pdl_launch_next();
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  for (unsigned t = blockIdx.x; t < (unsigned)tiles; t += gridDim.x) {
     const int b = t % p.KB, rb = t / p.KB;   // rb: tile row over all matrices
     const int e = rb / tall, r0 = (rb - e * tall) * kFp8Block, k = b * kFp8Block + 16 * (threadIdx.x & 7);
     const long long first = (long long)e * p.rows + r0;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) quant_tiles_kernel(const QuantParams p, i
   const int tall = fp8_blocks(p.rows);       // of one matrix
   pdl_wait_prev();
   pdl_launch_next();
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  for (unsigned t = blockIdx.x; t < (unsigned)tiles; t += gridDim.x) {
     const int b = t % p.KB, rb = t / p.KB;   // rb: tile row over all matrices
     const int e = rb / tall, r0 = (rb - e * tall) * kFp8Block, k0 = b * kFp8Block;
     const int n = min(kFp8Block, p.rows - r0);

@@ -24,12 +24,10 @@ using namespace tc;
 constexpr int kFtThreads = 384;
 constexpr int kFtK = 64;                 // K step: one 128-byte swizzled row
 
-template <int BN, int ACC>
+template <int BN>
 struct FtCfg {
-  static constexpr int kAcc = ACC;                           // accumulators of a unit
   static constexpr int kHalf = BN / 2;                       // rows of C that a CTA loads
-  static constexpr int kBytesR = 128 * 128;                  // rows of R of one accumulator
-  static constexpr int kBytesA = kAcc * kBytesR, kBytesB = kHalf * 128, kStage = kBytesA + kBytesB;
+  static constexpr int kBytesR = 128 * 128, kBytesC = kHalf * 128, kStage = kBytesR + kBytesC;
   static constexpr int kTables = 512;                        // barriers
   static constexpr int kStages = (227 * 1024 - 1024 - kTables) / kStage > 12
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
@@ -41,9 +39,9 @@ struct FtParams {
   CUtensorMap tm_r, tm_c;
   FfDims d;
   FfGemm g;
-  float* part;          // [pairs][2][2 CTAs][accumulators][BN / 4][128][4]
-  int32_t* tickets;     // [pairs][2 CTAs][2 accumulators]
-  int KT, RB, half;     // RB: row blocks with all accumulators; half: one more with one
+  float* part;          // [pairs][2][2 CTAs][BN / 4][128][4]
+  int32_t* tickets;     // [pairs][2 CTAs]
+  int KT, RB;           // K steps; row blocks
   int tiles, size;      // tiles of C, rows of a tile (the last may have fewer)
   int cut;              // whether the units left over are cut along K
   int r_mn, c_mn;       // operand stored with its rows along the contiguous dimension
@@ -194,10 +192,10 @@ __device__ __forceinline__ void ft_store(const FtParams& p, float (&v)[32], int 
   }
 }
 
-template <int EPI, int BN, int ACC>
+template <int EPI, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFtThreads, 1)
 ff_tc_kernel(const __grid_constant__ FtParams p) {
-  using Cfg = FtCfg<BN, ACC>;
+  using Cfg = FtCfg<BN>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* st = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -237,9 +235,9 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
   pdl_launch_next();
 
   // Every loop below is taken by whole warps; one lane issues.
-  constexpr int kRows = EPI == kFfGlu ? 64 : 128;    // output columns of one CTA and accumulator
+  constexpr int kRows = EPI == kFfGlu ? 64 : 128;    // output columns of one CTA
   GtWork work;
-  work.init(p.tiles, p.KT, p.RB, p.half, G, pair, p.cut ? 0 : 0x7FFFFFFF, false);
+  work.init(p.tiles, p.KT, p.RB, 0, G, pair, p.cut ? 0 : 0x7FFFFFFF, false);
   int u, tile, rb, k0, len;
   int s = 0, issued = 0;             // ring stage, stages filled
   uint32_t phase = 0;
@@ -256,17 +254,12 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
     n = min(p.size, p.g.nc - p0);
     nhalf = 8 * cdiv(n, 16);
   };
-  // first output column of a unit, and how many of its accumulators lie within the matrix
-  const auto unit_col = [&](int rb) { return rb * (2 * kRows * Cfg::kAcc); };
-  const auto accs_of = [&](int rb) { return Cfg::kAcc == 2 && rb < p.RB ? 2 : 1; };
   if (warp == 0) {
     const uint32_t bar0 = map_rank(&full[0], 0);
     while (ok && work.next(u, tile, rb, k0, len)) {
       int p0, n, nhalf;
       tile_at(tile, p0, n, nhalf);
-      const int accs = accs_of(rb);
-      const uint32_t bytes = 2u * (accs * Cfg::kBytesR + Cfg::kBytesB);
-      const int r0 = unit_col(rb) + (int)rank * kRows, c0 = p0 + (int)rank * nhalf;
+      const int r = (2 * rb + (int)rank) * kRows, c0 = p0 + (int)rank * nhalf;
       for (int x = k0 * kFtK; x < (k0 + len) * kFtK; x += kFtK, ++issued) {
         if (!mbar_wait_warp(&empty[s], phase ^ 1, err)) {
           ok = false;
@@ -274,24 +267,21 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         }
         if (lane == 0) {
           const uint32_t bar = bar0 + 8 * s;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Cfg::kStage);
           uint8_t* a = st + s * Cfg::kStage;
-          uint8_t* b = a + Cfg::kBytesA;
-          for (int c = 0; c < accs; ++c, a += Cfg::kBytesR) {
-            const int r = r0 + c * 2 * kRows;
-            if constexpr (EPI == kFfGlu) {
-              if (p.whole16) {
-                tma2_load_4d(a, &p.tm_r, x, 0, 0, r >> 4, bar);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tma2_load_3d(a + j * 4096, &p.tm_r, x, r + 16 * j, 0, bar);
-              }
-            } else if (p.r_mn) {
-              tma2_load_2d(a, &p.tm_r, r, x, bar);
-              tma2_load_2d(a + 8192, &p.tm_r, r + 64, x, bar);
+          uint8_t* b = a + Cfg::kBytesR;
+          if constexpr (EPI == kFfGlu) {
+            if (p.whole16) {
+              tma2_load_4d(a, &p.tm_r, x, 0, 0, r >> 4, bar);
             } else {
-              tma2_load_2d(a, &p.tm_r, x, r, bar);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) tma2_load_3d(a + j * 4096, &p.tm_r, x, r + 16 * j, 0, bar);
             }
+          } else if (p.r_mn) {
+            tma2_load_2d(a, &p.tm_r, r, x, bar);
+            tma2_load_2d(a + 8192, &p.tm_r, r + 64, x, bar);
+          } else {
+            tma2_load_2d(a, &p.tm_r, x, r, bar);
           }
           if (Cfg::kHalf >= 64 && p.c_mn) {
 #pragma unroll
@@ -317,8 +307,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
     const uint64_t dc = p.c_mn ? smem_desc(st, 8192, 1024, 2) : desc_sw128(st);
     const uint32_t hir = (uint32_t)(dr >> 32), lor = (uint32_t)dr, hic = (uint32_t)(dc >> 32), loc = (uint32_t)dc;
     const uint32_t stepr = p.r_mn ? 2048 >> 4 : 32 >> 4, stepc = p.c_mn ? 2048 >> 4 : 32 >> 4;
-    uint32_t uses[2] = {0, 0};       // units that each accumulator buffer has held
-    int seg = 0;
+    uint32_t seg = 0;                // units so far
     bool ready = false;              // the next step's operands are known to be there
     // nothing commits to this phase before the first unit's MMAs
     if (p.d.probe_ns != 0 && blockIdx.x == 0)
@@ -326,10 +315,8 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
     while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
       int p0, n, nhalf;
       tile_at(tile, p0, n, nhalf);
-      const int accs = accs_of(rb);
-      const int b0 = Cfg::kAcc == 2 ? 0 : seg & 1;
-      for (int c = 0; ok && c < accs; ++c)
-        ok = mbar_wait_warp(&tempty[b0 + c], (uses[b0 + c] & 1) ^ 1, err);
+      const int b = seg & 1;           // the buffer's turns: seg / 2
+      ok = mbar_wait_warp(&tempty[b], ((seg >> 1) & 1) ^ 1, err);
       if (!ok) break;
       tc_fence_after();
       const uint32_t idesc = idesc_pair16(p.bf16, 2 * nhalf) | (p.r_mn ? 1u << 15 : 0u) | (p.c_mn ? 1u << 16 : 0u);
@@ -345,15 +332,10 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         if (elect_one()) {
           const uint32_t at = s * (Cfg::kStage >> 4);
 #pragma unroll
-          for (int c = 0; c < Cfg::kAcc; ++c) {
-            if (c < accs) {
-#pragma unroll
-              for (int kb = 0; kb < 4; ++kb) {
-                const uint64_t da = ((uint64_t)hir << 32) | (lor + at + c * (Cfg::kBytesR >> 4) + kb * stepr);
-                const uint64_t db = ((uint64_t)hic << 32) | (loc + at + (Cfg::kBytesA >> 4) + kb * stepc);
-                mma2_f16(tmem + (b0 + c) * BN, da, db, idesc, kb == 0 ? accumulate : 1u);
-              }
-            }
+          for (int kb = 0; kb < 4; ++kb) {
+            const uint64_t da = ((uint64_t)hir << 32) | (lor + at + kb * stepr);
+            const uint64_t db = ((uint64_t)hic << 32) | (loc + at + (Cfg::kBytesR >> 4) + kb * stepc);
+            mma2_f16(tmem + b * BN, da, db, idesc, kb == 0 ? accumulate : 1u);
           }
           tc2_commit(&empty[s]);
         }
@@ -361,10 +343,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         advance();
         ready = __all_sync(0xffffffffu, next);
       }
-      for (int c = 0; c < accs; ++c) {
-        if (elect_one()) tc2_commit(&tfull[b0 + c]);
-        ++uses[b0 + c];
-      }
+      if (elect_one()) tc2_commit(&tfull[b]);
       ++seg;
     }
   } else if (warp >= 4) {
@@ -375,11 +354,10 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
     uint32_t uses = 0;
     const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
     for (int seg = 0; ok && work.next(u, tile, rb, k0, len); ++seg) {
-      if (Cfg::kAcc == 2 ? g >= accs_of(rb) : (seg & 1) != g) continue;
+      if ((seg & 1) != g) continue;
       int p0, n, nhalf;
       tile_at(tile, p0, n, nhalf);
-      const int acc = Cfg::kAcc == 2 ? g : 0;
-      const int col0 = unit_col(rb) + acc * 2 * kRows + (int)rank * kRows;
+      const int col0 = (2 * rb + (int)rank) * kRows;
       ok = mbar_wait_warp(&tfull[g], uses & 1, err);
       ++uses;
       float v[32];
@@ -401,9 +379,9 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         ok = s_ok[4 * g] && s_ok[4 * g + 1] && s_ok[4 * g + 2] && s_ok[4 * g + 3];
         if (!ok) break;
         tc_fence_after();
-        const size_t stride = (size_t)2 * Cfg::kAcc * BN * 128;     // floats of one slot
+        const size_t stride = (size_t)2 * BN * 128;      // floats of one slot
         // four columns of a lane are adjacent: 16-byte accesses
-        const size_t at = (size_t)(rank * Cfg::kAcc + acc) * BN * 128 + (q * 32 + lane) * 4;
+        const size_t at = (size_t)rank * BN * 128 + (q * 32 + lane) * 4;
         float* mine = p.part + (size_t)work.slot_of(pair, u) * stride + at;
 #pragma unroll 1
         for (int c0 = 0; c0 < n; c0 += 32) {
@@ -421,7 +399,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         work.owners(u, c_lo, c_hi);
         if (q == 0 && lane == 0) {
           __threadfence();                              // the group's sums, ordered by its barrier
-          int32_t* ticket = p.tickets + 4 * (u - work.first) + 2 * rank + acc;
+          int32_t* ticket = p.tickets + 2 * (u - work.first) + rank;
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                        // ready for the next call
           __threadfence();
@@ -525,8 +503,8 @@ static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
   return best;
 }
 
-// Scratch of cut units: [pairs][2][2 CTAs][accumulators][BN][128] fp32 of the widest tile.
-size_t ff_tc_part_bytes() { return (size_t)kGtMaxPairs * 2 * 2 * 2 * 256 * 128 * sizeof(float); }
+// Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of the widest tile.
+size_t ff_tc_part_bytes() { return (size_t)kGtMaxPairs * 2 * 2 * 256 * 128 * sizeof(float); }
 
 static bool ft_tmap(CUtensorMap* tm, bool bf16, int rank, const void* base, const cuuint64_t* dims,
                     const cuuint64_t* strides, const cuuint32_t* box) {
@@ -539,10 +517,10 @@ static bool ft_tmap(CUtensorMap* tm, bool bf16, int rank, const void* base, cons
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, int BN, int ACC = 1>
+template <int EPI, int BN>
 static cudaError_t launch_ft(FtParams& p, cudaStream_t st) {
-  using Cfg = FtCfg<BN, ACC>;
-  auto kernel = ff_tc_kernel<EPI, BN, ACC>;
+  using Cfg = FtCfg<BN>;
+  auto kernel = ff_tc_kernel<EPI, BN>;
   static PerDevice<int> per;
   int pairs = 0;
   cudaError_t err = on_device(per, &pairs, [&](int* v) {
@@ -584,13 +562,11 @@ static cudaError_t launch_ft(FtParams& p, cudaStream_t st) {
   const cuuint32_t cbox[2] = {64, p.c_mn ? (cuuint32_t)kFtK : (cuuint32_t)Cfg::kHalf};
   ok = ok && ft_tmap(&p.tm_c, p.bf16, 2, g.c, cdims, &crow, cbox);
   if (!ok) return cudaErrorInvalidValue;
-  const int blocks = cdiv(g.nr, EPI == kFfGlu ? 128 : 256);
-  p.RB = blocks / Cfg::kAcc;
-  p.half = blocks % Cfg::kAcc;
+  p.RB = cdiv(g.nr, EPI == kFfGlu ? 128 : 256);
   p.tiles = cdiv(g.nc, BN);
   p.size = p.tiles > 1 ? 16 * cdiv(cdiv(g.nc, p.tiles), 16) : BN;
   // no more pairs than K steps can keep busy
-  const long long units = (long long)p.tiles * (p.RB + p.half);
+  const long long units = (long long)p.tiles * p.RB;
   const long long useful = units * (p.KT < kGtMinSteps ? 1 : cdiv(p.KT, kGtMinSteps));
   const int G = useful < pairs ? (int)useful : pairs;
   return launch_kernel(kernel, dim3(2 * G), dim3(kFtThreads), Cfg::kSmem, st, true, p);

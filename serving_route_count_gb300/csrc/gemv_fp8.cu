@@ -58,10 +58,11 @@ __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p
       set_error(c.err, kErrRouteBounds);
       return;                            // every thread of the call
     }
-    if (e >= p.d.E || c.offsets[e] > p0) {       // past the last group, or before the first
+    if (e >= p.d.E) {                    // past the last group
       if (lane == 0 && part == 0 && col < p.cols) out[p0 * c.ldo + col] = from_f32<T>(0.f);
       return;                            // every thread of the CTA
     }
+    if (c.offsets[e] > p0) return;       // before the first
   }
   long long row[NC];
 #pragma unroll
