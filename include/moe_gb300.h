@@ -544,9 +544,9 @@ moe_status moe_fp8_scratch_bytes(const moe_fp8_t* plan, size_t* bytes);
  *   x [x_rows, K] codes, row stride ldx, x_scale [x_rows, KB], row stride ldxs;  w [E, N, K] codes with
  *   row stride ldw and expert stride ldw * N, w_scale [E, tile rows, KB] contiguous;  out [S, N or
  *   N / 2], row stride ldo.  out must not overlap an input.
- * Rows whose x, w and strides are 16-byte aligned run on the tensor cores (a few positions, up to four of
- * one matrix or eight over experts, on the CUDA cores as fast as the weights can be read); other operands
- * (for instance K % 16 != 0) on the CUDA cores, slower.
+ * Rows whose x, w and strides are 16-byte aligned run on the tensor cores (a few positions, two of one
+ * matrix, four where K >= 4096, or eight over experts, on the CUDA cores, which then read the weights
+ * faster); other operands (for instance K % 16 != 0) on the CUDA cores, slower.
  * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (S > max_rows), MOE_ERR_CUDA. */
 moe_status moe_fp8_run(const moe_fp8_t* plan, void* scratch, size_t scratch_bytes, const uint8_t* x,
                        long long ldx, int x_rows, const float* x_scale, long long ldxs, const uint8_t* w,
@@ -579,8 +579,8 @@ moe_status moe_ff_scratch_bytes(const moe_ff_t* plan, size_t* bytes);
  *            w13's order and h: what moe_ff_backward needs.  pre is not rounded: the backward pass clamps
  *            what the forward pass clamped, and du and dg are rounded once.
  * y, pre and h must not overlap an input or one another.
- * Products whose operands and strides are 16-byte aligned run on the tensor cores (up to four tokens on the
- * CUDA cores, as fast as the weights can be read); others (for instance H % 8 != 0) on the CUDA cores,
+ * Products whose operands and strides are 16-byte aligned run on the tensor cores (one or two tokens on the
+ * CUDA cores, which then read the weights faster); others (for instance H % 8 != 0) on the CUDA cores,
  * slower.  Results of a plan's calls do not depend on the stream or the call before; a token's may differ
  * in the last place with the number of tokens in its call.
  * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (M > max_rows), MOE_ERR_CUDA. */

@@ -17,6 +17,18 @@
 //     The 128 sums of a thread and what is in flight need 208 registers: the other warps give theirs
 //     up (setmaxnreg).
 //
+// Bounds and measurements (GB300, HBM at the measured 6784 GB/s, e4m3 at twice the measured bf16 rate):
+//   up projections + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 67 us, HBM floor 53; down projections
+//   of 16 tokens top-6, E = 384, K = 576, N = 7168: 83 us, floor 52 - the start (tables 2 us, first loads 2.5),
+//   units of five steps, their stores (76 us without) and 128-byte copies of 576-byte rows;
+//   2048 tokens top-8, skewed: 392 us, floor 241: bound by the epilogue's handling of a step at 128 tokens (272
+//   with the MMAs and copies alone);
+//   8192 x 7168 x 7168: 453 us, 1.86 PFLOP/s (floor 220; 277 with the MMAs and copies alone, 342 with the loads
+//   from tensor memory, the rest the FMAs that do not hide under them).
+// What cost most on the way, us of up decode / dense prefill: an arrival with cluster-scope release after the
+// tensor-memory loads waited for the scales' global loads, 145 / 883; its CTA-scope form 91 / 575; scales
+// from warps of their own and 64 columns in flight 78 / 443.
+//
 // Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-5 or 2-6 token copies (tiles, or
 // gathers of four rows by index; warp 3 also allocates the tensor memory, warp 2 asks for the next
 // unit's weight scales), the others up to warp 7 scales, warps 8-15 epilogue.
@@ -68,8 +80,6 @@ struct F8Cfg {
   static constexpr int kStages = (227 * 1024 - 1024 - kTables) / kStage > 12
                                      ? 12 : (227 * 1024 - 1024 - kTables) / kStage;
   static constexpr int kSmem = 1024 + kStages * kStage + kTables;
-  // K steps that joining the pieces of a unit costs (as for the 16-bit products)
-  static constexpr int kFixSteps = BN <= 32 ? 8 : (BN <= 64 ? 12 : (BN <= 128 ? 24 : 40));
 };
 
 struct F8Params {
@@ -82,6 +92,7 @@ struct F8Params {
   float* part;          // [pairs][2][2 CTAs][BN][128]
   int32_t* tickets;     // [pairs][2 CTAs][2 groups]
   int KT, RB, cols, tall;
+  int fix_steps;        // K steps that cutting the leftover units has to save (GtWork)
   int packed, vec;      // output rows on 4 bytes, on 16
   int whole16;          // SwiGLU weights by whole 16-row groups: one 5-d copy per K step
 };
@@ -206,7 +217,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
   // Every loop below is taken by whole warps; one lane issues.
   constexpr int kRows = ACT ? 64 : 128;      // output columns of one CTA's weight rows
   GtWork work;
-  work.init(total, p.KT, p.RB, 0, G, pair, Cfg::kFixSteps, false);
+  work.init(total, p.KT, p.RB, 0, G, pair, p.fix_steps, false);
   int u, tile, rb, k0, len;
   int s = 0, issued = 0;             // ring stage, stages filled
   uint32_t phase = 0;
@@ -543,7 +554,7 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
       const int n = h[kF8N];
       if (h[kF8Piece]) {
         GtWork w;
-        w.init(*s_total, p.KT, p.RB, 0, gridDim.x >> 1, blockIdx.x >> 1, Cfg::kFixSteps, false);
+        w.init(*s_total, p.KT, p.RB, 0, gridDim.x >> 1, blockIdx.x >> 1, p.fix_steps, false);
         const int unit = h[kF8Unit];
         const size_t stride = (size_t)2 * BN * 128;      // floats of one slot of the scratch buffer
         const size_t mine = ((size_t)rank * BN + g * CW) * 128 + t;
@@ -727,18 +738,55 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
 
 // ---------------------------------------------------------------------------------- host side
 
-// Token-tile width by the mean positions per expert, as for the 16-bit products; of one matrix, whose rows
-// are known, the narrowest that holds them.
-static int fp8_tc_bn(int S, int E) {
-  const bool dense = E == 1;
-  if ((long long)S * (dense ? 1 : 4) <= 32LL * E) return 32;
-  if (dense ? S <= 64 : (long long)S <= 24LL * E) return 64;
-  if (dense ? S <= 128 : (long long)S <= 64LL * E) return 128;
-  return 256;
+// Token-tile width, and whether the units that whole waves leave over are cut along K.
+// Over experts, whose rows are known on the device only, by the mean positions per expert (of S, dropped
+// slots among them): an expert should be one tile while HBM is the bound, and up to 64 tokens a step's
+// epilogue stays under its loads.  E = 256, K = 6144, N = 1024, SwiGLU, gathered, us at widths 32 / 64 /
+// 128 / 256: mean 16: 254 / 253 / 349 / 421;  24: 248 / 258 / 352 / 429;  32: 302 / 262 / 359 / 435;  48:
+// 395 / 270 / 368 / 443;  64: 504 / 389 / 373 / 450;  96: 690 / 496 / 387 / 460;  128: 890 / 625 / 576 / 472.
+// The kernel then cuts where that saves more K steps than joining costs.
+// Of one matrix the least of the estimated times: a unit's K step, and joining its pieces by rows and pieces.
+// K = 7168, N = 4096, us at the same widths: 32 rows 27 / 30 / 32 / 38;  128: 31 / 29 / 35 / 39;  200: 41 / 26 /
+// 36 / 39;  300: 56 / 57 (cut) / 34 / 40;  1000: 123 / 87 / 63 / 43.
+struct F8Plan {
+  int bn, fix_steps;
+};
+static F8Plan fp8_tc_plan(int S, int E, int KT, int RB, int pairs) {
+  if (E > 1) {
+    const long long e = E;
+    if (S <= 24 * e) return {32, 8};
+    if (S <= 56 * e) return {64, 12};
+    return S <= 104 * e ? F8Plan{128, 24} : F8Plan{256, 40};
+  }
+  F8Plan best{256, 0x7FFFFFFF};
+  double least = 1e300;
+  for (int bn = 32; bn <= 256; bn *= 2) {
+    const int tiles = cdiv(S, bn);
+    const double step = bn == 32 ? 320 : (bn == 64 ? 385 : (bn == 128 ? 560 : 740));     // ns
+    const long long units = (long long)tiles * RB, waves = units / pairs, left = units % pairs;
+    const double base = (double)waves * KT * step;
+    const double whole = base + (left ? KT * step : 0);
+    if (whole <= least) {
+      least = whole;
+      best = {bn, 0x7FFFFFFF};
+    }
+    if (left) {
+      const double pieces = (double)pairs / left + 1, rows = cdiv(S, tiles);
+      const double cut = base + (double)left * KT / pairs * step + 1000 + rows * (150 + 8.6 * pieces);
+      if (cut < least) {
+        least = cut;
+        best = {bn, 0};
+      }
+    }
+    if (bn >= S) break;                // one tile holds them all
+  }
+  return best;
 }
 
+// Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of the widest tile that calls of up to S positions may get.
 size_t fp8_tc_part_bytes(int S, int E) {
-  return (size_t)kGtMaxPairs * 2 * 2 * fp8_tc_bn(S, E) * 128 * sizeof(float);
+  const int bn = E > 1 ? fp8_tc_plan(S, E, 1, 1, 1).bn : (S <= 32 ? 32 : (S <= 64 ? 64 : (S <= 128 ? 128 : 256)));
+  return (size_t)kGtMaxPairs * 2 * 2 * bn * 128 * sizeof(float);
 }
 
 static bool f8_tmap(CUtensorMap* tm, int rank, const void* base, const cuuint64_t* dims,
@@ -805,7 +853,6 @@ static cudaError_t launch_f8(F8Params& p, cudaStream_t st) {
   const cuuint32_t xbox[2] = {kF8K, c.perm ? 1u : (cuuint32_t)Cfg::kChunk};
   ok = ok && f8_tmap(&p.tm_x, 2, c.x, xdims, xstr, xbox);
   if (!ok) return cudaErrorInvalidValue;
-  p.RB = cdiv(p.cols, ACT ? 128 : 256);
   // no more pairs than K steps can keep busy
   const long long units = ((long long)cdiv(c.S, BN) + (d.E < c.S ? d.E : c.S)) * p.RB;
   const long long useful = units * (p.KT < kGtMinSteps ? 1 : cdiv(p.KT, kGtMinSteps));
@@ -815,7 +862,20 @@ static cudaError_t launch_f8(F8Params& p, cudaStream_t st) {
 
 template <typename T, bool ACT>
 static cudaError_t launch_f8_bn(F8Params& p, cudaStream_t st) {
-  switch (fp8_tc_bn(p.c.S, p.d.E)) {
+  static PerDevice<int> per;           // CTA pairs of the device
+  int pairs = 0;
+  const cudaError_t e = on_device(per, &pairs, [](int* v) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    *v = std::max(1, sms / 2);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
+  p.RB = cdiv(p.cols, ACT ? 128 : 256);
+  const F8Plan plan = fp8_tc_plan(p.c.S, p.d.E, p.KT, p.RB, pairs);
+  p.fix_steps = plan.fix_steps;
+  switch (plan.bn) {
     case 32: return launch_f8<T, ACT, 32>(p, st);
     case 64: return launch_f8<T, ACT, 64>(p, st);
     case 128: return launch_f8<T, ACT, 128>(p, st);

@@ -1,11 +1,13 @@
-// gemv_ff.cu - products of the gated feed-forward block's forward pass for a few tokens (up to four):
+// gemv_ff.cu - products of the gated feed-forward block's forward pass for one or two tokens:
 // out[c][r] = act(sum_k R(r, k) C(c, k)), both operands along K.
 //
 // Bound by reading the weights once.  One to eight warps to an output row (GLU: to a pair of rows, up and
 // gate), as many as fill the GPU; a lane takes 16 bytes of every row at a time, four of them in flight, and
 // multiplies in fp32 on the CUDA cores, which at so few tokens keep up with HBM.  Sums go lane by lane, then
-// over the lanes, then over the warps: one order.  Units on the tensor cores are too large for this: one
-// token of 7168 -> 1152 -> 7168 took 24 us there, pieces of units and their joining among it.
+// over the lanes, then over the warps: one order.  Units on the tensor cores are cut into pieces for this,
+// which are joined: us of a forward pass here / there, weights in L2: 6144 -> 512 one token 7.3 / 20.0, two
+// 9.3 / 17.8, four (were they taken) 16.4 / 17.8;  7168 -> 1152 11.9 / 21.2, 16.6 / 21.3, 31.7 / 21.3;  4096 -> 4096
+// 21.5 / 28.5, 27.0 / 29.5, 50.5 / 28.8.  From HBM one token of 7168 -> 1152 takes 15.2 us (weights 7.3).
 #include "feed_forward.cuh"
 #include "../../include/moe_gb300.h"
 
@@ -100,9 +102,9 @@ __global__ void __launch_bounds__(kFvThreads) ff_gemv_kernel(const FvParams p) {
   }
 }
 
-// A few tokens, both operands along K in whole vectors (their alignment as for the tensor cores).
+// One or two tokens, both operands along K in whole vectors (their alignment as for the tensor cores).
 bool ff_gemv_takes(const FfGemm& g, int epilogue) {
-  return g.nc <= 4 && g.rk == 1 && g.ck == 1 && g.K % 8 == 0 && epilogue != kFfGrad;
+  return g.nc <= 2 && g.rk == 1 && g.ck == 1 && g.K % 8 == 0 && epilogue != kFfGrad;
 }
 
 template <typename T, int EPI>
@@ -112,8 +114,7 @@ static cudaError_t launch_fv(FvParams& p, cudaStream_t st) {
   while (p.warps < kFvWarps && p.g.nr * p.warps < 152 * 16 && p.g.K > p.warps * 256) p.warps *= 2;
   const dim3 grid(cdiv(p.g.nr, kFvWarps / p.warps));
   const auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kFvThreads), 0, st, true, p); };
-  if (p.g.nc == 1) return go(ff_gemv_kernel<T, EPI, 1>);
-  return p.g.nc == 2 ? go(ff_gemv_kernel<T, EPI, 2>) : go(ff_gemv_kernel<T, EPI, 4>);
+  return p.g.nc == 1 ? go(ff_gemv_kernel<T, EPI, 1>) : go(ff_gemv_kernel<T, EPI, 2>);
 }
 
 // early: the launch before this one in the stream is the block's own first product, which does not write these

@@ -1,5 +1,5 @@
-// gemv_fp8.cu - 8-bit products with block scales for a few positions: up to four of one matrix, or up to
-// eight over experts (one token's).
+// gemv_fp8.cu - 8-bit products with block scales for a few positions: two of one matrix, four where K is
+// long, or eight over experts (one token's).
 //
 // Bound by reading the weights once.  One to eight warps to an output column (SwiGLU: to a pair of weight
 // rows), as many as fill the GPU; a lane takes 16 codes of every row at a time, all of one block, sums
@@ -142,9 +142,12 @@ __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p
   out[(long long)(p0 + lane) * c.ldo + col] = from_f32<T>(y);
 }
 
-// A few positions in whole vectors (their alignment as for the tensor cores).
+// A few positions in whole vectors (their alignment as for the tensor cores).  Of one matrix, us here / on the
+// tensor cores: K = 7168, N = 2304 SwiGLU 1: 7.3 / 20.7;  2: 9.2 / 20.7;  4: 14.1 / 22.6;  8: 23 / 24;  K = 1152,
+// N = 7168 1: 6.7 / 9.1;  2: 8.7 / 9.0;  4: 13.2 / 9.3 (a long K is cut into pieces there, which are joined).  Over
+// experts (E = 256, K = 6144, N = 1024) 8: 17.8 / 22.3;  16: 33.9 / 26.6.
 bool fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f) {
-  return f.c.S <= (d.E == 1 ? 4 : 8) && d.K % 16 == 0;
+  return f.c.S <= (d.E > 1 ? 8 : (d.K >= 4096 ? 4 : 2)) && d.K % 16 == 0;
 }
 
 template <typename T, bool ACT>
