@@ -11,12 +11,13 @@
 // 64 rows along K x 64 elements, which land in shared memory as the MMA's 128-byte-swizzled MN-major
 // form, and the instruction descriptor says so.
 //
-// Bounds and measurements (GB300, bf16, measured 1910 TFLOP/s in a burst, 1726 sustained): 4096 tokens of 7168 ->
-// 4608 -> 7168, us alone and TFLOP/s: up projections with the saved sums 350 / 1546, without 240 at 6144 -> 4096
-// (1718); down 147 / 1841; dh with the activation's gradient 190 / 1424; dx 296 / 1828; dW13 317 / 1707; dW2 158 /
-// 1713: bound by the tensor cores and their power, the first and the third by their epilogues' accesses too.  The
-// whole step 1543 us (1578 TFLOP/s, 91 % of sustained).  777 tokens of 6144 -> 512 -> 6144: 114 us, floor 23: sixteen
-// to fifty units for 76 pairs, and a unit's 96 steps take 23 us.
+// Bounds and measurements (GB300, bf16, measured 1910 TFLOP/s in a burst, 1726 sustained): 2048 tokens of 7168 ->
+// 4608 -> 7168, us of each product alone and TFLOP/s (floor 142 for the two-halves ones, 71 for the others): up
+// projections with the saved sums 158 / 1712; down 76 / 1780; dh with the activation's gradient 106 / 1276; dx
+// 148 / 1828; dW13 161 / 1681; dW2 86 / 1573: bound by the tensor cores (pipe 80 to 85 % active; dW 67 to 72, dh
+// 54, whose epilogue reads two fp32 sums for every value).  The whole step of 4096 tokens 1520 us (1602 TFLOP/s,
+// 93 % of sustained).  777 tokens of 6144 -> 512 -> 6144: 91 us with the weights in L2, 118 from HBM, floor 23:
+// sixteen to fifty units for 76 pairs, and a unit's 96 steps take 23 us.
 //
 // Roles: warp 0 tile copies, warp 1 MMA issue (leader CTA), warp 2 tensor memory, warps 4-11 epilogue.
 #include "feed_forward.cuh"
@@ -47,7 +48,7 @@ struct FtParams {
   FfDims d;
   FfGemm g;
   float* part;          // [pairs][2][2 CTAs][BN / 4][128][4]
-  int32_t* tickets;     // [pairs][2 CTAs]
+  int32_t* tickets;     // [pairs][2 CTAs][2 groups]
   int KT, RB;           // K steps; row blocks
   int tiles, size;      // tiles of C, rows of a tile (the last may have fewer)
   int cut;              // whether the units left over are cut along K
@@ -229,7 +230,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);        // four epilogue warps of each CTA
+      mbar_init(&tempty[b], 16);       // eight epilogue warps of each CTA
     }
     fence_barrier_init();
   }
@@ -354,31 +355,35 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
       ++seg;
     }
   } else if (warp >= 4) {
-    // two groups of four warps, one per accumulator buffer
+    // Two groups of four warps take every other 32 columns of each unit, so that the last unit's epilogue, which
+    // nothing covers, and joining take half as long as with a unit to a group (us: 6144 -> 512, 200 tokens cut at
+    // 256 72 -> 54, 100 at 128 47 -> 35; the training step of 4096 tokens 1543 -> 1520).
     const int q = warp & 3, g = (warp - 4) >> 2;
-    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + g * BN;
-    const uint32_t bempty = map_rank(&tempty[g], 0);
-    uint32_t uses = 0;
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t bempty = map_rank(&tempty[0], 0);
     const auto sync_group = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
-    for (int seg = 0; ok && work.next(u, tile, rb, k0, len); ++seg) {
-      if ((seg & 1) != g) continue;
+    for (uint32_t seg = 0; ok && work.next(u, tile, rb, k0, len); ++seg) {
       int p0, n, nhalf;
       tile_at(tile, p0, n, nhalf);
       const int col0 = (2 * rb + (int)rank) * kRows;
-      ok = mbar_wait_warp(&tfull[g], uses & 1, err);
-      ++uses;
+      const uint32_t buf = seg & 1, tbuf = trow + buf * BN;
+      const auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_read(bempty + 8 * buf);
+      };
+      ok = mbar_wait_warp(&tfull[buf], (seg >> 1) & 1, err);
       float v[32];
       if (len == p.KT) {               // no named barrier from here on: pieces come first
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += 32) {
-          tmem_ld32(trow + c0, v);
+        for (int c0 = 32 * g; c0 < n; c0 += 64) {
+          tmem_ld32(tbuf + c0, v);
+          if (c0 + 64 >= n) release();
           ft_store<EPI>(p, v, p0, n, col0, c0, q, lane);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(bempty);
+        if (32 * g >= n) release();
       } else {
         // one verdict for the four warps: all of them reach the named barriers below, or none
         if (lane == 0) s_ok[4 * g + q] = ok;
@@ -386,27 +391,30 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
         ok = s_ok[4 * g] && s_ok[4 * g + 1] && s_ok[4 * g + 2] && s_ok[4 * g + 3];
         if (!ok) break;
         tc_fence_after();
+        if (32 * g >= n) {             // no columns of this group
+          release();
+          sync_group();                                 // s_ok read by all
+          continue;
+        }
         const size_t stride = (size_t)2 * BN * 128;      // floats of one slot
         // four columns of a lane are adjacent: 16-byte accesses
         const size_t at = (size_t)rank * BN * 128 + (q * 32 + lane) * 4;
         float* mine = p.part + (size_t)work.slot_of(pair, u) * stride + at;
 #pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += 32) {
-          tmem_ld32(trow + c0, v);
+        for (int c0 = 32 * g; c0 < n; c0 += 64) {
+          tmem_ld32(tbuf + c0, v);
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             if (c0 + j < n)
               __stcg(reinterpret_cast<float4*>(mine + (size_t)(c0 + j) * 128), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(bempty);
+        release();
         sync_group();
         int c_lo, c_hi;
         work.owners(u, c_lo, c_hi);
         if (q == 0 && lane == 0) {
           __threadfence();                              // the group's sums, ordered by its barrier
-          int32_t* ticket = p.tickets + 2 * (u - work.first) + rank;
+          int32_t* ticket = p.tickets + 4 * (u - work.first) + 2 * rank + g;
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                        // ready for the next call
           __threadfence();
@@ -441,7 +449,7 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
             ft_store<EPI>(p, v, p0, n, col0, 0, q, lane);
           } else {
 #pragma unroll 1
-            for (int c0 = 0; c0 < n; c0 += 32) {
+            for (int c0 = 32 * g; c0 < n; c0 += 64) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.f;
               for (int c = c_lo; c <= c_hi; c += 2) {
@@ -474,10 +482,11 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
 
 // Tile width, and whether the units that whole waves leave over are cut along K: the least of the estimated
 // times.  A K step of a unit takes what its MMAs or its loads take, whichever is more; joining the pieces of a
-// unit takes time by its rows of C and its pieces, one group of warps adding them.  Estimates from
-// us of the up projection, forward, at widths 32 / 64 / 128 / 256, c cut, w whole: H = 6144, I = 512, M = 48
-// 24c / 31w / 34w / 33w, M = 777 - / 40w / 41w / 40w (cut 41 / 43 / 55); H = I = 4096, M = 200 78c / 54w / 45w /
-// 47w, M = 2048 - / 315c / 187c / 129w.
+// unit takes time by its rows of C and its pieces, two groups of warps adding them.  Estimates from
+// us of the up projection and the down projection, at widths 32 / 64 / 128 / 256, c cut, w whole: H = 6144, I =
+// 512, M = 48 27c / 24c / 24c / 25c (whole 30 to 33), M = 200 27c / 25c / 37c / 54c (35w / 33w / 34w / 36w), M = 777
+// - / 39c / 36c / 44c (40w / 40w / 40w);  H = 7168, I = 1152, M = 400 71c / 49c / 45c / 53c (80w / 47w / 46w / 44w);
+// H = I = 4096, M = 2048 - / 315w / 187w / 129w.
 // Sums over tokens have both operands the other way round, whose boxes are 64 wide for each CTA: 128 at
 // least.
 struct FtPlan {
@@ -495,7 +504,7 @@ static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
     double whole = base + (left ? KT * step : 0), cut = 1e300;
     if (left) {
       const double pieces = (double)pairs / left + 1, rows = cdiv(g.nc, tiles);
-      cut = base + (double)left * KT / pairs * step + 1000 + rows * (150 + 8.6 * pieces);
+      cut = base + (double)left * KT / pairs * step + 1000 + rows * (75 + 4.3 * pieces);
     }
     if (whole <= least) {
       least = whole;
