@@ -318,6 +318,58 @@ def test_gradients_by_differences(moe):
 
 
 @gpu
+def test_past_32_bits(moe):
+    """More than 2^31 values of x and y, and sums over as many tokens: two kinds of rows of x, so that the sums are known."""
+    M, H, I = 270_001, 8192, 8
+    assert M * H > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(6)
+    kinds = torch.randn((2, H), generator=g, device="cuda").bfloat16()
+    dkinds = torch.randn((2, H), generator=g, device="cuda").bfloat16()
+    which = torch.zeros(M, dtype=torch.int64, device="cuda")
+    which[-3:] = 1
+    x, dy = kinds[which], torch.where(which[:, None] == 1, dkinds[1], torch.zeros_like(dkinds[0]))      # gradients of the last rows alone
+    w13 = (torch.randn((2 * I, H), generator=g, device="cuda") * H ** -0.5).bfloat16()
+    w2 = (torch.randn((H, I), generator=g, device="cuda") * I ** -0.5).bfloat16()
+    op = moe.MoEFeedForward(H, I, max_rows=M)
+    y, saved = op.forward(x, w13, w2)
+    dx, dw13, dw2 = op.backward(dy, x, w13, w2, saved)
+    assert op.device_error() == (0, 0)
+    small = moe.MoEFeedForward(H, I, max_rows=8)
+    tail = slice(M - 8, M)
+    sub = [t[tail].contiguous() for t in (x, dy, *saved)]
+    # rows of the tail: the same sums in whatever tiles, to a few units in the last place of their 16-bit roundings
+    y8 = small(sub[0], w13, w2)
+    dx8, dw138, dw28 = small.backward(sub[1], sub[0], w13, w2, (sub[2], sub[3]))
+    for a, b in ((y[tail], y8), (dx[tail], dx8), (dw13, dw138), (dw2, dw28)):
+        assert float((a.double() - b.double()).norm() / b.double().norm()) < 2.0 ** -7
+    assert torch.count_nonzero(dx[:-3]) == 0 and torch.equal(y[0], y[M // 2])
+
+
+@gpu
+def test_two_at_once(moe):
+    """Two plans' passes on two streams."""
+    made = [operands(300, 1024, 520, "bf16", seed) for seed in (1, 2)]
+    ops = [moe.MoEFeedForward(1024, 520, max_rows=300) for _ in made]
+
+    def step(op, c):
+        y, saved = op.forward(*c[:3])
+        return (y, *op.backward(c[3], *c[:3], saved))
+
+    want = [step(op, c) for op, c in zip(ops, made)]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for op, c, st in zip(ops, made, streams):
+            with torch.cuda.stream(st):
+                got.append(step(op, c))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i % 2]))
+    assert all(op.device_error() == (0, 0) for op in ops)
+
+
+@gpu
 def test_some_gradients(moe):
     op, (x, w13, w2, dy), y, saved, grads = check(moe, 30, 128, 64, "bf16")
     for need in ((True, False, False), (False, True, False), (False, False, True), (True, False, True), (False, False, False)):

@@ -368,6 +368,50 @@ def test_product_past_32_bits(moe):
 
 
 @gpu
+def test_rows_past_32_bits(moe):
+    """Quantisation and products of more than 2^31 values of x; the last rows are theirs."""
+    rows, K, N = 300_003, 7200, 24
+    assert rows * K > 1 << 31
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(4))
+    q, s = moe.moe_fp8_quant(x)
+    last = [0, 1, rows // 2, rows - 2, rows - 1]
+    wq, ws = F.quant_rows(x[last].float().cpu().numpy())
+    assert np.array_equal(codes(q.view(torch.uint8)[last]), wq) and np.array_equal(s[last].cpu().numpy(), ws)
+    w, wscale = moe.moe_fp8_quant(torch.randn((N, K), device="cuda"), form=moe.MOE_FP8_TILES)
+    op = moe.MoEFp8(1, N, K, max_rows=rows)
+    got = op(q, s, w, wscale)
+    assert op.device_error() == (0, 0)
+    xv, wv = F.values(wq, ws), F.weight_values(codes(w)[None], wscale.cpu().numpy()[None], False)[0]
+    ref, err = xv @ wv.T, (K + 3) * EPS32 * (np.abs(xv) @ np.abs(wv).T)
+    assert np.all(np.abs(f64(got[last]) - ref) <= 2.0 ** -8 * (np.abs(ref) + err) + err)
+
+
+@gpu
+def test_two_at_once(moe):
+    """Two plans' calls on two streams, and quantisation between them: nobody waits for another kernel."""
+    made = [case(4, 512, 1040, [40, 300, 0, 7], True, 1, True, seed) for seed in (1, 2)]
+    ops = [moe.MoEFp8(4, 512, 1040, max_rows=347, act=moe.MOE_ACT_SWIGLU) for _ in made]
+    want = [op(*c[:5], perm=c[5]) for op, c in zip(ops, made)]
+    h = torch.randn((5000, 7168), device="cuda").bfloat16()
+    q, s = moe.moe_fp8_quant(h)
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for op, c, st in zip(ops, made, streams):
+            with torch.cuda.stream(st):
+                got.append(op(*c[:5], perm=c[5]))
+                got.append(moe.moe_fp8_quant(h))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        if i % 2:
+            assert torch.equal(g[0].view(torch.uint8), q.view(torch.uint8)) and torch.equal(g[1], s)
+        else:
+            assert torch.equal(g, want[i // 2 % 2])
+    assert all(op.device_error() == (0, 0) for op in ops)
+
+
+@gpu
 def test_product_repeats_streams_and_graphs(moe):
     """One plan over calls of other sizes and offsets, on another stream, and replayed in a graph: every call
     gives the same bits again."""
