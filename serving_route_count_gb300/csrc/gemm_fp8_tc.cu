@@ -89,7 +89,7 @@ struct F8Params {
   const float* xs;
   const float* ws;
   long long ldxs;
-  float* part;          // [pairs][2][2 CTAs][BN][128]
+  float* part;          // [pairs][2][2 CTAs][BN / 4][128][4]
   int32_t* tickets;     // [pairs][2 CTAs][2 groups]
   int KT, RB, cols, tall;
   int fix_steps;        // K steps that cutting the leftover units has to save (GtWork)
@@ -556,15 +556,15 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
         GtWork w;
         w.init(*s_total, p.KT, p.RB, 0, gridDim.x >> 1, blockIdx.x >> 1, p.fix_steps, false);
         const int unit = h[kF8Unit];
-        const size_t stride = (size_t)2 * BN * 128;      // floats of one slot of the scratch buffer
-        const size_t mine = ((size_t)rank * BN + g * CW) * 128 + t;
-        float* out = p.part + (size_t)w.slot_of(blockIdx.x >> 1, unit) * stride + mine;
+        // four columns of a lane are adjacent: 16-byte accesses
+        const size_t stride = (size_t)2 * BN * 32;       // 16-byte words of one slot of the scratch buffer
+        float4* part = reinterpret_cast<float4*>(p.part) + ((size_t)rank * BN + g * CW) * 32 + t;
+        float4* mine = part + (size_t)w.slot_of(blockIdx.x >> 1, unit) * stride;
         const int m = Cfg::kTokenRows ? CW : n - g * CW;
 #pragma unroll
-        for (int c = 0; c < CW / 2; ++c) {
-          const float2 f = unpair_f32(acc[c]);
-          if (2 * c < m) __stcg(out + (size_t)(2 * c) * 128, f.x);
-          if (2 * c + 1 < m) __stcg(out + (size_t)(2 * c + 1) * 128, f.y);
+        for (int c = 0; c < CW / 4; ++c) {
+          const float2 lo = unpair_f32(acc[2 * c]), hi = unpair_f32(acc[2 * c + 1]);
+          if (4 * c < m) __stcg(mine + c * 128, make_float4(lo.x, lo.y, hi.x, hi.y));
         }
         if (!sync_group()) return false;
         int c_lo, c_hi;
@@ -575,22 +575,35 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
           const int last = atomicAdd(ticket, 1) == c_hi - c_lo;
           if (last) *ticket = 0;                         // ready for the next call
           __threadfence();
-          s_flag[g] = last;
+          s_flag[g] = last;                              // read by all before they meet again
         }
         if (!sync_group()) return false;
-        const bool last = s_flag[g];
-        if (!sync_group()) return false;                 // read by all
-        if (!last) return true;
+        if (!s_flag[g]) return true;
 #pragma unroll 1
         for (int b = 0; b < CW / 32; ++b) {
+          if (32 * b >= m) break;
           float x[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) x[c] = 0.f;
-          for (int o = c_lo; o <= c_hi; ++o) {
-            const float* src = p.part + (size_t)w.slot_of(o, unit) * stride + mine + (size_t)(32 * b) * 128;
+          for (int o = c_lo; o <= c_hi; o += 2) {        // two pieces in flight, added in K order
+            float4 y[2][8];
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (32 * b + c < m) x[c] += __ldcg(src + (size_t)c * 128);
+            for (int k = 0; k < 2; ++k) {
+              const float4* src = part + (size_t)w.slot_of(min(o + k, c_hi), unit) * stride + b * 8 * 128;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) y[k][c] = __ldcg(src + (32 * b + 4 * c < m ? c : 0) * 128);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const bool there = o + k <= c_hi;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                x[4 * c] += there ? y[k][c].x : 0.f;
+                x[4 * c + 1] += there ? y[k][c].y : 0.f;
+                x[4 * c + 2] += there ? y[k][c].z : 0.f;
+                x[4 * c + 3] += there ? y[k][c].w : 0.f;
+              }
+            }
           }
           store(h, b, x);
         }
@@ -783,7 +796,8 @@ static F8Plan fp8_tc_plan(int S, int E, int KT, int RB, int pairs) {
   return best;
 }
 
-// Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of the widest tile that calls of up to S positions may get.
+// Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of the widest tile that calls of up to S positions may
+// get.
 size_t fp8_tc_part_bytes(int S, int E) {
   const int bn = E > 1 ? fp8_tc_plan(S, E, 1, 1, 1).bn : (S <= 32 ? 32 : (S <= 64 ? 64 : (S <= 128 ? 128 : 256)));
   return (size_t)kGtMaxPairs * 2 * 2 * bn * 128 * sizeof(float);
