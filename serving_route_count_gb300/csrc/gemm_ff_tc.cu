@@ -504,7 +504,7 @@ static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
     double whole = base + (left ? KT * step : 0), cut = 1e300;
     if (left) {
       const double pieces = (double)pairs / left + 1, rows = cdiv(g.nc, tiles);
-      cut = base + (double)left * KT / pairs * step + 1000 + rows * (75 + 4.3 * pieces);
+      cut = base + (double)left * KT / pairs * step + 3500 + rows * (75 + 4.3 * pieces);
     }
     if (whole <= least) {
       least = whole;

@@ -759,8 +759,8 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
 // 395 / 270 / 368 / 443;  64: 504 / 389 / 373 / 450;  96: 690 / 496 / 387 / 460;  128: 890 / 625 / 576 / 472.
 // The kernel then cuts where that saves more K steps than joining costs.
 // Of one matrix the least of the estimated times: a unit's K step, and joining its pieces by rows and pieces.
-// K = 7168, N = 4096, us at the same widths: 32 rows 27 / 30 / 32 / 38;  128: 31 / 29 / 35 / 39;  200: 41 / 26 /
-// 36 / 39;  300: 56 / 57 (cut) / 34 / 40;  1000: 123 / 87 / 63 / 43.
+// K = 7168, N = 4096, us at the same widths: 32 rows 18 / 19 / 22 / 34;  128: 23 / 25 / 33 / 39;  200: 39 / 26 /
+// 33 / 40;  300: 54 / 46 / 34 / 40;  1000: 119 / 87 / 62 / 43.
 struct F8Plan {
   int bn, fix_steps;
 };
@@ -785,7 +785,7 @@ static F8Plan fp8_tc_plan(int S, int E, int KT, int RB, int pairs) {
     }
     if (left) {
       const double pieces = (double)pairs / left + 1, rows = cdiv(S, tiles);
-      const double cut = base + (double)left * KT / pairs * step + 1000 + rows * (150 + 8.6 * pieces);
+      const double cut = base + (double)left * KT / pairs * step + 4000 + rows * (100 + 6 * pieces);
       if (cut < least) {
         least = cut;
         best = {bn, 0};

@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p
 }
 
 // A few positions in whole vectors (their alignment as for the tensor cores).  Of one matrix, us here / on the
-// tensor cores: K = 7168, N = 2304 SwiGLU 1: 7.3 / 20.7;  2: 9.2 / 20.7;  4: 14.1 / 22.6;  8: 23 / 24;  K = 1152,
-// N = 7168 1: 6.7 / 9.1;  2: 8.7 / 9.0;  4: 13.2 / 9.3 (a long K is cut into pieces there, which are joined).  Over
-// experts (E = 256, K = 6144, N = 1024) 8: 17.8 / 22.3;  16: 33.9 / 26.6.
+// tensor cores: K = 7168, N = 2304 SwiGLU 1: 7.3 / 18.7;  2: 9.0 / 18.4;  4: 13.8 / 18.4;  8: 23 / 19;  K = 1152,
+// N = 7168 1: 6.8 / 9.1;  2: 8.4 / 9.0;  4: 13.1 / 9.3 (a long K is cut into pieces there, which are joined).  Over
+// experts (E = 256, K = 6144, N = 1024) 8: 18.5 / 21.9;  16: 34.4 / 26.1.
 bool fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f) {
   return f.c.S <= (d.E > 1 ? 8 : (d.K >= 4096 ? 4 : 2)) && d.K % 16 == 0;
 }
