@@ -14,8 +14,8 @@
 //   256: tokens are M and weight rows N.  A lane holds one token and 128 weight rows, all of one scale (two for
 //     a SwiGLU), so a step costs it one factor and 64 packed FMAs; with the scales read from shared
 //     memory, as above, those reads and the MMA's operands would share its bandwidth at par.
-//     The 128 sums of a thread and what is in flight need 208 registers: the other warps give theirs
-//     up (setmaxnreg).
+// The sums of an epilogue thread (up to 128) and what it has in flight need 184 or 208 registers: the other
+// warps give theirs up (setmaxnreg).
 //
 // Bounds and measurements (GB300, HBM at the measured 6784 GB/s, e4m3 at twice the measured bf16 rate):
 //   up projections + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 67 us, HBM floor 53; down projections
@@ -31,7 +31,7 @@
 //
 // Roles: warp 0 weight copies, warp 1 MMA issue (leader CTA), warps 2-5 or 2-6 token copies (tiles, or
 // gathers of four rows by index; warp 3 also allocates the tensor memory, warp 2 asks for the next
-// unit's weight scales), the others up to warp 7 scales, warps 8-15 epilogue.
+// unit's weight scales), the others up to warp 7 scales and units, warps 8-15 epilogue.
 #include <type_traits>
 
 #include "block_ops.cuh"
@@ -57,7 +57,6 @@ template <int BN, bool ACT>
 struct F8Cfg {
   static constexpr bool kTokenRows = BN == 256;              // tokens are the MMA's M operand
   // registers shared out anew by role: a thread's of the epilogue warps and of the others
-  static constexpr bool kSplit = true;
   static constexpr int kRegsMore = BN == 256 ? 208 : 184, kRegsLess = 256 - kRegsMore;
   static_assert(256 * (kRegsMore + kRegsLess) <= kF8Threads * kF8RegsLaunch, "register split");
   static constexpr int kHalf = BN / 2;                       // tokens a CTA loads
@@ -265,224 +264,224 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
     }
   };
   if (warp < 8) {
-  if constexpr (Cfg::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsLess));
-  if (warp == 0) {
-    const uint32_t bar0 = map_rank(&full[0], 0);
-    while (ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = tile_at(tile);
-      const int rows = p.c.perm != nullptr ? un.nhalf : cdiv(un.nhalf, Cfg::kChunk) * Cfg::kChunk;
-      const uint32_t bytes = 2u * (Cfg::kBytesW + rows * 128);
-      const int r = (2 * rb + (int)rank) * kRows;
-      for (int x = k0 * kF8K; x < (k0 + len) * kF8K; x += kF8K, ++issued) {
-        if (!mbar_wait_warp(&done[s], phase ^ 1, err)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          publish_count(s_fills, issued + 1);
-          const uint32_t bar = bar0 + 8 * s;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-          uint8_t* a = st + s * Cfg::kStage;
-          if constexpr (!ACT) {
-            tma2_load_3d(a, &p.tm_w, x, r, un.e, bar);
-          } else if (p.whole16) {
-            tma2_load_5d(a, &p.tm_w, x, 0, 0, r >> 4, un.e, bar);
-          } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              tma2_load_4d(a + b * 4096, &p.tm_w, x, r + 16 * b, 0, un.e, bar);
-          }
-        }
-        advance();
-      }
-    }
-    if (lane == 0) {
-      // the last fills have been multiplied: nothing arrives at this CTA's barriers any more
-      for (int j = max(0, issued - S); ok && j < issued; ++j)
-        ok = mbar_wait(&done[j % S], (j / S) & 1, err);
-      if (!ok && rank == 0) drain_stage_loads<S>(full, issued, err);
-    }
-  } else if (warp == 1) {
-    // operand descriptors: only the address changes from stage to stage and from K block to K block
-    const uint64_t desc0 = desc_sw128(st);
-    const uint32_t hi = (uint32_t)(desc0 >> 32), lo0 = (uint32_t)desc0;
-    uint32_t hand = 0;               // turns that have gone to tensor memory
-    bool ready = false;              // the next step's operands and buffer are known to be
-    // nothing commits to this phase before the first step's MMAs
-    if (p.d.probe_ns != 0 && blockIdx.x == 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(&done[0], 0, err, p.d.probe_ns));
-    while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = tile_at(tile);
-      const uint32_t idesc = idesc_pair8(Cfg::kTokenRows ? 256 : 2 * un.nhalf);
-      for (int i = 0; i < len; ++i) {
-        const uint32_t b = hand % TURNS;
-        if (!ready) {
-          if (i % Cfg::kTurn == 0)
-            ok = mbar_wait2_warp(&tempty[b], ((hand / TURNS) & 1) ^ 1, &full[s], phase, err);
-          else
-            ok = mbar_wait_warp(&full[s], phase, err);
-        }
-        if (!ok) break;
-        tc_fence_after();
-        // the next step, of this unit or another
-        const bool end = i % Cfg::kTurn == Cfg::kTurn - 1 || i + 1 == len;     // of the turn
-        const uint32_t s1 = s + 1 == S ? 0 : s + 1, h1 = hand + 1;
-        const bool next = mbar_test(&full[s1], phase ^ (s1 == 0)) &&
-                          (!end || mbar_test(&tempty[h1 % TURNS], ((h1 / TURNS) & 1) ^ 1));
-        if (elect_one()) {
-          const uint32_t lo = lo0 + s * (Cfg::kStage >> 4);
-#pragma unroll
-          for (int kb = 0; kb < 4; ++kb) {
-            const uint64_t dw = ((uint64_t)hi << 32) | (lo + 2 * kb);
-            const uint64_t dx = ((uint64_t)hi << 32) | (lo + (Cfg::kBytesW >> 4) + 2 * kb);
-            mma2_f8(tmem + (b * Cfg::kTurn + i % Cfg::kTurn) * BN, Cfg::kTokenRows ? dx : dw, Cfg::kTokenRows ? dw : dx, idesc, kb != 0);
-          }
-          tc2_commit(&done[s]);
-        }
-        advance();
-        hand += end;
-        ready = __all_sync(0xffffffffu, next);
-      }
-    }
-  } else if (warp < 2 + Cfg::kTokenWarps) {
-    const int tl = lane * Cfg::kTokenWarps + (warp - 2);
-    const uint32_t bar0 = map_rank(&full[0], 0);
-    // rows 4 tl .. 4 tl + 3 of this CTA's tokens by permutation (past the tile its last row again);
-    // a unit's entries are loaded under the copies of the one before it
-    int f[4] = {0, 0, 0, 0};
-    GtTile un = {};
-    const auto look_up = [&](int tile) {
-      un = tile_at(tile);
-      if (p.c.perm != nullptr) {
-        const int first = un.p0 + (int)rank * un.nhalf + 4 * tl;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = p.c.perm[min(first + i, un.p0 + un.n - 1)];
-      }
-      if (warp == 2) {
-        const int h = (lane >> 3) & 1, of = lane >> 4;   // set, and the CTA whose weight rows (tokens as M: both)
-        if (h < Cfg::kSets && (Cfg::kTokenRows || of == (int)rank))
-          f8_prefetch(scales_of(un.e, h, (2 * rb + of) * kRows) + k0, len, lane & 7);
-      }
-    };
-    // A warp may have no copy in a unit, and then nothing waits for it: it goes by the weight warp's
-    // count of empty stages, which the copies of every fill follow, and not by the barriers' parities
-    // (a warp two phases behind or ahead would take the wrong one).
-    int fill = 0;                    // fills before this unit
-    bool more = work.next(u, tile, rb, k0, len);
-    if (more) look_up(tile);
-    while (ok && more) {
-      int4 rows = make_int4(0, 0, 0, 0);
-      const bool gathers = p.c.perm != nullptr && 4 * tl < un.nhalf;
-      const bool copies = p.c.perm == nullptr && tl * Cfg::kChunk < un.nhalf;
-      if (gathers) {
-        int r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r[i] = f[i] < 0 ? -1 : f[i] / p.c.topk;
-          if (r[i] < 0 || r[i] >= p.c.x_rows) {
-            set_error(err, kErrRouteBounds);
-            r[i] = 0;
-          }
-        }
-        rows = make_int4(r[0], r[1], r[2], r[3]);
-      }
-      const int first = un.p0 + (int)rank * un.nhalf + tl * Cfg::kChunk;
-      const bool active = __any_sync(0xffffffffu, gathers || copies);
-      const int x0 = k0 * kF8K, steps = len;
-      more = work.next(u, tile, rb, k0, len);
-      if (more) look_up(tile);
-      if (active) {
-        s = fill % S;
-        for (int i = 0; i < steps; ++i) {
-          if (!wait_count_warp(s_fills, fill + i + 1, err)) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsLess));
+    if (warp == 0) {
+      const uint32_t bar0 = map_rank(&full[0], 0);
+      while (ok && work.next(u, tile, rb, k0, len)) {
+        const GtTile un = tile_at(tile);
+        const int rows = p.c.perm != nullptr ? un.nhalf : cdiv(un.nhalf, Cfg::kChunk) * Cfg::kChunk;
+        const uint32_t bytes = 2u * (Cfg::kBytesW + rows * 128);
+        const int r = (2 * rb + (int)rank) * kRows;
+        for (int x = k0 * kF8K; x < (k0 + len) * kF8K; x += kF8K, ++issued) {
+          if (!mbar_wait_warp(&done[s], phase ^ 1, err)) {
             ok = false;
             break;
           }
-          uint8_t* bs = st + s * Cfg::kStage + Cfg::kBytesW;
-          const int x = x0 + i * kF8K;
-          if (gathers) tma2_gather4(bs + tl * 512, &p.tm_x, x, rows, bar0 + 8 * s);
-          if (copies) tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, x, first, bar0 + 8 * s);
-          if (++s == S) s = 0;
+          if (lane == 0) {
+            publish_count(s_fills, issued + 1);
+            const uint32_t bar = bar0 + 8 * s;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+            uint8_t* a = st + s * Cfg::kStage;
+            if constexpr (!ACT) {
+              tma2_load_3d(a, &p.tm_w, x, r, un.e, bar);
+            } else if (p.whole16) {
+              tma2_load_5d(a, &p.tm_w, x, 0, 0, r >> 4, un.e, bar);
+            } else {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                tma2_load_4d(a + b * 4096, &p.tm_w, x, r + 16 * b, 0, un.e, bar);
+            }
+          }
+          advance();
         }
       }
-      fill += steps;
-    }
-  } else if constexpr (Cfg::kTokenRows) {
-    // tokens as M: units alone, the epilogue warps fetch their few scales themselves
-    while (ok && work.next(u, tile, rb, k0, len)) {
-      const GtTile un = tile_at(tile);
-      ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
-      if (!ok) break;
-      if (lane == 0) head(un, len, true);
-      publish();
-    }
-    if (ok && mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err)) {
-      if (lane == 0) s_head[slot * kF8Head + kF8Steps] = 0;
-      publish();
-    }
-  } else {
-    // Scales of the tokens' columns: warp 6 columns 0 .. 31 and 64 .. 95, warp 7 the others.  Those of the next
-    // four steps, of the next unit too, are on their way while these wait for their slot.
-    constexpr int M = (BN + 63) / 64, SETS = Cfg::kSets;
-    const int c0 = (warp - 6) * 32 + lane;
-    float nx[M][4], nw[SETS][4];
-    const float* xs[M];
-    const float* w[SETS];
-    GtTile un = {};
-    int i0 = 0, n = 0;
-    len = 0;
-    const auto fetch = [&]() {         // steps of the block that it asks for, 0 at the end
-      i0 += n;
-      if (i0 >= len) {
-        if (!work.next(u, tile, rb, k0, len)) return 0;
+      if (lane == 0) {
+        // the last fills have been multiplied: nothing arrives at this CTA's barriers any more
+        for (int j = max(0, issued - S); ok && j < issued; ++j)
+          ok = mbar_wait(&done[j % S], (j / S) & 1, err);
+        if (!ok && rank == 0) drain_stage_loads<S>(full, issued, err);
+      }
+    } else if (warp == 1) {
+      // operand descriptors: only the address changes from stage to stage and from K block to K block
+      const uint64_t desc0 = desc_sw128(st);
+      const uint32_t hi = (uint32_t)(desc0 >> 32), lo0 = (uint32_t)desc0;
+      uint32_t hand = 0;               // turns that have gone to tensor memory
+      bool ready = false;              // the next step's operands and buffer are known to be
+      // nothing commits to this phase before the first step's MMAs
+      if (p.d.probe_ns != 0 && blockIdx.x == 0)
+        ok = __all_sync(0xffffffffu, mbar_wait(&done[0], 0, err, p.d.probe_ns));
+      while (rank == 0 && ok && work.next(u, tile, rb, k0, len)) {
+        const GtTile un = tile_at(tile);
+        const uint32_t idesc = idesc_pair8(Cfg::kTokenRows ? 256 : 2 * un.nhalf);
+        for (int i = 0; i < len; ++i) {
+          const uint32_t b = hand % TURNS;
+          if (!ready) {
+            if (i % Cfg::kTurn == 0)
+              ok = mbar_wait2_warp(&tempty[b], ((hand / TURNS) & 1) ^ 1, &full[s], phase, err);
+            else
+              ok = mbar_wait_warp(&full[s], phase, err);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          // the next step, of this unit or another
+          const bool end = i % Cfg::kTurn == Cfg::kTurn - 1 || i + 1 == len;     // of the turn
+          const uint32_t s1 = s + 1 == S ? 0 : s + 1, h1 = hand + 1;
+          const bool next = mbar_test(&full[s1], phase ^ (s1 == 0)) &&
+                            (!end || mbar_test(&tempty[h1 % TURNS], ((h1 / TURNS) & 1) ^ 1));
+          if (elect_one()) {
+            const uint32_t lo = lo0 + s * (Cfg::kStage >> 4);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+              const uint64_t dw = ((uint64_t)hi << 32) | (lo + 2 * kb);
+              const uint64_t dx = ((uint64_t)hi << 32) | (lo + (Cfg::kBytesW >> 4) + 2 * kb);
+              mma2_f8(tmem + (b * Cfg::kTurn + i % Cfg::kTurn) * BN, Cfg::kTokenRows ? dx : dw, Cfg::kTokenRows ? dw : dx, idesc, kb != 0);
+            }
+            tc2_commit(&done[s]);
+          }
+          advance();
+          hand += end;
+          ready = __all_sync(0xffffffffu, next);
+        }
+      }
+    } else if (warp < 2 + Cfg::kTokenWarps) {
+      const int tl = lane * Cfg::kTokenWarps + (warp - 2);
+      const uint32_t bar0 = map_rank(&full[0], 0);
+      // rows 4 tl .. 4 tl + 3 of this CTA's tokens by permutation (past the tile its last row again);
+      // a unit's entries are loaded under the copies of the one before it
+      int f[4] = {0, 0, 0, 0};
+      GtTile un = {};
+      const auto look_up = [&](int tile) {
         un = tile_at(tile);
+        if (p.c.perm != nullptr) {
+          const int first = un.p0 + (int)rank * un.nhalf + 4 * tl;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-          xs[m] = p.xs + row_of(un.p0 + min(c0 + 64 * m, un.n - 1)) * p.ldxs + k0;
+          for (int i = 0; i < 4; ++i) f[i] = p.c.perm[min(first + i, un.p0 + un.n - 1)];
+        }
+        if (warp == 2) {
+          const int h = (lane >> 3) & 1, of = lane >> 4;   // set, and the CTA whose weight rows (tokens as M: both)
+          if (h < Cfg::kSets && (Cfg::kTokenRows || of == (int)rank))
+            f8_prefetch(scales_of(un.e, h, (2 * rb + of) * kRows) + k0, len, lane & 7);
+        }
+      };
+      // A warp may have no copy in a unit, and then nothing waits for it: it goes by the weight warp's
+      // count of empty stages, which the copies of every fill follow, and not by the barriers' parities
+      // (a warp two phases behind or ahead would take the wrong one).
+      int fill = 0;                    // fills before this unit
+      bool more = work.next(u, tile, rb, k0, len);
+      if (more) look_up(tile);
+      while (ok && more) {
+        int4 rows = make_int4(0, 0, 0, 0);
+        const bool gathers = p.c.perm != nullptr && 4 * tl < un.nhalf;
+        const bool copies = p.c.perm == nullptr && tl * Cfg::kChunk < un.nhalf;
+        if (gathers) {
+          int r[4];
 #pragma unroll
-        for (int h = 0; h < SETS; ++h) w[h] = scales_of(un.e, h, (2 * rb + (int)rank) * kRows) + k0;
-        i0 = 0;
+          for (int i = 0; i < 4; ++i) {
+            r[i] = f[i] < 0 ? -1 : f[i] / p.c.topk;
+            if (r[i] < 0 || r[i] >= p.c.x_rows) {
+              set_error(err, kErrRouteBounds);
+              r[i] = 0;
+            }
+          }
+          rows = make_int4(r[0], r[1], r[2], r[3]);
+        }
+        const int first = un.p0 + (int)rank * un.nhalf + tl * Cfg::kChunk;
+        const bool active = __any_sync(0xffffffffu, gathers || copies);
+        const int x0 = k0 * kF8K, steps = len;
+        more = work.next(u, tile, rb, k0, len);
+        if (more) look_up(tile);
+        if (active) {
+          s = fill % S;
+          for (int i = 0; i < steps; ++i) {
+            if (!wait_count_warp(s_fills, fill + i + 1, err)) {
+              ok = false;
+              break;
+            }
+            uint8_t* bs = st + s * Cfg::kStage + Cfg::kBytesW;
+            const int x = x0 + i * kF8K;
+            if (gathers) tma2_gather4(bs + tl * 512, &p.tm_x, x, rows, bar0 + 8 * s);
+            if (copies) tma2_load_2d(bs + tl * Cfg::kChunk * 128, &p.tm_x, x, first, bar0 + 8 * s);
+            if (++s == S) s = 0;
+          }
+        }
+        fill += steps;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = min(i0 + j, len - 1);
-#pragma unroll
-        for (int m = 0; m < M; ++m) nx[m][j] = xs[m][i];
-#pragma unroll
-        for (int h = 0; h < SETS; ++h) nw[h][j] = w[h][i];
-      }
-      return min(4, len - i0);
-    };
-    n = fetch();
-    while (ok) {
-      ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
-      if (!ok) break;
-      if (warp == 6 && lane == 0) head(un, n, i0 + 4 >= len);
-      if (n == 0) {
+    } else if constexpr (Cfg::kTokenRows) {
+      // tokens as M: units alone, the epilogue warps fetch their few scales themselves
+      while (ok && work.next(u, tile, rb, k0, len)) {
+        const GtTile un = tile_at(tile);
+        ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
+        if (!ok) break;
+        if (lane == 0) head(un, len, true);
         publish();
-        break;
       }
-      float now[M][SETS][4];
-#pragma unroll
-      for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int h = 0; h < SETS; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) now[m][h][j] = nx[m][j] * nw[h][j];
-      n = fetch();
-      float* to = s_scale + slot * Cfg::kSlot + c0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int h = 0; h < SETS; ++h)
+      if (ok && mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err)) {
+        if (lane == 0) s_head[slot * kF8Head + kF8Steps] = 0;
+        publish();
+      }
+    } else {
+      // Scales of the tokens' columns: warp 6 columns 0 .. 31 and 64 .. 95, warp 7 the others.  Those of the next
+      // four steps, of the next unit too, are on their way while these wait for their slot.
+      constexpr int M = (BN + 63) / 64, SETS = Cfg::kSets;
+      const int c0 = (warp - 6) * 32 + lane;
+      float nx[M][4], nw[SETS][4];
+      const float* xs[M];
+      const float* w[SETS];
+      GtTile un = {};
+      int i0 = 0, n = 0;
+      len = 0;
+      const auto fetch = [&]() {         // steps of the block that it asks for, 0 at the end
+        i0 += n;
+        if (i0 >= len) {
+          if (!work.next(u, tile, rb, k0, len)) return 0;
+          un = tile_at(tile);
 #pragma unroll
           for (int m = 0; m < M; ++m)
-            if (c0 + 64 * m < BN) to[j * Cfg::kStep + h * Cfg::kPad + 64 * m] = now[m][h][j];
-      publish();
+            xs[m] = p.xs + row_of(un.p0 + min(c0 + 64 * m, un.n - 1)) * p.ldxs + k0;
+#pragma unroll
+          for (int h = 0; h < SETS; ++h) w[h] = scales_of(un.e, h, (2 * rb + (int)rank) * kRows) + k0;
+          i0 = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = min(i0 + j, len - 1);
+#pragma unroll
+          for (int m = 0; m < M; ++m) nx[m][j] = xs[m][i];
+#pragma unroll
+          for (int h = 0; h < SETS; ++h) nw[h][j] = w[h][i];
+        }
+        return min(4, len - i0);
+      };
+      n = fetch();
+      while (ok) {
+        ok = mbar_wait_warp(&sempty[slot], (turn & 1) ^ 1, err);
+        if (!ok) break;
+        if (warp == 6 && lane == 0) head(un, n, i0 + 4 >= len);
+        if (n == 0) {
+          publish();
+          break;
+        }
+        float now[M][SETS][4];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int h = 0; h < SETS; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) now[m][h][j] = nx[m][j] * nw[h][j];
+        n = fetch();
+        float* to = s_scale + slot * Cfg::kSlot + c0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < SETS; ++h)
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+              if (c0 + 64 * m < BN) to[j * Cfg::kStep + h * Cfg::kPad + 64 * m] = now[m][h][j];
+        publish();
+      }
     }
-  }
   } else {
-    if constexpr (Cfg::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsMore));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsMore));
     // Groups of four warps share the columns of every step.  They follow the slots of scales, which say where
     // units end; nothing of the schedule is kept in their registers.
     constexpr int CW = Cfg::kWide, SETS = Cfg::kSets;
@@ -823,7 +822,7 @@ static cudaError_t launch_f8(F8Params& p, cudaStream_t st) {
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    if (Cfg::kSplit) {
+    {
       // the split draws on the registers of the launch: with fewer it would wait forever
       cudaFuncAttributes a;
       e = cudaFuncGetAttributes(&a, kernel);
