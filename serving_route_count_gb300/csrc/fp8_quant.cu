@@ -70,10 +70,13 @@ struct Quant16 {
       return m;
     }
   }
-  // Codes by one reciprocal, with Markstein's correction: for r = 1 / s rounded to nearest and q within an
-  // ulp of x / s, q + r (x - q s) with two fused operations is x / s rounded to nearest.  The residual has
-  // to be exact: scales of 2^-60 and more keep it above the least subnormal wherever the quotient does not
-  // round to a zero code; smaller scales and infinite ones take the division.
+  // Codes by one reciprocal, with Markstein's correction: for r = 1 / s rounded to nearest and q near x / s, the
+  // two fused operations of q + r (x - q s) give x / s rounded to nearest.  His theorem asks for a q within an ulp;
+  // q = x r may be 1.5 off (half an ulp of its own rounding, up to one by r's).  What is needed here is less: only
+  // quotients next to the middle of two codes decide a code, and for every mantissa of s, every middle and all x
+  // within 3 ulps of their product the result is the IEEE quotient (4.7e9 cases, on the host).  The residual must
+  // not underflow: scales of 2^-60 and more keep it above the least subnormal wherever the quotient does not round
+  // to a zero code; smaller scales and infinite ones take the division.
   __device__ __forceinline__ uint4 codes(float scale) const {
     T v[16];
     memcpy(v, w, sizeof(v));

@@ -150,6 +150,31 @@ def test_quant_extremes(moe, form, dtype):
     check_quant(moe, x.cuda(), form)
 
 
+def next_to_middles(s, seed):
+    """fp32 values, 127 to a row: middles of two codes times the row's scale s, up to 2 ulps off, of both signs."""
+    rng = np.random.default_rng(seed)
+    mids = np.concatenate([np.arange(1, 16, 2) * 2.0 ** -10] + [(8.5 + np.arange(8)) * 2.0 ** e for e in range(-9, 6)]).astype(np.float32)
+    mids = mids[mids < 448]
+    x = rng.choice(mids, (len(s), 127)) * s[:, None]                            # rounded to fp32 once
+    return (x.view(np.int32) + rng.integers(-2, 3, x.shape, np.int32)).view(np.float32) * rng.choice(np.float32([-1, 1]), x.shape)
+
+
+@gpu
+@pytest.mark.parametrize("least", [2.0 ** -8, 2.0 ** -60 * (1 - 2.0 ** -12), 2.0 ** -100, 2.0 ** 100])
+def test_quant_next_to_the_middle_of_two_codes(moe, least):
+    """Scales of many mantissas, on both sides of the one from which a reciprocal replaces the division; codes
+    and scales are those of the IEEE quotients, bit for bit."""
+    rng = np.random.default_rng(5)
+    s = np.concatenate((np.float32(least) * (1 + rng.random(8192)).astype(np.float32), np.float32(least) * (1 + np.arange(-64, 8192, 2) * np.float32(2.0 ** -23))))
+    top = s.astype(np.float32) * np.float32(448)                                # the largest value, whose scale is within an ulp of s
+    s = top / np.float32(448)
+    x = torch.from_numpy(np.concatenate((top[:, None], next_to_middles(s, 6)), axis=1)).cuda()
+    q, _ = check_quant(moe, x, moe.MOE_FP8_ROWS)
+    shifted = torch.empty(x.numel() + 1, device="cuda")[1:].view(x.shape)       # rows off 16 bytes: the division throughout
+    q2, _ = check_quant(moe, shifted.copy_(x), moe.MOE_FP8_ROWS)
+    assert np.array_equal(codes(q), codes(q2))
+
+
 @gpu
 def test_quant_strides_and_outputs(moe):
     """Row strides of input and outputs, bases off 16 bytes; what lies between the rows stays as it was."""
