@@ -570,7 +570,8 @@ void moe_destroy_fp8(moe_fp8_t* plan);
 typedef struct moe_ff_s moe_ff_t;
 moe_status moe_ff_plan(int H, int I, int dtype, int layout, float limit, float alpha, float beta,
                        int max_rows, moe_ff_t** out);
-/* Bytes of the scratch buffer of both passes (256-byte aligned, caller-owned). */
+/* Bytes of the scratch buffer of both passes (256-byte aligned, caller-owned), by max_rows: 5 MB up to 32 tokens,
+ * 10 up to 64, 21 up to 128, 42 beyond, and the rows [max_rows, 2 I] between two products. */
 moe_status moe_ff_scratch_bytes(const moe_ff_t* plan, size_t* bytes);
 /* y [M, H] of x [M, H], w13 [2 I, H], w2 [H, I] (row strides ld*).
  *   scratch  as for moe_grouped_run: its first 4096 bytes zero before the first use, calls that share it

@@ -15,7 +15,7 @@ cudaError_t launch_ff_simt(const FfDims& d, const FfGemm& g, int epilogue, cudaS
 bool ff_gemv_takes(const FfGemm& g, int epilogue);
 cudaError_t launch_ff_gemv(const FfDims& d, const FfGemm& g, int epilogue, bool early, cudaStream_t st);
 // gemm_ff_tc.cu
-size_t ff_tc_part_bytes();
+size_t ff_tc_part_bytes(int max_rows);
 bool ff_tc_addressable(const FfGemm& g);
 cudaError_t launch_ff_tc(const FfDims& d, const FfGemm& g, int epilogue, float* part, int32_t* tickets,
                          cudaStream_t st);
@@ -62,7 +62,7 @@ moe_status moe_ff_plan(int H, int I, int dtype, int layout, float limit, float a
   moe_ff_s* f = new (std::nothrow) moe_ff_s();
   if (f == nullptr) return MOE_ERR_ARG;
   f->d = FfDims{H, I, dtype, layout, max_rows, limit, alpha, beta, 0};
-  f->rows_at = kGtPartAt + ff_tc_part_bytes();
+  f->rows_at = kGtPartAt + ff_tc_part_bytes(max_rows);
   // h [M, I] of a forward pass, d(up, gate) [M, 2 I] of a backward one
   f->bytes = f->rows_at + align_up((size_t)max_rows * 2 * I * 2, 256);
   *out = f;

@@ -489,10 +489,11 @@ ff_tc_kernel(const __grid_constant__ FtParams p) {
 // H = I = 4096, M = 2048 - / 315w / 187w / 129w.
 // Sums over tokens have both operands the other way round, whose boxes are 64 wide for each CTA: 128 at
 // least.
+// Units are cut at widths up to cut_bn, which the scratch buffer holds the pieces of.
 struct FtPlan {
   int bn, cut;
 };
-static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
+static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs, int cut_bn) {
   FtPlan best{256, 0};
   double least = 1e300;
   for (int bn = g.ck != 1 ? 128 : 32; bn <= 256; bn *= 2) {
@@ -502,7 +503,7 @@ static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
     const long long waves = units / pairs, left = units % pairs;
     const double base = (double)waves * KT * step;
     double whole = base + (left ? KT * step : 0), cut = 1e300;
-    if (left) {
+    if (left && bn <= cut_bn) {
       const double pieces = (double)pairs / left + 1, rows = cdiv(g.nc, tiles);
       cut = base + (double)left * KT / pairs * step + 3500 + rows * (75 + 4.3 * pieces);
     }
@@ -519,8 +520,16 @@ static FtPlan ff_tc_plan(const FfGemm& g, int epilogue, int pairs) {
   return best;
 }
 
-// Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of the widest tile.
-size_t ff_tc_part_bytes() { return (size_t)kGtMaxPairs * 2 * 2 * 256 * 128 * sizeof(float); }
+// The widest tile that a plan of up to max_rows tokens cuts: the one that holds them all.  Wider ones are of
+// the sums over tokens, whose K is the tokens: up to 128 of them are two K steps, which take less time than joining
+// pieces does, so those products would not be cut anyway.
+static int ff_cut_width(int max_rows) {
+  return max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : (max_rows <= 128 ? 128 : 256));
+}
+// Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of that tile (5 MB up to 32 tokens, 42 past 128).
+size_t ff_tc_part_bytes(int max_rows) {
+  return (size_t)kGtMaxPairs * 2 * 2 * ff_cut_width(max_rows) * 128 * sizeof(float);
+}
 
 static bool ft_tmap(CUtensorMap* tm, bool bf16, int rank, const void* base, const cuuint64_t* dims,
                     const cuuint64_t* strides, const cuuint32_t* box) {
@@ -600,7 +609,7 @@ static cudaError_t launch_ft_bn(FtParams& p, cudaStream_t st) {
     return e;
   });
   if (e != cudaSuccess) return e;
-  const FtPlan plan = ff_tc_plan(p.g, EPI, pairs);
+  const FtPlan plan = ff_tc_plan(p.g, EPI, pairs, ff_cut_width(p.d.max_rows));
   p.cut = plan.cut;
   switch (plan.bn) {
     case 32: return launch_ft<EPI, 32>(p, st);

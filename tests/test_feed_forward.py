@@ -107,6 +107,19 @@ def test_arguments():
             m.moe_ff_plan(8, 8, 0, 0, 1.0, alpha, beta, 4)
 
 
+def test_scratch_bytes_by_rows():
+    """A plan of a few tokens, as each layer of a decode step has one, does not hold the widest tile's pieces: 80 pairs x 2
+    pieces x 2 CTAs x 128 rows in fp32 for each token of the tile, the first 4096 bytes and the rows between two products."""
+    import serving_route_count_gb300 as m
+    from serving_route_count_gb300 import build
+    build.build()
+    for max_rows, tile in ((0, 32), (1, 32), (32, 32), (33, 64), (64, 64), (65, 128), (128, 128), (129, 256), (4096, 256)):
+        p = m.moe_ff_plan(7168, 1152, m.MOE_DTYPE_BF16, 0, math.inf, 1.0, 0.0, max_rows)
+        need = 4096 + 80 * 2 * 2 * tile * 128 * 4 + max_rows * 2 * 1152 * 2
+        assert need <= m.moe_ff_scratch_bytes(p) < need + 256
+        m.moe_destroy_ff(p)
+
+
 # ------------------------------------------------------------------------------------ both passes
 
 def strided(t, ld, shift=0):
@@ -273,6 +286,26 @@ def test_a_few_tokens(moe, M, H, I):
         graph.replay()
         assert torch.equal(out, y)
     assert op.device_error() == (0, 0)
+
+
+@gpu
+@pytest.mark.parametrize("max_rows", [1, 3, 32, 33, 64, 65, 128, 129])
+@pytest.mark.parametrize("H,I", [(7168, 576), (520, 4104)])
+def test_scratch_of_a_small_plan(moe, H, I, max_rows):
+    """Nothing is written behind the bytes that a plan asks for, and the results are those of a plan of more tokens, bit for bit."""
+    op, large = moe.MoEFeedForward(H, I, max_rows), moe.MoEFeedForward(H, I, 512)
+    n = op.scratch.numel()
+    buf = torch.full((n + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    buf[:4096] = 0
+    op.scratch, op._fixed = buf[:n], (op.plan, buf.data_ptr(), n)
+    for M in sorted({1, max_rows // 2 + 1, max_rows}):
+        x, w13, w2, dy = operands(M, H, I, "bf16", M)
+        y, saved = op.forward(x, w13, w2)
+        want, kept = large.forward(x, w13, w2)
+        assert torch.equal(y, want) and torch.equal(op(x, w13, w2), want) and all(torch.equal(a, b) for a, b in zip(saved, kept))
+        for a, b in zip(op.backward(dy, x, w13, w2, saved), large.backward(dy, x, w13, w2, kept)):
+            assert torch.equal(a, b)
+    assert torch.all(buf[n:] == 0xA5) and op.device_error() == (0, 0)
 
 
 @gpu
