@@ -544,9 +544,9 @@ moe_status moe_fp8_scratch_bytes(const moe_fp8_t* plan, size_t* bytes);
  *   x [x_rows, K] codes, row stride ldx, x_scale [x_rows, KB], row stride ldxs;  w [E, N, K] codes with
  *   row stride ldw and expert stride ldw * N, w_scale [E, tile rows, KB] contiguous;  out [S, N or
  *   N / 2], row stride ldo.  out must not overlap an input.
- * Rows whose x, w and strides are 16-byte aligned run on the tensor cores (a few positions, two of one
- * matrix, four where K >= 4096, or eight over experts, on the CUDA cores, which then read the weights
- * faster); other operands (for instance K % 16 != 0) on the CUDA cores, slower.
+ * Rows whose x, w and strides are 16-byte aligned run on the tensor cores; a few positions of a matrix that is not
+ * too large, at most two of one matrix, four where K >= 4096, or eight over experts, on the CUDA cores, where those
+ * read the weights faster.  Other operands (for instance K % 16 != 0) run on the CUDA cores, slower.
  * Errors: MOE_ERR_ARG, MOE_ERR_CAPACITY (S > max_rows), MOE_ERR_CUDA. */
 moe_status moe_fp8_run(const moe_fp8_t* plan, void* scratch, size_t scratch_bytes, const uint8_t* x,
                        long long ldx, int x_rows, const float* x_scale, long long ldxs, const uint8_t* w,

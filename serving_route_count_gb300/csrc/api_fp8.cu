@@ -15,7 +15,7 @@ cudaError_t launch_fp8_quant(const void* x, int dtype, long long ldx, int E, int
 // gemm_fp8_simt.cu
 cudaError_t launch_fp8_simt(const GroupedDims& d, const Fp8Call& f, cudaStream_t st);
 // gemv_fp8.cu
-bool fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f);
+cudaError_t fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f, bool* takes);
 cudaError_t launch_fp8_gemv(const GroupedDims& d, const Fp8Call& f, cudaStream_t st);
 // gemm_fp8_tc.cu
 size_t fp8_tc_part_bytes(int S, int E);
@@ -109,7 +109,10 @@ moe_status moe_fp8_run(const moe_fp8_t* plan, void* scratch, size_t scratch_byte
                   x_scale, ldxs, w_scale};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!fp8_tc_addressable(d, f)) return status(launch_fp8_simt(d, f, st));
-  if (fp8_gemv_takes(d, f)) return status(launch_fp8_gemv(d, f, st));
+  bool few = false;
+  const cudaError_t e = fp8_gemv_takes(d, f, &few);
+  if (e != cudaSuccess) return status(e);
+  if (few) return status(launch_fp8_gemv(d, f, st));
   uint8_t* base = static_cast<uint8_t*>(scratch);
   return status(launch_fp8_tc(d, f, reinterpret_cast<float*>(base + kGtPartAt),
                               reinterpret_cast<int32_t*>(base + kGtTicketsAt), st));

@@ -1,5 +1,5 @@
-// block_launch.cuh - launch shapes of the 16-bit block's kernels: host arithmetic alone, without
-// CUDA, so that it can be checked on any host.
+// block_launch.cuh - launch shapes of the kernels of the 16-bit block and of the 8-bit products of a few
+// positions: host arithmetic alone, without CUDA, so that it can be checked on any host.
 #pragma once
 
 #include <algorithm>
@@ -74,6 +74,48 @@ struct GsGrid {
 inline GsGrid grouped_simt_grid(int S, int E, int cols) {
   return {(unsigned)((S + kGsTile - 1) / kGsTile) + (unsigned)std::min(E, S),
           (unsigned)std::min((cols + kGsTile - 1) / kGsTile, 65535)};
+}
+
+// ---------------------------------------------------------------------------------- 8-bit products of a few positions
+constexpr int kF8vThreads = 256, kF8vWarps = kF8vThreads / 32;
+
+// CUDA-core kernel: positions that share a CTA's rows, warps of an output column, CTAs over the columns and over
+// the positions.
+struct F8vShape {
+  int nc, warps, x, y;
+};
+
+inline F8vShape fp8_few_shape(int S, bool offsets, int cols, int K, int sms) {
+  F8vShape f;
+  f.nc = offsets ? 1 : (S > 2 ? 4 : S);
+  f.y = (S + f.nc - 1) / f.nc;
+  f.warps = 1;
+  // warps enough for every SM to have 16, as far as each still has a vector of every lane
+  while (f.warps < kF8vWarps && (long long)cols * f.y * f.warps < 16LL * sms && K > f.warps * 512) f.warps *= 2;
+  const int per = kF8vWarps / f.warps;
+  f.x = (cols + per - 1) / per;
+  return f;
+}
+
+// Whether a call takes that kernel or the tensor cores', whose units stream a matrix once for all positions of it, after
+// a start of 6 us and more with K.  The CUDA cores win as long as their CTAs run at once or nearly: an SM holds four
+// (a SwiGLU's hold twice the loads), and of those without a SwiGLU a second wave pays still.  us on the CUDA cores /
+// on the tensor cores, weights from HBM:
+//   one position to a CTA (offsets), by CTAs: SwiGLU K = 6144, N = 1024, 8 positions of as many experts, 512 CTAs: 19.2 /
+//   23.0;  K = 7168, N = 2304, 4 (576): 22.8 / 26.0, 6 (864): 39.2 / 30.2;  K = 2048, N = 8192, 1 (512): 8.4 / 16.6, 2
+//   (1024): 15.1 / 13.4;  none: K = 7168, N = 9216, 1 (1152): 23.4 / 25.5;  K = 4096, N = 2560, 4 (1280): 15.6 / 21.3;
+//   K = 576, N = 7168, 1 (896): 7.1 / 7.8, 2 (1792): 11.7 / 8.8, 8 (7168): 40.9 / 15.2;  K = 576, N = 16384, 1 (2048): 13.2 / 9.0.
+//   Positions of one expert read its rows once each, where the tensor cores read them once: K = 7168, N = 2304, 4: 19.0 / 19.0.
+//   two of one matrix: SwiGLU K = 7168, N = 2304 (576): 9.1 / 18.3;  none: K = 4096, N = 4096 (512): 10.7 / 16.5;  K = 512,
+//   N = 6144 (768): 7.1 / 6.2;  K = 7168, N = 7168 (896): 27.4 / 21.9.
+//   three or four: K = 7168, N = 2304 SwiGLU 15.1 / 18.3;  K = 4096, N = 2560 12.0 / 15.4;  K = 7168, N = 2816 22.2 / 17.8;
+//   K = 4096, N = 4096 20.9 / 16.6;  K = 2048, N = 4096 12.5 / 9.9.
+inline bool fp8_few_takes(int S, int E, bool offsets, bool act, int N, int K, int sms) {
+  if (K % 16 != 0 || S < 1 || S > (E > 1 ? 8 : (K >= 4096 ? 4 : 2))) return false;
+  const F8vShape f = fp8_few_shape(S, offsets, act ? N / 2 : N, K, sms);
+  const long long ctas = (long long)f.x * f.y;
+  if (f.nc == 4) return ctas <= 4LL * sms && N <= 2560;
+  return ctas <= (f.nc == 1 && !act ? 17LL * sms / 2 : 4LL * sms);
 }
 
 // ---------------------------------------------------------------------------------- norms

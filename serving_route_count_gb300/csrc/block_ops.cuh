@@ -15,6 +15,16 @@ cudaError_t on_device(PerDevice<V>& per, V* out, Init init) {
   return e != cudaSuccess ? e : static_cast<cudaError_t>(per.get(dev, out, init));
 }
 
+// SMs of the current device.
+inline cudaError_t device_sms(int* sms) {
+  static PerDevice<int> per;
+  return on_device(per, sms, [](int* v) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+  });
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

@@ -1,11 +1,11 @@
-// gemv_fp8.cu - 8-bit products with block scales for a few positions: two of one matrix, four where K is
-// long, or eight over experts (one token's).
+// gemv_fp8.cu - 8-bit products with block scales for a few positions, of one matrix or over experts (one token's),
+// where they are few enough for this launch (fp8_few_takes in block_launch.cuh: the rule and both sides' times).
 //
 // Bound by reading the weights once.  One to eight warps to an output column (SwiGLU: to a pair of weight
 // rows), as many as fill the GPU; a lane takes 16 codes of every row at a time, all of one block, sums
 // their products in fp32 and adds them times both scales.  Sums go lane by lane, then over the lanes, then
-// over the warps: one order.  Positions of one matrix share its rows; over experts each position reads its
-// own expert's (two of one expert read them twice, the second time from L2).
+// over the warps: one order.  Positions of one matrix share its rows; where there are offsets each position reads its
+// expert's, also where two have the same one: a matrix sweep apart, so from L2 only where the matrix fits there.
 #include <cuda_fp8.h>
 
 #include "block_ops.cuh"
@@ -13,8 +13,6 @@
 #include "../../include/moe_gb300.h"
 
 namespace moe {
-
-constexpr int kF8vThreads = 256, kF8vWarps = kF8vThreads / 32;
 
 struct F8vParams {
   GroupedDims d;
@@ -142,24 +140,24 @@ __global__ void __launch_bounds__(kF8vThreads) fp8_gemv_kernel(const F8vParams p
   out[(long long)(p0 + lane) * c.ldo + col] = from_f32<T>(y);
 }
 
-// A few positions in whole vectors (their alignment as for the tensor cores).  Of one matrix, us here / on the
-// tensor cores: K = 7168, N = 2304 SwiGLU 1: 7.3 / 18.7;  2: 9.0 / 18.4;  4: 13.8 / 18.4;  8: 23 / 19;  K = 1152,
-// N = 7168 1: 6.8 / 9.1;  2: 8.4 / 9.0;  4: 13.1 / 9.3 (a long K is cut into pieces there, which are joined).  Over
-// experts (E = 256, K = 6144, N = 1024) 8: 18.5 / 21.9;  16: 34.4 / 26.1.
-bool fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f) {
-  return f.c.S <= (d.E > 1 ? 8 : (d.K >= 4096 ? 4 : 2)) && d.K % 16 == 0;
+// A few positions in whole vectors (their alignment as for the tensor cores).
+cudaError_t fp8_gemv_takes(const GroupedDims& d, const Fp8Call& f, bool* takes) {
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  *takes = e == cudaSuccess && fp8_few_takes(f.c.S, d.E, f.c.offsets != nullptr, d.act != 0, d.N, d.K, sms);
+  return e;
 }
 
 template <typename T, bool ACT>
 static cudaError_t launch_f8v(F8vParams& p, cudaStream_t st) {
-  const int nc = p.f.c.offsets != nullptr ? 1 : (p.f.c.S > 2 ? 4 : p.f.c.S);
-  const int each = cdiv(p.f.c.S, nc);
-  // warps enough for every SM to have 16, as far as each still has a vector of every lane
-  while (p.warps < kF8vWarps && (long long)p.cols * each * p.warps < 152 * 16 && p.d.K > p.warps * 512) p.warps *= 2;
-  const dim3 grid(cdiv(p.cols, kF8vWarps / p.warps), each);
-  const auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kF8vThreads), 0, st, true, p); };
-  if (nc == 1) return go(fp8_gemv_kernel<T, ACT, 1>);
-  return nc == 2 ? go(fp8_gemv_kernel<T, ACT, 2>) : go(fp8_gemv_kernel<T, ACT, 4>);
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  const F8vShape f = fp8_few_shape(p.f.c.S, p.f.c.offsets != nullptr, p.cols, p.d.K, sms);
+  p.warps = f.warps;
+  const auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(f.x, f.y), dim3(kF8vThreads), 0, st, true, p); };
+  if (f.nc == 1) return go(fp8_gemv_kernel<T, ACT, 1>);
+  return f.nc == 2 ? go(fp8_gemv_kernel<T, ACT, 2>) : go(fp8_gemv_kernel<T, ACT, 4>);
 }
 
 cudaError_t launch_fp8_gemv(const GroupedDims& d, const Fp8Call& f, cudaStream_t st) {
