@@ -110,8 +110,11 @@ bool ff_gemv_takes(const FfGemm& g, int epilogue) {
 template <typename T, int EPI>
 static cudaError_t launch_fv(FvParams& p, cudaStream_t st) {
   // warps enough for every SM to have 16, as far as each still has a vector of every lane
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
   p.warps = 1;
-  while (p.warps < kFvWarps && p.g.nr * p.warps < 152 * 16 && p.g.K > p.warps * 256) p.warps *= 2;
+  while (p.warps < kFvWarps && p.g.nr * p.warps < sms * 16 && p.g.K > p.warps * 256) p.warps *= 2;
   const dim3 grid(cdiv(p.g.nr, kFvWarps / p.warps));
   const auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kFvThreads), 0, st, true, p); };
   return p.g.nc == 1 ? go(ff_gemv_kernel<T, EPI, 1>) : go(ff_gemv_kernel<T, EPI, 2>);
