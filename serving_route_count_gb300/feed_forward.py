@@ -116,16 +116,23 @@ class MoEFeedForward:
     def backward(self, dy, x, w13, w2, saved, need=(True, True, True), dx=None, dw13=None, dw2=None,
                  stream=None):
         """(dx, dw13, dw2) of forward's y at dy [M, H], in new tensors or the given ones; None for each
-        that `need` leaves out.  x, w13, w2 and saved are forward's."""
+        that `need` leaves out.  x, w13, w2 and saved are forward's; those that no gradient of `need` takes may be
+        None: x (dw13), w13 (dx), saved[1] (dw2), w2 and saved[0] (dx and dw13)."""
         dev = self._here(dy, "dy")
         H, I, dtype = self.H, self.I, self.dtype
         dyp, lddy = _rows(dy, "dy", dev, None, H, dtype)
         M = dy.shape[0]
-        xp, ldx = _rows(x, "x", dev, M, H, dtype)
-        w13p, ldw13 = _rows(w13, "w13", dev, 2 * I, H, dtype)
-        w2p, ldw2 = _rows(w2, "w2", dev, H, I, dtype)
-        pre, h = saved
-        pre_p, h_p = _whole(pre, "saved[0]", dev, torch.float32, M * 2 * I), _whole(h, "saved[1]", dev, dtype, M * I)
+        need_x, need_w13, need_w2 = need
+        inner = need_x or need_w13
+        pre, h = (None, None) if saved is None else saved
+        for t, name, used in ((x, "x", need_w13), (w13, "w13", need_x), (w2, "w2", inner), (pre, "saved[0]", inner), (h, "saved[1]", need_w2)):
+            if t is None and used:
+                raise ValueError(f"{name} is needed for these gradients")
+        xp, ldx = (None, H) if x is None else _rows(x, "x", dev, M, H, dtype)
+        w13p, ldw13 = (None, H) if w13 is None else _rows(w13, "w13", dev, 2 * I, H, dtype)
+        w2p, ldw2 = (None, I) if w2 is None else _rows(w2, "w2", dev, H, I, dtype)
+        pre_p = None if pre is None else _whole(pre, "saved[0]", dev, torch.float32, M * 2 * I)
+        h_p = None if h is None else _whole(h, "saved[1]", dev, dtype, M * I)
         wanted, on = [], dy.device
         for needed, t, name, rows, cols in zip(need, (dx, dw13, dw2), ("dx", "dw13", "dw2"), (M, 2 * I, H), (H, H, I)):
             if not needed:

@@ -126,6 +126,33 @@ def test_one_matrix(lib, w, ldw):
         product()(t((4, 144), E4M3), t((4, 2), F32), t((2, 8, 144), E4M3), t((2, 1, 2), F32), out=t((4, 8)), stream=7)
 
 
+def test_operands_that_no_gradient_takes(lib):
+    """What the C call takes as NULL may be None; what a gradient needs may not."""
+    _, tensors, other = operands()[4]
+    pre, h = other["saved"]
+    uses = dict(x=(0, 1, 0), w13=(1, 0, 0), w2=(1, 1, 0), pre=(1, 1, 0), h=(0, 0, 1))
+    for need in [(a, b, c) for a in (False, True) for b in (False, True) for c in (False, True)]:
+        kept = {k: v for k, v in tensors.items() if k not in ("dx", "dw13", "dw2") or need[("dx", "dw13", "dw2").index(k)]}
+        have = {k: any(n and u for n, u in zip(need, use)) for k, use in uses.items()}
+        kept.update({k: v if have[k] else None for k, v in kept.items() if k in uses})
+        saved = (pre if have["pre"] else None, h if have["h"] else None)
+        got = feed().backward(**kept, saved=saved if any(need) else None, need=need, stream=7)
+        args = lib.calls[-1][1]
+        assert [g is not None for g in got] == list(need)
+        assert [args[i] is not None for i in (5, 7, 9, 11, 12)] == [have[k] for k in ("x", "w13", "w2", "pre", "h")]
+        n = len(lib.calls)
+        for k in uses:
+            if have[k]:
+                bad = {**kept, "saved": saved}
+                if k in kept:
+                    bad[k] = None
+                else:
+                    bad["saved"] = (None, saved[1]) if k == "pre" else (saved[0], None)
+                with pytest.raises(ValueError, match="saved" if k in ("pre", "h") else k):
+                    feed().backward(**bad, need=need, stream=7)
+        assert len(lib.calls) == n
+
+
 def test_gradients_left_out(lib):
     _, tensors, other = operands()[4]
     for need in ((True, False, False), (False, True, False), (False, False, True)):

@@ -414,6 +414,17 @@ def test_some_gradients(moe):
 
 
 @gpu
+def test_some_gradients_from_what_they_take(moe):
+    """A caller with frozen weights keeps neither x nor h, one with a frozen input no w13: the same bits."""
+    op, (x, w13, w2, dy), y, (pre, h), (dx, dw13, dw2) = check(moe, 30, 128, 64, "bf16")
+    assert torch.equal(op.backward(dy, None, w13, w2, (pre, None), need=(True, False, False))[0], dx)
+    assert torch.equal(op.backward(dy, x, None, w2, (pre, None), need=(False, True, False))[1], dw13)
+    assert torch.equal(op.backward(dy, None, None, None, (None, h), need=(False, False, True))[2], dw2)
+    with pytest.raises(ValueError, match="w13"):
+        op.backward(dy, x, None, w2, (pre, h))
+
+
+@gpu
 @pytest.mark.parametrize("H,I", [(64, 32), (33, 31)])
 def test_no_tokens(moe, H, I):
     op = moe.MoEFeedForward(H, I, max_rows=4)
