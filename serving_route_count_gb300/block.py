@@ -86,6 +86,11 @@ def _rows(t, name, dev, rows, cols, dtype=None):
     return t.data_ptr(), step
 
 
+def _sizes(*sizes):
+    """The error of a call with a size that the library's 32-bit integers do not hold (ctypes would cut it)."""
+    raise ValueError(f"sizes {', '.join(map(str, sizes))}: each must be below 2^31")
+
+
 def _code(t, name):
     code = _CODE.get(t.dtype)
     if code is None:

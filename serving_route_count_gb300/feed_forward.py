@@ -12,12 +12,14 @@ import ctypes
 import torch
 
 from . import _lib
-from .block import _CODE, _elsewhere, _rows, _stream, _whole
+from .block import _CODE, _elsewhere, _rows, _sizes, _stream, _whole
 from . import block as _block
 from .moe import MOE_W13_UP_GATE, _check
 
 
 def moe_ff_plan(H, I, dtype, layout, limit, alpha, beta, max_rows) -> int:
+    if max(H, I, max_rows) >> 31 > 0:
+        _sizes(H, I, max_rows)
     out = ctypes.c_void_p()
     _check(_lib.load().moe_ff_plan(H, I, dtype, layout, limit, alpha, beta, max_rows, ctypes.byref(out)),
            "moe_ff_plan")
@@ -93,6 +95,8 @@ class MoEFeedForward:
         H, I, dtype = self.H, self.I, self.dtype
         xp, ldx = _rows(x, "x", dev, None, H, dtype)
         M = x.shape[0]
+        if M >> 31:
+            _sizes(M)
         w13p, ldw13 = _rows(w13, "w13", dev, 2 * I, H, dtype)
         w2p, ldw2 = _rows(w2, "w2", dev, H, I, dtype)
         pre_p = h_p = None
@@ -122,6 +126,8 @@ class MoEFeedForward:
         H, I, dtype = self.H, self.I, self.dtype
         dyp, lddy = _rows(dy, "dy", dev, None, H, dtype)
         M = dy.shape[0]
+        if M >> 31:
+            _sizes(M)
         need_x, need_w13, need_w2 = need
         inner = need_x or need_w13
         pre, h = (None, None) if saved is None else saved

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .block import _CODE, _code, _dev, _elsewhere, _rows, _stream, _whole, MOE_ACT_NONE, MOE_ACT_SWIGLU
+from .block import _CODE, _code, _dev, _elsewhere, _rows, _sizes, _stream, _whole, MOE_ACT_NONE, MOE_ACT_SWIGLU
 from . import block as _block
 from .moe import MOE_W13_UP_GATE, _check
 
@@ -53,6 +53,8 @@ def moe_fp8_quant(x, form=MOE_FP8_ROWS, q=None, scale=None, stream=None):
         if x.dim() != 2:
             raise ValueError(f"x must be [rows, K], not {list(x.shape)}")
         E, (rows, K) = 1, x.shape
+        if (rows | K) >> 31:
+            _sizes(rows, K)
         KB = _blocks(K)
         ldx, unit = x.stride()
         if unit != 1 or ldx < K:
@@ -70,6 +72,8 @@ def moe_fp8_quant(x, form=MOE_FP8_ROWS, q=None, scale=None, stream=None):
         if x.dim() not in (2, 3):
             raise ValueError(f"x must be [rows, K] or [E, rows, K], not {list(x.shape)}")
         E, rows, K = (1, *x.shape) if x.dim() == 2 else x.shape
+        if (E | rows | K) >> 31:
+            _sizes(E, rows, K)
         KB, lead = _blocks(K), x.shape[:-2]
         ldx = _stack(x if lead else x.unsqueeze(0), "x", E, rows, K)
         ldq, lds = K, KB
@@ -94,6 +98,8 @@ def moe_fp8_quant(x, form=MOE_FP8_ROWS, q=None, scale=None, stream=None):
 
 
 def moe_fp8_plan(E, N, K, dtype, act, layout, limit, alpha, beta, max_rows) -> int:
+    if max(E, N, K, max_rows) >> 31 > 0:
+        _sizes(E, N, K, max_rows)
     out = ctypes.c_void_p()
     _check(_lib.load().moe_fp8_plan(E, N, K, dtype, act, layout, limit, alpha, beta, max_rows,
                                     ctypes.byref(out)), "moe_fp8_plan")
@@ -160,6 +166,8 @@ class MoEFp8:
         rows = x.shape[0]
         xsp, ldxs = _rows(x_scale, "x_scale", dev, rows, self.blocks, torch.float32)
         S = rows if perm is None else perm.numel()
+        if (rows | S) >> 31:
+            _sizes(rows, S)
         if self.E == 1 and w.dim() == 2:
             wp, ldw = _rows(w, "w", dev, self.N, self.K, _E4M3)
         else:

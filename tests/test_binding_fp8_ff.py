@@ -126,6 +126,35 @@ def test_one_matrix(lib, w, ldw):
         product()(t((4, 144), E4M3), t((4, 2), F32), t((2, 8, 144), E4M3), t((2, 1, 2), F32), out=t((4, 8)), stream=7)
 
 
+def large(shape, dtype=BF16):
+    """A tensor with sizes alone."""
+    return torch.empty(shape, dtype=dtype, device="meta").as_subclass(On0)
+
+
+@pytest.mark.parametrize("rows", [1 << 31, (1 << 32) + 5])
+def test_rows_past_31_bits(lib, rows):
+    """The library takes 32-bit integers: more rows are refused and not cut (2^32 + 5 of them would be 5)."""
+    x, xs = large((rows, 144), E4M3), large((rows, 2), F32)
+    w, ws = t((2, 8, 144), E4M3), t((2, 1, 2), F32)
+    ff = operands()[4][1]
+    pre, h = large((rows, 16), F32), large((rows, 8))
+    for call in (lambda: fp8.moe_fp8_quant(large((rows, 1)), stream=7), lambda: fp8.moe_fp8_quant(large((rows, 1)), form=fp8.MOE_FP8_TILES, stream=7),
+                 lambda: fp8.moe_fp8_quant(large((1, rows)), stream=7), lambda: fp8.moe_fp8_quant(large((rows, 1, 1)), form=fp8.MOE_FP8_TILES, stream=7),
+                 lambda: product()(x, xs, w, ws, offsets=t(3, I32), stream=7),
+                 lambda: product()(t((4, 144), E4M3), t((4, 2), F32), w, ws, offsets=t(3, I32), perm=large(rows, I32), topk=2, stream=7),
+                 lambda: feed()(large((rows, 16)), ff["w13"], ff["w2"], stream=7), lambda: feed().forward(large((rows, 16)), ff["w13"], ff["w2"], stream=7),
+                 lambda: feed().backward(large((rows, 16)), large((rows, 16)), ff["w13"], ff["w2"], (pre, h), stream=7)):
+        with pytest.raises(ValueError, match="below 2"):
+            call()
+    for E, N, K, most in ((rows, 8, 8, 8), (1, rows, 8, 8), (1, 8, rows, 8), (1, 8, 8, rows)):
+        with pytest.raises(ValueError, match="below 2"):
+            fp8.moe_fp8_plan(E, N, K, 0, 0, 0, 1.0, 1.0, 0.0, most)
+        if E == 1:
+            with pytest.raises(ValueError, match="below 2"):
+                feed_forward.moe_ff_plan(N, K, 0, 0, 1.0, 1.0, 0.0, most)
+    assert not lib.calls
+
+
 def test_operands_that_no_gradient_takes(lib):
     """What the C call takes as NULL may be None; what a gradient needs may not."""
     _, tensors, other = operands()[4]
