@@ -1,5 +1,4 @@
-// block_launch.cuh - launch shapes of the kernels of the 16-bit block and of the 8-bit products of a few
-// positions: host arithmetic alone, without CUDA, so that it can be checked on any host.
+// block_launch.cuh - launch shapes of the kernels of the 16-bit block and of the 8-bit products: host arithmetic alone, without CUDA, so that it can be checked on any host.
 #pragma once
 
 #include <algorithm>
@@ -116,6 +115,72 @@ inline bool fp8_few_takes(int S, int E, bool offsets, bool act, int N, int K, in
   const long long ctas = (long long)f.x * f.y;
   if (f.nc == 4) return ctas <= 4LL * sms && N <= 2560;
   return ctas <= (f.nc == 1 && !act ? 17LL * sms / 2 : 4LL * sms);
+}
+
+// ---------------------------------------------------------------------------------- 8-bit products, tensor cores
+// Token-tile width, and the K steps that cutting the units which whole waves leave over has to save (none: 0; as many
+// as there are: never).
+struct F8Plan {
+  int bn, fix_steps;
+};
+
+// Over experts, whose rows are known on the device only, by the mean positions per expert (of S, dropped
+// slots among them): an expert should be one tile while HBM is the bound, and up to 64 tokens a step's
+// epilogue stays under its loads.  E = 256, K = 6144, N = 1024, SwiGLU, gathered, us at widths 32 / 64 /
+// 128 / 256: mean 16: 254 / 253 / 349 / 421;  24: 248 / 258 / 352 / 429;  32: 302 / 262 / 359 / 435;  48:
+// 395 / 270 / 368 / 443;  64: 504 / 389 / 373 / 450;  96: 690 / 496 / 387 / 460;  128: 890 / 625 / 576 / 472.
+// The crossings are of that layer, where units are many: E = 64, K = 7168, N = 2304, mean 60 takes 128 (246 us; 64:
+// 175), E = 64, K = 576, N = 7168, mean 120 takes 256 (147; 128: 106).
+inline F8Plan fp8_tc_by_rows(int S, int E) {
+  const long long e = E;
+  if (S <= 24 * e) return {32, 8};
+  if (S <= 56 * e) return {64, 12};
+  return S <= 104 * e ? F8Plan{128, 24} : F8Plan{256, 40};
+}
+
+// The least of the estimated times at widths up to `widest`, for S positions spread evenly over E experts (one
+// matrix: E = 1): a unit's K step, and joining its pieces by rows and pieces.  One matrix, K = 7168, N = 4096, us at
+// widths 32 / 64 / 128 / 256: 32 rows 18 / 19 / 22 / 34;  128: 23 / 25 / 33 / 39;  200: 39 / 26 / 33 / 40;  300: 54 /
+// 46 / 34 / 40;  1000: 119 / 87 / 62 / 43.
+inline F8Plan fp8_tc_by_time(int S, int E, int KT, int RB, int pairs, int widest) {
+  const long long touched = std::min(S, E), per = (S + touched - 1) / touched;
+  F8Plan best{widest, 0x7FFFFFFF};
+  double least = 1e300;
+  for (int bn = 32; bn <= widest; bn *= 2) {
+    const long long tiles = touched * ((per + bn - 1) / bn);
+    const double step = bn == 32 ? 320 : (bn == 64 ? 385 : (bn == 128 ? 560 : 740));     // ns
+    const long long units = tiles * RB, waves = units / pairs, left = units % pairs;
+    const double base = (double)waves * KT * step;
+    const double whole = base + (left ? KT * step : 0);
+    if (whole <= least) {
+      least = whole;
+      best = {bn, 0x7FFFFFFF};
+    }
+    if (left) {
+      const double pieces = (double)pairs / left + 1, rows = (double)((S + tiles - 1) / tiles);
+      const double cut = base + (double)left * KT / pairs * step + 4000 + rows * (100 + 6 * pieces);
+      if (cut < least) {
+        least = cut;
+        best = {bn, 0};
+      }
+    }
+    if (bn >= per) break;              // one tile holds an expert's
+  }
+  return best;
+}
+
+// One matrix goes by estimated time.  Experts go by rows, but where the units of that width leave half of the pairs or
+// more idle (few experts, a small N): there too the estimate decides, at widths up to that one, which the scratch
+// buffer is sized for.  us by rows / here, E = 4, K = 4096, N = 1024 without a SwiGLU: mean 120: 26 / 17;  60: 27 / 16;
+// E = 8, K = 7168, N = 512, mean 120: 36 / 24;  E = 4, K = 7168, N = 2304 SwiGLU, mean 120: 40 / 28.  With half of all rows at
+// one expert, which the mean does not tell, narrow tiles lose once more pairs are busy (E = 16, K = 6144, N = 1024, mean
+// 120: 41 by rows, 63 by the estimate), hence the half.
+inline F8Plan fp8_tc_plan(int S, int E, int KT, int RB, int pairs) {
+  if (E == 1) return fp8_tc_by_time(S, 1, KT, RB, pairs, 256);
+  const F8Plan p = fp8_tc_by_rows(S, E);
+  const long long touched = std::min(S, E), per = (S + touched - 1) / touched;
+  const long long units = touched * ((per + p.bn - 1) / p.bn) * RB;
+  return 2 * units <= pairs ? fp8_tc_by_time(S, E, KT, RB, pairs, p.bn) : p;
 }
 
 // ---------------------------------------------------------------------------------- norms

@@ -750,55 +750,10 @@ fp8_tc_kernel(const __grid_constant__ F8Params p) {
 
 // ---------------------------------------------------------------------------------- host side
 
-// Token-tile width, and whether the units that whole waves leave over are cut along K.
-// Over experts, whose rows are known on the device only, by the mean positions per expert (of S, dropped
-// slots among them): an expert should be one tile while HBM is the bound, and up to 64 tokens a step's
-// epilogue stays under its loads.  E = 256, K = 6144, N = 1024, SwiGLU, gathered, us at widths 32 / 64 /
-// 128 / 256: mean 16: 254 / 253 / 349 / 421;  24: 248 / 258 / 352 / 429;  32: 302 / 262 / 359 / 435;  48:
-// 395 / 270 / 368 / 443;  64: 504 / 389 / 373 / 450;  96: 690 / 496 / 387 / 460;  128: 890 / 625 / 576 / 472.
-// The kernel then cuts where that saves more K steps than joining costs.
-// Of one matrix the least of the estimated times: a unit's K step, and joining its pieces by rows and pieces.
-// K = 7168, N = 4096, us at the same widths: 32 rows 18 / 19 / 22 / 34;  128: 23 / 25 / 33 / 39;  200: 39 / 26 /
-// 33 / 40;  300: 54 / 46 / 34 / 40;  1000: 119 / 87 / 62 / 43.
-struct F8Plan {
-  int bn, fix_steps;
-};
-static F8Plan fp8_tc_plan(int S, int E, int KT, int RB, int pairs) {
-  if (E > 1) {
-    const long long e = E;
-    if (S <= 24 * e) return {32, 8};
-    if (S <= 56 * e) return {64, 12};
-    return S <= 104 * e ? F8Plan{128, 24} : F8Plan{256, 40};
-  }
-  F8Plan best{256, 0x7FFFFFFF};
-  double least = 1e300;
-  for (int bn = 32; bn <= 256; bn *= 2) {
-    const int tiles = cdiv(S, bn);
-    const double step = bn == 32 ? 320 : (bn == 64 ? 385 : (bn == 128 ? 560 : 740));     // ns
-    const long long units = (long long)tiles * RB, waves = units / pairs, left = units % pairs;
-    const double base = (double)waves * KT * step;
-    const double whole = base + (left ? KT * step : 0);
-    if (whole <= least) {
-      least = whole;
-      best = {bn, 0x7FFFFFFF};
-    }
-    if (left) {
-      const double pieces = (double)pairs / left + 1, rows = cdiv(S, tiles);
-      const double cut = base + (double)left * KT / pairs * step + 4000 + rows * (100 + 6 * pieces);
-      if (cut < least) {
-        least = cut;
-        best = {bn, 0};
-      }
-    }
-    if (bn >= S) break;                // one tile holds them all
-  }
-  return best;
-}
-
 // Scratch of cut units: [pairs][2][2 CTAs][BN][128] fp32 of the widest tile that calls of up to S positions may
 // get.
 size_t fp8_tc_part_bytes(int S, int E) {
-  const int bn = E > 1 ? fp8_tc_plan(S, E, 1, 1, 1).bn : (S <= 32 ? 32 : (S <= 64 ? 64 : (S <= 128 ? 128 : 256)));
+  const int bn = E > 1 ? fp8_tc_by_rows(S, E).bn : (S <= 32 ? 32 : (S <= 64 ? 64 : (S <= 128 ? 128 : 256)));
   return (size_t)kGtMaxPairs * 2 * 2 * bn * 128 * sizeof(float);
 }
 

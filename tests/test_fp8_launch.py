@@ -1,5 +1,5 @@
 """Which of its two kernels an 8-bit product of a few positions takes (csrc/block_launch.cuh, compiled for this host): the one that
-was measured to be faster, and launches that cover all columns and positions."""
+was measured to be faster, and launches that cover all columns and positions.  Widths of the tensor cores' tiles."""
 import ctypes
 import os
 import subprocess
@@ -11,6 +11,10 @@ SHIM = """
 #include "block_launch.cuh"
 extern "C" int takes(int S, int E, int offsets, int act, int N, int K) {
   return moe::fp8_few_takes(S, E, offsets, act, N, K, 152);
+}
+extern "C" void plan(int S, int E, int KT, int RB, int* o) {
+  const moe::F8Plan p = moe::fp8_tc_plan(S, E, KT, RB, 76), most = moe::fp8_tc_by_rows(S, E);
+  o[0] = p.bn; o[1] = p.fix_steps; o[2] = most.bn; o[3] = most.fix_steps;
 }
 extern "C" void shape(int S, int offsets, int cols, int K, int* o) {
   const moe::F8vShape f = moe::fp8_few_shape(S, offsets, cols, K, 152);
@@ -66,3 +70,39 @@ def test_every_column_and_position_has_a_cta(few, offsets):
                 nc, warps, x, y = o
                 assert nc in (1, 2, 4) and warps in (1, 2, 4, 8) and nc * y >= S > nc * (y - 1)
                 assert x * (8 // warps) >= cols > (x - 1) * (8 // warps) and y <= 8
+
+
+def tiles(few, S, E, N, K, act):
+    o = (ctypes.c_int * 4)()
+    few.plan(S, E, -(-K // 128), -(-(N // 2) // 128) if act else -(-N // 256), o)
+    return list(o)
+
+
+# E, rows of each, N, K, SwiGLU; the fastest width measured, and whether whole units were faster than cut ones
+@pytest.mark.parametrize("E,mean,N,K,act,bn,whole", [
+    (4, 120, 1024, 4096, 0, 32, 1), (4, 60, 1024, 4096, 0, 32, 1), (4, 250, 1024, 4096, 0, 64, 1), (8, 60, 1024, 4096, 0, 32, 1),
+    (8, 120, 1024, 4096, 0, 64, 1), (2, 120, 2304, 7168, 1, 32, 1), (4, 60, 2304, 7168, 1, 32, 1), (4, 120, 2304, 7168, 1, 64, 1),
+    (8, 120, 1024, 6144, 1, 64, 1), (4, 250, 1024, 6144, 1, 64, 1), (8, 120, 512, 7168, 0, 32, 1), (8, 250, 512, 7168, 0, 64, 1),
+    (16, 120, 512, 7168, 0, 64, 1), (2, 16, 4096, 2048, 0, 32, 1), (2, 100, 512, 7168, 0, 32, 0), (2, 120, 512, 7168, 0, 32, 0)])
+def test_few_experts_take_the_fastest_width(few, E, mean, N, K, act, bn, whole):
+    got = tiles(few, E * mean, E, N, K, act)
+    assert got[:2] == [bn, 0x7FFFFFFF if whole else 0]
+
+
+def test_widths_over_many_experts_go_by_rows(few):
+    for S, bn in ((64, 32), (24 * 256, 32), (24 * 256 + 1, 64), (56 * 256, 64), (56 * 256 + 1, 128), (104 * 256, 128), (104 * 256 + 1, 256)):
+        got = tiles(few, S, 256, 1024, 6144, 1)
+        assert got[0] == bn and got[:2] == got[2:]
+
+
+def test_no_width_is_wider_than_the_scratch_buffer(few):
+    """The buffer is sized by the most positions of a plan; a call of fewer gets at most the width by rows, which grows with them."""
+    for E in (2, 3, 8, 40, 1024):
+        for N, K, act in ((16, 16, 0), (1024, 4096, 0), (2304, 7168, 1)):
+            last = 0
+            for S in sorted({*range(1, 300, 7), *range(E, 300 * E, max(1, 11 * E // 2)), 1 << 30}):
+                bn, _, most, _ = tiles(few, S, E, N, K, act)
+                assert bn in (32, 64, 128, 256) and bn <= most and most >= last
+                last = most
+    for S in (1, 32, 33, 64, 65, 128, 129, 5000, 1 << 30):                        # one matrix: the tile that holds all positions
+        assert tiles(few, S, 1, 4096, 7168, 0)[0] <= max(32, 1 << (min(S, 256) - 1).bit_length())
