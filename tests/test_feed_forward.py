@@ -309,6 +309,31 @@ def test_scratch_of_a_small_plan(moe, H, I, max_rows):
 
 
 @gpu
+@pytest.mark.parametrize("H,I", [(7168, 576), (520, 1032), (100, 64)])       # 100: the first product's rows are off 16 bytes
+def test_weights_written_just_before_the_call(moe, H, I):
+    """The second product of one or two tokens may load its weights while the first one runs, and not before what wrote them
+    is over: weights that change between calls, in the stream and in a graph."""
+    op = moe.MoEFeedForward(H, I, max_rows=2)
+    for M in (1, 2):
+        x, w13, w2, _ = operands(M, H, I, "bf16", M)
+        sets = [(w13, w2), (w13.flip(0).contiguous(), w2.flip(0).contiguous()), (-w13, 2 * w2)]
+        want = [op(x, *s).clone() for s in sets]
+        a, b = torch.empty_like(w13), torch.empty_like(w2)
+        step = lambda s: (a.copy_(s[0]), b.copy_(s[1]), op(x, a, b))[2]  # noqa: E731
+        got = [step(sets[i % 3]) for i in range(60)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = [step(s) for s in sets]
+        for _ in range(5):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert op.device_error() == (0, 0)
+
+
+@gpu
 @pytest.mark.parametrize("M,H,I", [(40, 4096, 256), (600, 1024, 4096)])
 def test_a_wait_that_runs_out(moe, M, H, I):
     """The first CTA pair's MMA issuer gives up a wait of 2 ms in every product: both passes end with MOE_ERR_TIMEOUT in the error
