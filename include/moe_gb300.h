@@ -523,6 +523,7 @@ typedef enum { MOE_FP8_ROWS = 0, MOE_FP8_TILES = 1 } moe_fp8_form;
  *   MOE_FP8_ROWS (E = 1): x [rows, K], scale [rows, KB], KB = ceil(K / 128).
  *   MOE_FP8_TILES: E matrices x [E, rows, K] with evenly spaced rows, ldx apart over all of them, q
  *   likewise; scale [E, ceil(rows / 128), KB], rows of scales lds apart over all matrices.
+ *   q and scale must not overlap x or one another.
  *   dtype of x: MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32.  Row strides ldx, ldq, lds in elements.
  * E == 0 or rows == 0 is a no-op.  Limits: K <= 2^24, E * rows < 2^31, fewer than 2^31 tiles.
  * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (type), MOE_ERR_CUDA. */
@@ -534,6 +535,8 @@ moe_status moe_fp8_quant(const void* x, int dtype, long long ldx, int E, int row
  * with groups, row(p), act and the rows past the last group as for moe_grouped_run; without offsets
  * (E = 1) all S positions are the one matrix's.  t(n) = n / 128; with MOE_ACT_SWIGLU each half of N / 2
  * rows has tiles of its own: half h's row i is in tile row h * ceil(N / 2 / 128) + i / 128.
+ * The two scales of a block are multiplied first, in fp32: a product below 2^-126 loses places, or the whole
+ * block below 2^-149, and one past fp32's range is infinite (NaN where the block's sum is 0).
  * The plan's arguments, limits and errors are moe_grouped_plan's; dtype is the type of out. */
 typedef struct moe_fp8_s moe_fp8_t;
 moe_status moe_fp8_plan(int E, int N, int K, int dtype, int act, int layout, float limit, float alpha,

@@ -12,11 +12,12 @@
 // form, and the instruction descriptor says so.
 //
 // Bounds and measurements (GB300, bf16, measured 1910 TFLOP/s in a burst, 1726 sustained): 2048 tokens of 7168 ->
-// 4608 -> 7168, us of each product alone and TFLOP/s (floor 142 for the two-halves ones, 71 for the others): up
-// projections with the saved sums 158 / 1712; down 76 / 1780; dh with the activation's gradient 106 / 1276; dx
-// 148 / 1828; dW13 161 / 1681; dW2 86 / 1573: bound by the tensor cores (pipe 80 to 85 % active; dW 67 to 72, dh
-// 54, whose epilogue reads two fp32 sums for every value).  The whole step of 4096 tokens 1520 us (1602 TFLOP/s,
-// 93 % of sustained).  777 tokens of 6144 -> 512 -> 6144: 91 us with the weights in L2, 118 from HBM, floor 23:
+// 4608 -> 7168, us of each product and TFLOP/s under the counters, one kernel at a time at 1.45 to 1.55 GHz (floor 142
+// for the two-halves ones, 71 for the others): up projections with the saved sums 168 / 1610; down 82 / 1650; dh with
+// the activation's gradient 104 / 1300; dx 155 / 1740; dW13 167 / 1625; dW2 88 / 1540: bound by the tensor cores (pipe 78
+// to 83 % active; dW 67 to 70, dh 58, whose epilogue reads two fp32 sums for every value).  The whole step of 4096 tokens
+// 1520 to 1640 us from box to box (1.48 to 1.60 PFLOP/s, 86 to 93 % of sustained).  777 tokens of 6144 -> 512 -> 6144: 91
+// us with the weights in L2, 111 to 118 from HBM, floor 23:
 // sixteen to fifty units for 76 pairs, and a unit's 96 steps take 23 us.
 //
 // Roles: warp 0 tile copies, warp 1 MMA issue (leader CTA), warp 2 tensor memory, warps 4-11 epilogue.

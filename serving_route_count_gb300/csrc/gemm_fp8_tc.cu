@@ -15,14 +15,15 @@
 //     a SwiGLU), so a step costs it one factor and 64 packed FMAs; with the scales read from shared
 //     memory, as above, those reads and the MMA's operands would share its bandwidth at par.
 // The sums of an epilogue thread (up to 128) and what it has in flight need 184 or 208 registers: the other
-// warps give theirs up (setmaxnreg).
+// warps give theirs up (setmaxnreg).  The compiler, which shares out 128 for all roles, spills a few words of the widths
+// 128 and 256 (4 to 32 bytes stored, 12 to 36 loaded); whether inside a step is not known.
 //
 // Bounds and measurements (GB300, HBM at the measured 6784 GB/s, e4m3 at twice the measured bf16 rate):
-//   up projections + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 67 us, HBM floor 53; down projections
-//   of 16 tokens top-6, E = 384, K = 576, N = 7168: 83 us, floor 52 - the start (tables 2 us, first loads 2.5),
+//   up projections + SwiGLU of 8 tokens top-8, E = 256, K = 6144, N = 1024: 63 to 70 us, HBM floor 53; down projections
+//   of 16 tokens top-6, E = 384, K = 576, N = 7168: 81 to 88 us, floor 52 - the start (tables 2 us, first loads 2.5),
 //   units of five steps, their stores (76 us without) and 128-byte copies of 576-byte rows;
-//   2048 tokens top-8, skewed: 392 us, floor 241: bound by the epilogue's handling of a step at 128 tokens (272
-//   with the MMAs and copies alone);
+//   2048 tokens top-8, skewed: 395 us, floor 241: bound by the epilogue's handling of a step at 128 tokens (272
+//   with the MMAs and copies alone), which takes the tile's whole width however few rows it holds;
 //   8192 x 7168 x 7168: 453 us, 1.86 PFLOP/s (floor 220; 277 with the MMAs and copies alone, 342 with the loads
 //   from tensor memory, the rest the FMAs that do not hide under them).
 // What cost most on the way, us of up decode / dense prefill: an arrival with cluster-scope release after the

@@ -7,7 +7,9 @@
 // over the lanes, then over the warps: one order.  Units on the tensor cores are cut into pieces for this,
 // which are joined: us of a forward pass here / there, weights in L2: 6144 -> 512 one token 7.3 / 20.0, two
 // 9.3 / 17.8, four (were they taken) 16.4 / 17.8;  7168 -> 1152 11.9 / 21.2, 16.6 / 21.3, 31.7 / 21.3;  4096 -> 4096
-// 21.5 / 28.5, 27.0 / 29.5, 50.5 / 28.8.  From HBM one token of 7168 -> 1152 takes 15.2 us (weights 7.3).
+// 21.5 / 28.5, 27.0 / 29.5, 50.5 / 28.8.  From HBM, one / two tokens: 7168 -> 1152 14.5 / 23.9, 19.4 / 23.9 (weights 7.3);
+// 512 -> 512 3.8 / 9.9, 4.2 / 9.8;  7168 -> 4608 39.6 / 53.4, 49.5 / 51.4;  16384 -> 2048 40.3 / 48.4, 48.2 / 48.6; only the
+// largest lose, 8192 -> 16384 142 / 135, 161 / 136.
 #include "feed_forward.cuh"
 #include "../../include/moe_gb300.h"
 
